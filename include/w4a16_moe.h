@@ -543,6 +543,113 @@ w4a16_status w4a16_mxfp4_gate_up_silu(const w4a16_weight_desc* desc, const void*
                                       const w4a16_indexed_routing* routing, uint8_t* out_codes,
                                       uint8_t* out_scales, const w4a16_config* cfg, w4a16_stream_t stream);
 
+/* Quantise and pack an MXFP4 weight in one pass: w [E, N, K] row-major, of
+ * w_dtype W4A16_DTYPE_F32 or W4A16_DTYPE_BF16, through the conversion of
+ * w4a16_mxfp4_quant (fp32 values are rounded once, from all their bits) into
+ * the packed layout of desc (gate/up interleaved where its flags say so).
+ * The packed buffers hold the same bytes as quantising the rows and packing
+ * the codes.  w must be finite.  Pointers 16-byte aligned.
+ * Errors: ERR_ARG, ERR_LAYOUT (not an MXFP4 weight), ERR_UNSUPPORTED
+ * (w_dtype), ERR_HIP. */
+w4a16_status w4a16_mxfp4_quant_pack(const void* w, int32_t w_dtype, const w4a16_weight_desc* desc, void* packed_w,
+                                    void* packed_s, w4a16_stream_t stream);
+
+/* The values a packed MXFP4 weight stands for, in the logical row order:
+ * out [E, N, K] bf16, exact (code 255 of a scale gives NaN, a product past
+ * the largest bf16 infinity).  Pointers 16-byte aligned.
+ * Errors: ERR_ARG, ERR_LAYOUT, ERR_HIP. */
+w4a16_status w4a16_mxfp4_dequant(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                 uint16_t* out, w4a16_stream_t stream);
+
+/* The grouped layouts on MXFP4 rows (a_codes [rows, K/2], a_scales
+ * [rows, K/32], as w4a16_mxfp4_quant writes them) and an MXFP4 weight:
+ * layouts, written and unwritten rows as w4a16_grouped_contiguous and
+ * w4a16_grouped_masked; products exact, fp32 accumulation, one rounding to
+ * bf16.  A gate/up-interleaved weight gives its columns in logical order.
+ * The calls choose their own tiles and need no workspace.
+ * Contiguous: rows = m_rows, a multiple of 128; a row's m_indices entry
+ * outside [0, E) marks padding, and a segment's valid rows come first.
+ * Masked: rows = E * max_m; a count masked_m[g] outside [0, max_m] is taken
+ * as the nearer end; expected_m (host, > 0) only steers the tile choice.
+ * Sizes: rows * K / 2 below 4 GiB (ERR_SHAPE).
+ * Pointers: packed_w, packed_s, a_codes, out 16-byte aligned.
+ * Errors: ERR_ARG, ERR_LAYOUT (not an MXFP4 weight), ERR_SHAPE, ERR_HIP. */
+w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                            const uint8_t* a_codes, const uint8_t* a_scales, int64_t m_rows,
+                                            const int32_t* m_indices, uint16_t* out, w4a16_stream_t stream);
+w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                        const uint8_t* a_codes, const uint8_t* a_scales, int32_t max_m,
+                                        const int32_t* masked_m, int32_t expected_m, uint16_t* out,
+                                        w4a16_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Router: gate logits -> topk_ids and topk_weights (what w4a16_moe_align,
+ * the combine and w4a16_moe_few_tokens take).
+ * ---------------------------------------------------------------------- */
+
+#define W4A16_DTYPE_F32 0
+#define W4A16_DTYPE_BF16 1
+#define W4A16_DTYPE_F16 2
+#define W4A16_SCORE_SOFTMAX 0
+#define W4A16_SCORE_SIGMOID 1
+#define W4A16_ROUTE_MAX_TOPK 32
+#define W4A16_ROUTE_MAX_EXPERTS 1024
+
+/* logits: T rows of E values of dtype W4A16_DTYPE_*, row_stride elements
+ * apart (>= E).  Per row, the topk experts in falling order, the lower expert
+ * first where two are equal:
+ *   W4A16_SCORE_SOFTMAX: by logit; weight exp(l_e - max) / sum over all live
+ *     experts, or over the chosen ones with renormalize;
+ *   W4A16_SCORE_SIGMOID: by s_e + bias[e] (in 64-bit arithmetic), or by logit
+ *     when bias (float [E]) is NULL; weight s_e = 1 / (1 + exp(-l_e)), with
+ *     renormalize divided by (sum of the chosen s + 1e-20).
+ * Every weight is multiplied by scale (finite).  An expert whose logit or
+ * bias is -inf or NaN is masked; +inf counts as the largest finite value.
+ * Slots left without an expert get topk_ids -1 and topk_weights 0, which
+ * w4a16_moe_align (validate = 0), the combine and w4a16_moe_few_tokens skip
+ * like any expert held elsewhere.
+ * topk_ids: int32 [T, topk]; topk_weights: float [T, topk].
+ * Sizes: topk <= min(E, W4A16_ROUTE_MAX_TOPK), E <= W4A16_ROUTE_MAX_EXPERTS.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_UNSUPPORTED (dtype, scoring, or a bias with
+ * softmax), ERR_HIP. */
+w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride,
+                             const float* bias, int32_t topk, int32_t scoring, int32_t renormalize, float scale,
+                             int32_t* topk_ids, float* topk_weights, w4a16_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A whole MoE layer for a few tokens: gate/up, SiLU * up, down and the
+ * weighted sum over a token's experts, in two kernels and without routing
+ * buffers.
+ * ---------------------------------------------------------------------- */
+
+#define W4A16_FEW_MAX_TOKENS 64
+#define W4A16_FEW_MAX_SLOTS 1024   /* T * topk */
+
+/* x bf16 [T, H] -> out bf16 [T, H],
+ *   out[t] = sum over j with first_expert <= topk_ids[t][j] < first_expert + E
+ *            of topk_weights[t][j] * down_e . bf16(silu(gate_e . x_t) * (up_e . x_t))
+ * with fp32 sums and one rounding at the end; tokens without a local expert
+ * get 0.  The weights are both INT4 (values bf16_rne((q - 8) s)) or both
+ * MXFP4, activations stay bf16 in either case: gate_up [E, 2 I, H] packed
+ * with W4A16_DESC_GATE_UP, down [E, H, I].  Ids outside the local range
+ * (-1 among them) are skipped; an expert a token lists twice counts with the
+ * sum of its weights.  T = 0 does nothing.
+ * workspace: w4a16_moe_few_tokens_workspace_bytes(gate_up, T, topk) bytes,
+ * not initialised; its contents are the call's own until it has finished.
+ * out must not overlap any input.
+ * Sizes: T <= W4A16_FEW_MAX_TOKENS, T * topk <= W4A16_FEW_MAX_SLOTS
+ * (ERR_SHAPE; larger batches take w4a16_moe_align and the GEMM calls).
+ * Pointers 16-byte aligned (topk_ids, topk_weights: 4).
+ * Errors: ERR_ARG, ERR_LAYOUT (packing), ERR_SHAPE, ERR_WORKSPACE, ERR_HIP. */
+w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* gate_up_w, const void* gate_up_s,
+                                  const w4a16_weight_desc* down, const void* down_w, const void* down_s,
+                                  const uint16_t* x, int32_t T, int32_t topk, const int32_t* topk_ids,
+                                  const float* topk_weights, int32_t first_expert, uint16_t* out, void* workspace,
+                                  size_t workspace_bytes, w4a16_stream_t stream);
+
+/* Workspace bytes of w4a16_moe_few_tokens; 0 on bad arguments. */
+size_t w4a16_moe_few_tokens_workspace_bytes(const w4a16_weight_desc* gate_up, int32_t T, int32_t topk);
+
 #ifdef __cplusplus
 }
 #endif

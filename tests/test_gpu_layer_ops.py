@@ -1,0 +1,551 @@
+"""GPU parity of the router, the few-token layer, the MXFP4 weight quantiser
+and the grouped MXFP4 products against the float64 oracle."""
+import os
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+from gpu_util import bits, dev, log, to_dev, to_dev_bf16  # noqa: E402
+
+from oracle import layer_oracle as LO  # noqa: E402
+from oracle import moe_oracle as O  # noqa: E402
+from oracle import mx_oracle as X  # noqa: E402
+from synth import workloads as W  # noqa: E402
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="no GPU visible")]
+
+import w4a16_int4_mixture_moe_amd as M  # noqa: E402
+
+
+# ------------------------------------------------------------------ router
+
+def _check_route(logits: torch.Tensor, k, scoring, bias=None, renorm=True, scale=1.0, what=""):
+    ids, w = M.moe_route(logits, k, scoring=scoring, bias=bias, renormalize=renorm, scale=scale)
+    ref_ids, ref_w, tol = LO.route(logits.double().cpu().numpy(), k, scoring,
+                                   None if bias is None else bias.double().cpu().numpy(), renorm, scale)
+    np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids, err_msg=what)
+    err = np.abs(w.double().cpu().numpy() - ref_w)
+    assert (err <= tol).all(), (what, float((err / np.maximum(tol, 1e-300)).max()))
+    return ids, w
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 5), (5, 63, 2), (4, 64, 32), (7, 65, 8), (257, 384, 8),
+                                   (33, 448, 9), (9, 768, 6), (66, 896, 16), (6, 1024, 32)])
+def test_route_shapes(T, E, k, dtype):
+    g = torch.Generator().manual_seed(T * 131 + E)
+    l = torch.randn(T, E, generator=g).to(dtype).to(dev())
+    b = (0.1 * torch.randn(E, generator=g)).to(dev())
+    for renorm in (True, False):
+        _check_route(l, k, "softmax", None, renorm, 1.0, "softmax")
+        _check_route(l, k, "sigmoid", None, renorm, 2.5, "sigmoid")
+        _check_route(l, k, "sigmoid", b, renorm, 2.5, "sigmoid + bias")
+
+
+@pytest.mark.parametrize("scoring,biased", [("softmax", False), ("sigmoid", False), ("sigmoid", True)])
+def test_route_masks_infinities_and_ties(scoring, biased):
+    n, inf, big = float("nan"), float("inf"), 3e38
+    E, k = 70, 4
+    rows = torch.zeros(9, E)
+    rows[0] = -inf                                        # nothing left
+    rows[1] = n
+    rows[2] = -inf
+    rows[2, 69] = -3.0                                    # fewer than k
+    rows[2, 1] = 1.0
+    rows[3, 5] = inf
+    rows[3, 66] = inf                                     # two infinities share
+    rows[3, 7] = n
+    rows[4] = -0.0
+    rows[4, 3] = 0.0                                      # equal to -0
+    rows[5] = -200.0                                      # scores below fp32's range
+    rows[6, ::2] = -big
+    rows[7, 68] = big
+    rows[8] = torch.arange(E) % 3                         # many ties
+    b = torch.zeros(E) if biased else None
+    if biased:
+        b[0], b[1], b[2], b[9] = -inf, n, inf, 2.0
+    l = rows.to(dev())
+    b = None if b is None else b.to(dev())
+    for renorm in (True, False):
+        _check_route(l, k, scoring, b, renorm, 1.0, f"{scoring} {renorm}")
+
+
+def test_route_orders_near_ties_in_64_bits():
+    """Biases that bring every sum to about one half: 32-bit keys cannot order them."""
+    g = torch.Generator().manual_seed(11)
+    E = 384
+    l = torch.randn(40, E, generator=g)
+    l[20:] = l[0]
+    l[20:30] += 1e-6 * torch.randn(10, E, generator=g)
+    b = (0.5 - torch.sigmoid(l[0].double())).float()
+    _check_route(l.to(dev()), 8, "sigmoid", b.to(dev()), True, 1.0, "near ties")
+    _check_route(torch.zeros(5, E, device=dev()), 8, "sigmoid", torch.zeros(E, device=dev()), True, 1.0, "all equal")
+    huge = torch.linspace(1e4, 1e4 + 0.4, E).to(dev())    # the bias swallows the score's low bits in 32 bits
+    _check_route(l.to(dev()), 8, "sigmoid", huge, True, 1.0, "large bias")
+
+
+def test_route_strided_rows_other_stream_and_refusals():
+    wide = torch.randn(50, 512, device=dev())
+    _check_route(wide[::2, 64:64 + 96], 5, "softmax", what="strided")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ids, w = M.moe_route(wide, 4)
+    s.synchronize()
+    ref = M.moe_route(wide, 4)
+    assert torch.equal(ids, ref[0]) and torch.equal(w, ref[1])
+    e = M.moe_route(wide[:0], 4)
+    assert e[0].shape == (0, 4) and e[1].shape == (0, 4)
+    with pytest.raises(ValueError):
+        M.moe_route(wide.t(), 4)
+    with pytest.raises(ValueError):
+        M.moe_route(wide, 4, scoring="max")
+    with pytest.raises(TypeError):
+        M.moe_route(wide.double(), 4)
+    with pytest.raises(ValueError):
+        M.moe_route(wide, 4, scoring="sigmoid", bias=torch.zeros(4, device=dev()))
+    with pytest.raises(M.W4A16Error):
+        M.moe_route(wide, 33)
+
+
+# ------------------------------------------------------------------ few-token layer
+
+class Layer:
+    """Seeded weights of one layer share, on the device and as float64."""
+
+    def __init__(self, kind, E, H, I, seed=0):
+        rng = np.random.default_rng(seed)
+        self.kind, self.E, self.H, self.I = kind, E, H, I
+        if kind == "int4":
+            c1, c2 = (rng.integers(0, 16, s, dtype=np.uint8) for s in ((E, 2 * I, H), (E, H, I)))
+            s1, s2 = (W.to_bf16_bits(rng.uniform(0.005, 0.02, s).astype(np.float32))
+                      for s in ((E, 2 * I, H // 32), (E, H, I // 32)))
+            self.p1 = M.pack_w4(to_dev(c1), to_dev_bf16(s1), gate_up=True)
+            self.p2 = M.pack_w4(to_dev(c2), to_dev_bf16(s2))
+            self.w1, self.w2 = O.dequant(c1, s1), O.dequant(c2, s2)
+        else:
+            c1, c2 = (rng.integers(0, 256, s, dtype=np.uint8) for s in ((E, 2 * I, H // 2), (E, H, I // 2)))
+            s1, s2 = (rng.integers(119, 123, s, dtype=np.uint8) for s in ((E, 2 * I, H // 32), (E, H, I // 32)))
+            self.p1 = M.pack_mxfp4(to_dev(c1), to_dev(s1), gate_up=True)
+            self.p2 = M.pack_mxfp4(to_dev(c2), to_dev(s2))
+            self.w1 = X.mx_dequant(X.unpack_nibbles(c1), s1)
+            self.w2 = X.mx_dequant(X.unpack_nibbles(c2), s2)
+
+    def check(self, x_bits, ids, wt, first, what):
+        T, k = ids.shape
+        n = M.few_tokens_workspace_bytes(self.p1, T, k)
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=dev())     # not initialised: any contents do
+        out = torch.full((T + 1, self.H), 7.0, dtype=torch.bfloat16, device=dev())
+        M.moe_few_tokens(to_dev_bf16(x_bits), self.p1, self.p2, to_dev(ids), to_dev(wt), first, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        assert (out[T] == 7.0).all(), f"{what}: wrote behind the last token"
+        ref, tol = LO.few_tokens(x_bits, self.w1, self.w2, ids, wt, first)
+        share = LO.assert_within(bits(out[:T]), ref, tol, what)
+        log(f"few {self.kind} {what}: {share:.2f} of the bound")
+        return bits(out[:T])
+
+
+def _tokens(T, k, E_glob, H, seed):
+    rng = np.random.default_rng(seed)
+    x = W.to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))
+    ids = np.stack([rng.permutation(E_glob)[:k] for _ in range(T)]).astype(np.int32) if T else np.zeros((0, k), np.int32)
+    wt = rng.uniform(0.05, 1.0, (T, k)).astype(np.float32)
+    return x, ids, wt
+
+
+@pytest.fixture(scope="module")
+def layers():
+    return {"int4": Layer("int4", 6, 288, 160), "mxfp4": Layer("mxfp4", 6, 384, 128),
+            "int4_wide": Layer("int4", 3, 1280, 640, 1)}
+
+
+@pytest.mark.parametrize("kind", ["int4", "mxfp4"])
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 6), (2, 3), (7, 4), (16, 2), (17, 3), (32, 6), (33, 2), (64, 4), (64, 16)])
+def test_few_tokens_shapes(layers, kind, T, k):
+    lay = layers[kind]
+    x, ids, wt = _tokens(T, k, 20, lay.H, T * 17 + k)      # experts 3..8 of 20 are held here
+    lay.check(x, ids, wt, 3, f"T={T} k={k}")
+
+
+@pytest.mark.parametrize("kind", ["int4", "mxfp4"])
+def test_few_tokens_routing_corners(layers, kind):
+    lay = layers[kind]
+    x, ids, wt = _tokens(40, 3, 6, lay.H, 5)
+    hot = ids.copy()
+    hot[:, 0] = 2                                          # one expert holds every token: blocks of 16, 16, 8
+    hot[:, 1] = np.where(ids[:, 1] == 2, 0, ids[:, 1])
+    lay.check(x, hot, wt, 0, "hot expert")
+    twice = ids.copy()
+    twice[::3, 2] = twice[::3, 0]                          # a token names an expert twice
+    twice[4] = 5
+    lay.check(x, twice, wt, 0, "twice")
+    away = ids.copy()
+    away[::2] = -1                                         # rows without any expert
+    away[1, 1] = 99
+    away[3] = np.iinfo(np.int32).min
+    y = lay.check(x, away, wt, 0, "held elsewhere")
+    assert not y[::2].any()
+    lay.check(x, np.full_like(ids, 9), wt, 0, "none held")
+    wt[:, 1] = 0.0
+    wt[5] = -wt[5]
+    lay.check(x, ids, wt, 0, "zero and negative weights")
+
+
+def test_few_tokens_wide_layer_and_nan_rows(layers):
+    lay = layers["int4_wide"]
+    x, ids, wt = _tokens(20, 2, 3, lay.H, 8)
+    y = lay.check(x, ids, wt, 0, "wide")
+    x2 = x.copy()
+    x2[3] = 0x7FC0                                         # one token's NaN stays with it
+    x2[17, 0] = 0x7F80
+    out = M.moe_few_tokens(to_dev_bf16(x2), lay.p1, lay.p2, to_dev(ids), to_dev(wt))
+    got = bits(out)
+    keep = [t for t in range(20) if t not in (3, 17)]
+    np.testing.assert_array_equal(got[keep], y[keep])
+    assert torch.isnan(out[3].float()).all()
+
+
+def test_few_tokens_empty_and_refusals(layers):
+    lay = layers["int4"]
+    x, ids, wt = _tokens(4, 2, 6, lay.H, 1)
+    dx, di, dw = to_dev_bf16(x), to_dev(ids), to_dev(wt)
+    assert M.moe_few_tokens(dx[:0], lay.p1, lay.p2, di[:0], dw[:0]).shape == (0, lay.H)
+    with pytest.raises(ValueError):
+        M.moe_few_tokens(dx, lay.p1, lay.p2, di[:3], dw)
+    with pytest.raises(ValueError):
+        M.moe_few_tokens(dx[:, :256].contiguous(), lay.p1, lay.p2, di, dw)
+    with pytest.raises(ValueError):
+        M.moe_few_tokens(dx.t().contiguous().t(), lay.p1, lay.p2, di, dw)
+    with pytest.raises(TypeError):
+        M.moe_few_tokens(dx, lay.p1, lay.p2, di.long(), dw)
+    with pytest.raises(M.W4A16Error):
+        M.moe_few_tokens(dx, lay.p2, lay.p1, di, dw) if lay.p2.K == lay.H else M.moe_few_tokens(
+            dx, lay.p1, lay.p1, di, dw)
+    with pytest.raises(M.W4A16Error):
+        M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, workspace=torch.empty(64, dtype=torch.uint8, device=dev()))
+
+
+def test_few_tokens_agrees_with_the_routed_path(layers):
+    """align + fused gate/up + down on the same inputs: the same h up to its
+    extra bf16 roundings of gate and up, the same sums."""
+    lay = layers["int4_wide"]
+    x, ids, wt = _tokens(24, 2, 3, lay.H, 21)
+    dx, di, dw = to_dev_bf16(x), to_dev(ids), to_dev(wt)
+    y = M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw).float()
+    r = M.moe_align(di, 3, 0, 3, 16)
+    z = M.moe_w4a16_gemm(M.moe_gate_up_silu(dx, lay.p1, r), lay.p2, r, dw, a_layout="sorted").float()
+    # gate, up and their product rounded to bf16: three half steps an h instead of one, independent,
+    # against sums whose root mean square is that of the outputs
+    rms = y.pow(2).mean().sqrt()
+    assert ((y - z).abs() <= 7 * 4 * 2.0 ** -8 * rms + 2.0 ** -7 * y.abs()).all()
+
+
+# ------------------------------------------------------------------ chain, graph, streams
+
+def test_route_then_layer_captured_and_replayed(layers):
+    """Router and layer in one HIP graph on new inputs each replay, eager work
+    between, against the eager calls; two graphs alive at once."""
+    for kind in ("int4", "mxfp4"):
+        lay = layers[kind]
+        T, k = 18, 3
+        x = torch.empty(T, lay.H, dtype=torch.bfloat16, device=dev())
+        l = torch.empty(T, lay.E, device=dev())
+
+        def step():
+            ids, w = M.moe_route(l, k, scoring="sigmoid")
+            return M.moe_few_tokens(x, lay.p1, lay.p2, ids, w)
+
+        x.normal_()
+        l.normal_()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graphs = []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                y = step()
+            graphs.append((g, y))
+        for rep in range(4):
+            x.normal_()
+            l.normal_()
+            l[rep] = float("-inf")                          # a padded token: no expert
+            torch.cuda.synchronize()
+            for g, y in graphs:
+                g.replay()
+            torch.cuda.synchronize()
+            ref = step()
+            for g, y in graphs:
+                assert torch.equal(y, ref), (kind, rep)
+            assert not ref[rep].any()
+            _ = (x.float() @ x.float().t()).sum().item()
+
+
+def test_few_tokens_on_two_streams_at_once(layers):
+    lay = layers["int4_wide"]
+    x, ids, wt = _tokens(30, 2, 3, lay.H, 77)
+    dx, di, dw = to_dev_bf16(x), to_dev(ids), to_dev(wt)
+    ref = M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(5):
+        for s, o in zip(streams, outs):
+            with torch.cuda.stream(s):
+                o.append(M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw))
+    torch.cuda.synchronize()
+    for o in outs:
+        for y in o:
+            assert torch.equal(y, ref)
+
+
+# ------------------------------------------------------------------ MXFP4 weights
+
+def _special(N, K, rng):
+    v = rng.standard_normal((N, K)) * np.repeat(2.0 ** rng.integers(-20, 20, (N, K // 32)), 32, axis=1)
+    v[0, :32] = 0.0
+    v[1, :32] = -0.0
+    v[2, :12] = [6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -2.5, 5.01, 0.24]     # every tie, at scale 1
+    v[2, 12:32] = 0.0
+    v[3, :32] = 2.0 ** -130
+    v[4, :4] = [7.5, -7.9, 7.0, 0.1]
+    v[5, :2] = [2.0 ** 127, -(2.0 ** 126)]
+    return v
+
+
+@pytest.mark.parametrize("gate_up", [False, True])
+@pytest.mark.parametrize("E,N,K", [(1, 64, 128), (3, 192, 384), (2, 64, 1280)])
+def test_quant_pack_bf16_equals_quantise_then_pack(E, N, K, gate_up):
+    rng = np.random.default_rng(N + K)
+    w = W.to_bf16_bits(np.stack([_special(N, K, rng) for _ in range(E)]).astype(np.float32))
+    d = to_dev_bf16(w)
+    p = M.quant_pack_mxfp4(d, gate_up=gate_up)
+    q = M.mxfp4_quant(d.view(E * N, K))
+    ref = M.pack_mxfp4(q.codes.view(E, N, K // 2), q.scales.view(E, N, K // 32), gate_up=gate_up)
+    assert torch.equal(p.w, ref.w) and torch.equal(p.s, ref.s)
+    oc, os_ = X.mx_quantize(w.reshape(E * N, K))
+    val = X.mx_dequant(oc, os_).reshape(E, N, K)
+    got = O.bf16_to_f64(bits(M.dequant_mxfp4(p)))
+    np.testing.assert_array_equal(got, val)
+    assert (np.signbit(got) == np.signbit(val)).all()
+
+
+def test_quant_pack_fp32_rounds_once():
+    rng = np.random.default_rng(4)
+    E, N, K = 2, 96, 256
+    v = np.stack([_special(N, K, rng) for _ in range(E)]).astype(np.float32)
+    # just beside ties that a bf16 copy would land on
+    v[0, 6, :32] = np.float32(2.5) * np.where(np.arange(32) % 2, 1 + 2.0 ** -20, 1 - 2.0 ** -20)
+    v[0, 6, 0] = 6.0
+    v[0, 7, :32] = np.float32(1.0)
+    v[0, 7, 0] = np.nextafter(np.float32(8.0), np.float32(0))        # the exponent from all 24 bits
+    got = O.bf16_to_f64(bits(M.dequant_mxfp4(M.quant_pack_mxfp4(to_dev(v)))))
+    f = v.astype(np.float64).reshape(E, N, K // 32, 32)
+    amax = np.abs(f).max(-1)
+    code = np.where(amax > 0, np.clip(np.frexp(amax)[1].astype(np.int64) - 3, -127, 127) + 127, 0)
+    y = f / X.e8m0_to_f64(code)[..., None]
+    ref = X.e2m1_to_f64(X.f64_to_e2m1(y, np.signbit(f))) * X.e8m0_to_f64(code)[..., None]
+    np.testing.assert_array_equal(got, ref.reshape(E, N, K))
+
+
+def test_dequant_covers_every_scale_code():
+    codes = np.tile(np.arange(256, dtype=np.uint8), (1, 16, 256 * 16 // 256))[:, :, :256 * 16]     # K = 8192
+    scales = np.tile(np.arange(256, dtype=np.uint8), (1, 16, 1))
+    got = M.dequant_mxfp4(M.pack_mxfp4(to_dev(codes), to_dev(scales))).float().cpu().numpy()
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref = X.mx_dequant(X.unpack_nibbles(codes), scales)
+        ref = np.where(np.abs(ref) >= 2.0 ** 128, np.sign(ref) * np.inf, ref)
+    np.testing.assert_array_equal(got.astype(np.float64)[..., :255 * 32], ref[..., :255 * 32])
+    assert np.isnan(got[..., 255 * 32:]).all()
+
+
+def test_quant_pack_refusals():
+    with pytest.raises(TypeError):
+        M.quant_pack_mxfp4(torch.zeros(1, 16, 128, dtype=torch.float16, device=dev()))
+    with pytest.raises(ValueError):
+        M.quant_pack_mxfp4(torch.zeros(16, 128, device=dev()))
+    with pytest.raises(ValueError):
+        M.quant_pack_mxfp4(torch.zeros(1, 128, 16, device=dev()).transpose(1, 2))
+    with pytest.raises(M.W4A16Error):
+        M.quant_pack_mxfp4(torch.zeros(1, 16, 96, device=dev()))         # K % 128
+    with pytest.raises(ValueError):
+        M.dequant_mxfp4(M.pack_w4(torch.zeros(1, 16, 128, dtype=torch.uint8, device=dev()),
+                                  torch.zeros(1, 16, 4, dtype=torch.bfloat16, device=dev())))
+
+
+# ------------------------------------------------------------------ grouped MXFP4
+
+def _mx_weight(E, N, K, seed, gate_up=False):
+    rng = np.random.default_rng(seed)
+    c = rng.integers(0, 256, (E, N, K // 2), dtype=np.uint8)
+    s = rng.integers(119, 124, (E, N, K // 32), dtype=np.uint8)
+    return M.pack_mxfp4(to_dev(c), to_dev(s), gate_up=gate_up), X.mx_dequant(X.unpack_nibbles(c), s)
+
+
+def _mx_rows(m, K, seed):
+    rng = np.random.default_rng(seed)
+    c = rng.integers(0, 256, (m, K // 2), dtype=np.uint8)
+    s = rng.integers(124, 129, (m, K // 32), dtype=np.uint8)
+    return c, s, X.mx_dequant(X.unpack_nibbles(c), s)
+
+
+def _grouped_check(got, rows, experts, a, w, what):
+    """Rows of `rows` against a . w[expert]; every other row still holds the sentinel."""
+    touched = np.zeros(len(got), bool)
+    worst = 0.0
+    for e in sorted(set(experts)):
+        r = np.array([i for i, x in zip(rows, experts) if x == e])
+        touched[r] = True
+        ref, tol = LO.product(a[r], w[e])
+        worst = max(worst, LO.assert_within(got[r], ref, tol, f"{what} expert {e}"))
+    assert (got[~touched] == 0x4000).all(), f"{what}: wrote rows that hold nothing"
+    log(f"grouped {what}: {worst:.2f} of the bound")
+
+
+CONTIGUOUS = [((1,), 1, 16, 128), ((128, 0, 5), 4, 208, 256), ((129, 300, 0, 17, 64), 5, 1040, 640),
+              ((40, 256, 384), 3, 512, 384), ((1000,), 1, 768, 1152)]
+
+
+@pytest.mark.parametrize("counts,E,N,K", CONTIGUOUS)
+@pytest.mark.parametrize("gate_up", [False, True])
+def test_grouped_contiguous(counts, E, N, K, gate_up):
+    if gate_up and N % 64:
+        N = (N + 63) // 64 * 64
+    packed, w = _mx_weight(E, N, K, N + K, gate_up)
+    idx = []
+    for e, n in enumerate(counts):
+        idx += [e] * n + [-1] * (-n % 128)
+    idx += [-1] * 128                                     # an over-allocated tail
+    c, s, a = _mx_rows(len(idx), K, 3)
+    pad = np.array(idx) < 0
+    s[pad] = 255                                          # NaN rows in the padding
+    out = torch.full((len(idx) + 2, N), 2.0, dtype=torch.bfloat16, device=dev())
+    M.grouped_mxfp4_contiguous(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array(idx, np.int32)), out=out)
+    live = [i for i, e in enumerate(idx) if e >= 0]
+    _grouped_check(bits(out), live, [idx[i] for i in live], a, w, f"contiguous {counts} N={N} K={K}")
+
+
+def test_grouped_contiguous_experts_out_of_order_and_foreign_ids():
+    packed, w = _mx_weight(4, 96, 256, 9)
+    idx = [3] * 100 + [-1] * 28 + [0] * 128 + [0] * 2 + [-1] * 126 + [7] * 128 + [-5] * 128 + [1] * 1 + [-1] * 127
+    c, s, a = _mx_rows(len(idx), 256, 4)
+    out = torch.full((len(idx), 96), 2.0, dtype=torch.bfloat16, device=dev())
+    M.grouped_mxfp4_contiguous(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array(idx, np.int32)), out=out)
+    live = [i for i, e in enumerate(idx) if 0 <= e < 4]
+    _grouped_check(bits(out), live, [idx[i] for i in live], a, w, "out of order")
+
+
+MASKED = [((1,), 1, 1, 1, 16, 128), ((0, 3, 16), 16, 5, 3, 208, 256), ((17, 0, 40, 33), 40, 20, 4, 1040, 640),
+          ((128, 1, 70), 130, 60, 3, 512, 384), ((500, 130, 0), 512, 200, 3, 272, 1152), ((9, 200, 1), 200, 4, 3, 64, 256)]
+
+
+@pytest.mark.parametrize("counts,max_m,expected,E,N,K", MASKED)
+def test_grouped_masked(counts, max_m, expected, E, N, K):
+    packed, w = _mx_weight(E, N, K, N + K + 1)
+    c, s, a = _mx_rows(E * max_m, K, 6)
+    live = [(g * max_m + r, g) for g, n in enumerate(counts) for r in range(n)]
+    dead = np.ones(E * max_m, bool)
+    dead[[i for i, _ in live]] = False
+    s[dead] = 255
+    out = torch.full((E * max_m + 1, N), 2.0, dtype=torch.bfloat16, device=dev())
+    M.grouped_mxfp4_masked(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array(counts, np.int32)), expected, out=out)
+    _grouped_check(bits(out), [i for i, _ in live], [g for _, g in live], a, w, f"masked {counts} N={N} K={K}")
+
+
+def test_grouped_masked_clamps_counts():
+    packed, w = _mx_weight(3, 64, 128, 2)
+    c, s, a = _mx_rows(3 * 20, 128, 6)
+    out = torch.full((60, 64), 2.0, dtype=torch.bfloat16, device=dev())
+    M.grouped_mxfp4_masked(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array([-4, 99, 2], np.int32)), 8, out=out)
+    rows = list(range(20, 40)) + [40, 41]
+    _grouped_check(bits(out), rows, [1] * 20 + [2] * 2, a, w, "clamped")
+
+
+def test_grouped_mxfp4_refusals_and_empty():
+    packed, _ = _mx_weight(2, 64, 128, 2)
+    c, s, _ = _mx_rows(256, 128, 6)
+    rows = M.MXRows(to_dev(c), to_dev(s))
+    idx = torch.zeros(256, dtype=torch.int32, device=dev())
+    with pytest.raises(ValueError):
+        M.grouped_mxfp4_contiguous(rows, packed, idx[:128])
+    with pytest.raises(ValueError):
+        M.grouped_mxfp4_contiguous(M.MXRows(rows.codes, rows.scales[:, :2].contiguous()), packed, idx)
+    with pytest.raises(ValueError):
+        M.grouped_mxfp4_masked(rows, packed, idx[:3], 8)
+    with pytest.raises(ValueError):
+        M.grouped_mxfp4_masked(M.MXRows(rows.codes[:255], rows.scales[:255]), packed, idx[:2], 8)
+    with pytest.raises(M.W4A16Error):
+        M.grouped_mxfp4_masked(rows, packed, idx[:2], 0)
+    with pytest.raises(M.W4A16Error):
+        M.grouped_mxfp4_contiguous(M.MXRows(rows.codes[:64], rows.scales[:64]), packed, idx[:64])
+    e = M.grouped_mxfp4_contiguous(M.MXRows(rows.codes[:0], rows.scales[:0]), packed, idx[:0])
+    assert e.shape == (0, 64)
+
+
+def test_quantised_layer_over_the_contiguous_layout_matches_the_indexed_calls():
+    """A layer as a user runs it: weights quantised and packed from bf16,
+    logits routed, rows laid out by expert, both projections grouped; against
+    the indexed A4W4 calls on the same routing."""
+    T, k, E, H, I = 150, 2, 4, 256, 128
+    g = torch.Generator().manual_seed(2)
+    w1 = (0.05 * torch.randn(E, 2 * I, H, generator=g)).to(torch.bfloat16).to(dev())
+    w2 = (0.05 * torch.randn(E, H, I, generator=g)).to(torch.bfloat16).to(dev())
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).to(dev())
+    p1, p2 = M.quant_pack_mxfp4(w1), M.quant_pack_mxfp4(w2)
+    ids, wt = M.moe_route(torch.randn(T, E, generator=g).to(dev()), k)
+    flat = ids.cpu().numpy().reshape(-1)
+    rows, idx = [], []
+    for e in range(E):
+        sl = np.nonzero(flat == e)[0]
+        rows += sl.tolist() + [0] * (-len(sl) % 128)
+        idx += [e] * len(sl) + [-1] * (-len(sl) % 128)
+    rows_d, idx_d = to_dev(np.array(rows)), to_dev(np.array(idx, np.int32))
+    h = M.grouped_mxfp4_contiguous(M.mxfp4_quant(x[rows_d // k]), p1, idx_d)
+    r = M.moe_align(ids, E, 0, E, 64)
+    hi = M.moe_mxfp4_gemm(M.mxfp4_quant(x), p1, r)
+    live = idx_d >= 0
+    assert torch.equal(h[live], hi[rows_d[live]])          # one summation order whatever the tile
+    act = (torch.nn.functional.silu(h[:, :I].float()) * h[:, I:].float()).to(torch.bfloat16)
+    z = M.grouped_mxfp4_contiguous(M.mxfp4_quant(act.contiguous()), p2, idx_d)
+    slot = torch.zeros(T * k, H, device=dev())
+    slot[rows_d[live]] = z[live].float()
+    y = (slot.view(T, k, H) * wt[..., None]).sum(1)
+    acti = torch.zeros(T * k, I, dtype=torch.bfloat16, device=dev())
+    acti[rows_d[live]] = act[live]
+    ref = M.moe_mxfp4_gemm(M.mxfp4_quant(acti), p2, r, wt).float()
+    # here each expert's row is rounded to bf16 before the sum, there the sum is rounded once
+    tol = 2.0 ** -8 * ((slot.abs().view(T, k, H) * wt[..., None]).sum(1) + 2 * ref.abs())
+    assert ((y - ref).abs() <= tol).all()
+
+
+def test_grouped_mxfp4_captured_and_replayed():
+    packed, _ = _mx_weight(3, 320, 512, 5)
+    c, s, _ = _mx_rows(384, 512, 6)
+    rows = M.MXRows(to_dev(c), to_dev(s))
+    idx = to_dev(np.array([1] * 100 + [-1] * 28 + [0] * 128 + [2] * 3 + [-1] * 125, np.int32))
+    cnt = to_dev(np.array([5, 128, 0], np.int32))
+    x = torch.randn(384, 512, dtype=torch.bfloat16, device=dev())
+
+    def step():
+        M.mxfp4_quant(x, out=rows)
+        return M.grouped_mxfp4_contiguous(rows, packed, idx), M.grouped_mxfp4_masked(rows, packed, cnt, 40)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for rep in range(4):
+        x.normal_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        ref = step()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]), rep
+        _ = (x.float() @ x.float().t()).sum().item()

@@ -37,6 +37,8 @@ DESC_GATE_UP = 1            # W4A16_DESC_GATE_UP
 DESC_MXFP4 = 2              # W4A16_DESC_MXFP4
 A_TOKEN, A_SLOT, A_SORTED = 0, 1, 2   # W4A16_A_TOKEN / _SLOT / _SORTED
 ROUTE_INDEXED, ROUTE_CONTIGUOUS, ROUTE_MASKED = 0, 1, 2   # W4A16_ROUTE_*
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2                # W4A16_DTYPE_*
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1                       # W4A16_SCORE_*
 
 
 class Config(ctypes.Structure):
@@ -102,6 +104,14 @@ SIGNATURES = {
     "w4a16_mxfp4_moe_gemm": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _P, _I64, _I32,
                                     ctypes.POINTER(IndexedRouting), _P, _P, ctypes.POINTER(Config),
                                     _P, _SZ, _P]),
+    "w4a16_mxfp4_quant_pack": (_I32, [_P, _I32, ctypes.POINTER(WeightDesc), _P, _P, _P]),
+    "w4a16_mxfp4_dequant": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _P]),
+    "w4a16_mxfp4_grouped_contiguous": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _P, _I64, _P, _P, _P]),
+    "w4a16_mxfp4_grouped_masked": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _P, _I32, _P, _I32, _P, _P]),
+    "w4a16_moe_route": (_I32, [_P, _I32, _I32, _I32, _I64, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
+    "w4a16_moe_few_tokens": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, ctypes.POINTER(WeightDesc), _P, _P, _P,
+                                    _I32, _I32, _P, _P, _I32, _P, _P, _SZ, _P]),
+    "w4a16_moe_few_tokens_workspace_bytes": (_SZ, [ctypes.POINTER(WeightDesc), _I32, _I32]),
 }
 
 _lib = None

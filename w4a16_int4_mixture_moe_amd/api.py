@@ -16,6 +16,12 @@ the computation runs in the HIP library's kernels.
     pm = pack_mxfp4(codes_u8[E, N, K/2], scales_e8m0[E, N, K/32])
     q = mxfp4_quant(x[T, K])                                         # MXFP4 rows
     h = moe_mxfp4_gemm(q, pm, routing)                               # per slot
+    pm = quant_pack_mxfp4(w[E, N, K])                                # from bf16 / fp32 weights
+    out = grouped_mxfp4_contiguous(q, pm, m_indices)
+    out = grouped_mxfp4_masked(q, pm, masked_m, expected_m)
+    # router, and the whole layer for a few tokens (p1 / p2 INT4 or MXFP4)
+    topk_ids, topk_weights = moe_route(logits[T, E_glob], k)
+    y = moe_few_tokens(x, p1, p2, topk_ids, topk_weights)
 """
 from __future__ import annotations
 
@@ -25,8 +31,9 @@ from typing import Optional
 
 import torch
 
-from ._lib import (A_SLOT, A_SORTED, A_TOKEN, DESC_GATE_UP, DESC_MXFP4, ROUTE_CONTIGUOUS, ROUTE_INDEXED,
-                   ROUTE_MASKED, Config, IndexedRouting, W4A16Error, WeightDesc, check, load)
+from ._lib import (A_SLOT, A_SORTED, A_TOKEN, DESC_GATE_UP, DESC_MXFP4, DTYPE_BF16, DTYPE_F16, DTYPE_F32,
+                   ROUTE_CONTIGUOUS, ROUTE_INDEXED, ROUTE_MASKED, SCORE_SIGMOID, SCORE_SOFTMAX, Config,
+                   IndexedRouting, W4A16Error, WeightDesc, check, load)
 
 
 def _stream(dev: torch.device) -> ctypes.c_void_p:
@@ -498,4 +505,188 @@ def moe_mxfp4_gate_up_silu(x: MXRows, packed: PackedW4, routing: Routing, cfg: O
                                           x.codes.data_ptr(), x.scales.data_ptr(), x.rows, ctypes.byref(r),
                                           out.codes.data_ptr(), out.scales.data_ptr(),
                                           None if cfg is None else ctypes.byref(cfg), _stream(dev)))
+    return out
+
+
+def quant_pack_mxfp4(w: torch.Tensor, gate_up: bool = False) -> PackedW4:
+    """Quantise a weight to MXFP4 and pack it in one pass: w bf16 or float32
+    [E, N, K] (finite, K % 128 == 0) -> the weight pack_mxfp4 builds from the
+    quantised codes (mxfp4_quant's conversion, blocks of 32 along K)."""
+    _need(w, "w", tuple(_WEIGHT_DTYPES), 3)
+    E, N, K = w.shape
+    d = mxfp4_weight_desc(E, N, K, gate_up)
+    pw = torch.empty(d.w_bytes, dtype=torch.uint8, device=w.device)
+    ps = torch.empty(d.s_bytes, dtype=torch.uint8, device=w.device)
+    with torch.cuda.device(w.device):
+        check(load().w4a16_mxfp4_quant_pack(w.data_ptr(), _WEIGHT_DTYPES[w.dtype], ctypes.byref(d), pw.data_ptr(),
+                                            ps.data_ptr(), _stream(w.device)))
+    return PackedW4(d, pw, ps)
+
+
+def dequant_mxfp4(packed: PackedW4, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values a packed MXFP4 weight stands for, bf16 [E, N, K] (exact, in
+    the logical row order)."""
+    if not packed.desc.flags & DESC_MXFP4:
+        raise ValueError("dequant_mxfp4 needs an MXFP4 weight")
+    shape = (packed.E, packed.N, packed.K)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=packed.w.device)
+    else:
+        _need(out, "out", (torch.bfloat16,), 3)
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out must be {list(shape)}")
+    _same_device(packed.w, w=packed.w, s=packed.s, out=out)
+    with torch.cuda.device(out.device):
+        check(load().w4a16_mxfp4_dequant(ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(),
+                                         out.data_ptr(), _stream(out.device)))
+    return out
+
+
+def _same_device(ref: torch.Tensor, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+_WEIGHT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+_LOGIT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_SCORINGS = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+def _grouped_mx_args(a: MXRows, packed: PackedW4, index: torch.Tensor, name: str, rows: int,
+                     out: Optional[torch.Tensor]) -> torch.Tensor:
+    if not packed.desc.flags & DESC_MXFP4:
+        raise ValueError("the grouped MXFP4 calls need an MXFP4 weight")
+    _need(a.codes, "a.codes", (torch.uint8,), 2)
+    _need(a.scales, "a.scales", (torch.uint8,), 2)
+    _need(index, name, (torch.int32,), 1)
+    if a.K != packed.K or tuple(a.scales.shape) != (a.rows, packed.K // 32):
+        raise ValueError(f"activations [{a.rows}, {a.K}] with scales {tuple(a.scales.shape)} do not match K={packed.K}")
+    if a.rows != rows:
+        raise ValueError(f"activations have {a.rows} rows, expected {rows}")
+    if out is None:
+        out = torch.zeros(rows, packed.N, dtype=torch.bfloat16, device=a.codes.device)
+    else:
+        _need(out, "out", _BF16, 2)
+        if out.shape[0] < rows or out.shape[1] != packed.N:
+            raise ValueError(f"out must be [{rows}, {packed.N}]")
+    _same_device(a.codes, scales=a.scales, index=index, weight=packed.w, weight_scales=packed.s, out=out)
+    return out
+
+
+def grouped_mxfp4_contiguous(a: MXRows, packed: PackedW4, m_indices: torch.Tensor,
+                             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A4W4 on the contiguous layout: MXFP4 rows a [m, K] (experts' rows back
+    to back, segments at multiples of 128 rows, m a multiple of 128),
+    m_indices int32 [m] (-1 on padding) -> out bf16 [m, N]; padding rows are
+    left as they are (zero in an out made here)."""
+    out = _grouped_mx_args(a, packed, m_indices, "m_indices", m_indices.shape[0], out)
+    with torch.cuda.device(out.device):
+        check(load().w4a16_mxfp4_grouped_contiguous(ctypes.byref(packed.desc), packed.w.data_ptr(),
+                                                    packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(),
+                                                    a.rows, m_indices.data_ptr(), out.data_ptr(),
+                                                    _stream(out.device)))
+    return out
+
+
+def grouped_mxfp4_masked(a: MXRows, packed: PackedW4, masked_m: torch.Tensor, expected_m: int,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A4W4 on the masked layout: MXFP4 rows a [E * max_m, K] (max_m rows a
+    group), masked_m int32 [E] -> out bf16 [E * max_m, N]; rows at or past a
+    group's count are left as they are (zero in an out made here)."""
+    if packed.E == 0 or a.rows % packed.E or a.rows == 0:
+        raise ValueError(f"{a.rows} rows are not a whole number of rows for each of {packed.E} groups")
+    out = _grouped_mx_args(a, packed, masked_m, "masked_m", a.rows, out)
+    if masked_m.shape[0] != packed.E:
+        raise ValueError(f"masked_m has {masked_m.shape[0]} entries, the weight {packed.E} experts")
+    with torch.cuda.device(out.device):
+        check(load().w4a16_mxfp4_grouped_masked(ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(),
+                                                a.codes.data_ptr(), a.scales.data_ptr(), a.rows // packed.E,
+                                                masked_m.data_ptr(), int(expected_m), out.data_ptr(),
+                                                _stream(out.device)))
+    return out
+
+
+# ------------------------------------------------------------ router, few-token layer
+
+def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
+              renormalize: bool = True, scale: float = 1.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gate logits [T, E] (float32, bfloat16 or float16; rows may be strided)
+    -> topk_ids int32 [T, topk], topk_weights float32 [T, topk], in falling
+    order, ties to the lower expert.  scoring "softmax" orders by logit,
+    "sigmoid" by sigmoid + bias (float32 [E], selection only).  renormalize
+    divides by the chosen scores' sum; scale multiplies the weights.  Logits
+    (or biases) of -inf or NaN mask an expert; a slot without one left gets
+    id -1 and weight 0."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a GPU")
+    if logits.dtype not in _LOGIT_DTYPES:
+        raise TypeError(f"logits has dtype {logits.dtype}, expected one of {tuple(_LOGIT_DTYPES)}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have 2 dims, got {tuple(logits.shape)}")
+    T, E = logits.shape
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("the experts of a row must be contiguous")
+    if scoring not in _SCORINGS:
+        raise ValueError(f"scoring must be one of {sorted(_SCORINGS)}")
+    if bias is not None:
+        _need(bias, "bias", (torch.float32,), 1)
+        if bias.shape[0] != E:
+            raise ValueError(f"bias has {bias.shape[0]} entries, logits {E} experts")
+        _same_device(logits, bias=bias)
+    dev = logits.device
+    ids = torch.empty(T, max(int(topk), 0), dtype=torch.int32, device=dev)
+    weights = torch.empty(T, max(int(topk), 0), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        check(load().w4a16_moe_route(logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E,
+                                     logits.stride(0) if T > 1 else E, _ptr(bias), int(topk), _SCORINGS[scoring],
+                                     int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(),
+                                     _stream(dev)))
+    return ids, weights
+
+
+def few_tokens_workspace_bytes(gate_up: PackedW4, T: int, topk: int) -> int:
+    """Workspace bytes of moe_few_tokens (0 where the call refuses T, topk)."""
+    return int(load().w4a16_moe_few_tokens_workspace_bytes(ctypes.byref(gate_up.desc), T, topk))
+
+
+def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids: torch.Tensor,
+                   topk_weights: torch.Tensor, first_expert: int = 0, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole MoE layer for at most 64 tokens (and 1024 routed slots): x bf16
+    [T, H], gate_up [E, 2I, H] packed with gate_up=True, down [E, H, I], both
+    INT4 or both MXFP4, topk_ids int32 and topk_weights float32 [T, k] ->
+    bf16 [T, H], the sum over each token's experts in [first_expert,
+    first_expert + E) of weight * down(silu(gate x) * up x)."""
+    _need(x, "x", _BF16, 2)
+    _need(topk_ids, "topk_ids", (torch.int32,), 2)
+    _need(topk_weights, "topk_weights", (torch.float32,), 2)
+    T, H = x.shape
+    if H != gate_up.K:
+        raise ValueError(f"x has H={H}, the gate/up weight K={gate_up.K}")
+    if topk_ids.shape[0] != T or topk_weights.shape != topk_ids.shape:
+        raise ValueError(f"topk_ids {tuple(topk_ids.shape)} / topk_weights {tuple(topk_weights.shape)} "
+                         f"do not match {T} tokens")
+    k = topk_ids.shape[1]
+    dev = x.device
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", _BF16, 2)
+        if out.shape[0] < T or out.shape[1] != H:
+            raise ValueError(f"out must be [{T}, {H}]")
+    if workspace is None:
+        nws = few_tokens_workspace_bytes(gate_up, T, k)
+        if nws:
+            workspace = torch.empty(nws, dtype=torch.uint8, device=dev)
+    _same_device(x, gate_up=gate_up.w, gate_up_scales=gate_up.s, down=down.w, down_scales=down.s, topk_ids=topk_ids,
+                 topk_weights=topk_weights, out=out, workspace=workspace)
+    with torch.cuda.device(dev):
+        check(load().w4a16_moe_few_tokens(ctypes.byref(gate_up.desc), gate_up.w.data_ptr(), gate_up.s.data_ptr(),
+                                          ctypes.byref(down.desc), down.w.data_ptr(), down.s.data_ptr(), x.data_ptr(),
+                                          T, k, topk_ids.data_ptr(), topk_weights.data_ptr(), int(first_expert),
+                                          out.data_ptr(), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel(), _stream(dev)))
     return out

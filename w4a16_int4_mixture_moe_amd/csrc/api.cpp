@@ -1052,6 +1052,49 @@ w4a16_status w4a16_grouped_masked(const w4a16_weight_desc* desc, const void* pac
                         static_cast<hipStream_t>(stream), "grouped_masked launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+// ---- checks the grouped MXFP4 calls share
+w4a16_status check_mx_grouped(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                              const uint8_t* a_codes, const uint16_t* out) {
+  w4a16_status st = check_mx_desc(desc);
+  if (st != W4A16_OK) return st;
+  if (!packed_w || !packed_s) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (!aligned16(packed_w) || !aligned16(packed_s) || !aligned16(a_codes) || !aligned16(out))
+    return fail(W4A16_ERR_ARG, "packed weights, activation codes and output must be 16-byte aligned");
+  return W4A16_OK;
+}
+
+w4a16_status check_mx_rows(int64_t rows, int32_t K) {
+  if (rows >= INT32_MAX / 2) return fail(W4A16_ERR_SHAPE, "%lld rows are too many", (long long)rows);
+  if (rows * (int64_t)(K / 2) >= ((int64_t)1 << 32))
+    return fail(W4A16_ERR_SHAPE, "activation codes exceed 4 GiB (32-bit row offsets)");
+  return W4A16_OK;
+}
+
+// ---- workspace of the few-token layer: [h, bf16 slots x I][rows][leaders]
+struct FewWorkspace {
+  size_t h = 0, rows = 0, leaders = 0;
+  size_t total() const { return h + rows + leaders; }
+};
+
+FewWorkspace few_workspace(int32_t I, int32_t slots) {
+  FewWorkspace w;
+  w.h = al256((size_t)slots * I * 2);
+  w.rows = al256((size_t)slots * 16 * sizeof(w4a16::FewRow));
+  w.leaders = al256((size_t)slots * 4);
+  return w;
+}
+
+static_assert(W4A16_FEW_MAX_TOKENS == w4a16::kFewMaxTokens && W4A16_FEW_MAX_SLOTS == w4a16::kFewMaxSlots,
+              "the header's limits are the kernels'");
+
+}  // namespace
+
+extern "C" {
+
 // ------------------------------------------------------------ A4W4 (MXFP4)
 
 w4a16_status w4a16_mxfp4_weight_desc_init(int32_t E, int32_t N, int32_t K, w4a16_weight_desc* out) {
@@ -1268,6 +1311,184 @@ w4a16_status w4a16_mxfp4_gate_up_silu(const w4a16_weight_desc* desc, const void*
   hipError_t e = w4a16::launch_mx_gemm(w4a16::kEpiSiluMx, c.block_m / 16, c.nr, c.waves, c.stages, p,
                                        static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "mxfp4_gate_up_silu launch");
+  return W4A16_OK;
+}
+
+w4a16_status w4a16_mxfp4_quant_pack(const void* w, int32_t w_dtype, const w4a16_weight_desc* desc, void* packed_w,
+                                    void* packed_s, w4a16_stream_t stream) {
+  w4a16_status st = check_mx_desc(desc);
+  if (st != W4A16_OK) return st;
+  if (w_dtype != W4A16_DTYPE_F32 && w_dtype != W4A16_DTYPE_BF16)
+    return fail(W4A16_ERR_UNSUPPORTED, "w_dtype %d: weights are quantised from W4A16_DTYPE_F32 or W4A16_DTYPE_BF16", w_dtype);
+  if (!w || !packed_w || !packed_s) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (!aligned16(w) || !aligned16(packed_w) || !aligned16(packed_s))
+    return fail(W4A16_ERR_ARG, "weights and packed buffers must be 16-byte aligned");
+  hipError_t e = w4a16::launch_mx_quant_pack(w, w_dtype == W4A16_DTYPE_F32, desc->E, desc->N, desc->K,
+                                             (desc->flags & W4A16_DESC_GATE_UP) != 0, static_cast<uint32_t*>(packed_w),
+                                             static_cast<uint8_t*>(packed_s), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "mxfp4_quant_pack launch");
+  return W4A16_OK;
+}
+
+w4a16_status w4a16_mxfp4_dequant(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                 uint16_t* out, w4a16_stream_t stream) {
+  w4a16_status st = check_mx_desc(desc);
+  if (st != W4A16_OK) return st;
+  if (!packed_w || !packed_s || !out) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (!aligned16(packed_w) || !aligned16(packed_s) || !aligned16(out))
+    return fail(W4A16_ERR_ARG, "packed buffers and output must be 16-byte aligned");
+  hipError_t e = w4a16::launch_mx_dequant(static_cast<const uint32_t*>(packed_w), static_cast<const uint8_t*>(packed_s),
+                                          desc->E, desc->N, desc->K, (desc->flags & W4A16_DESC_GATE_UP) != 0, out,
+                                          static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "mxfp4_dequant launch");
+  return W4A16_OK;
+}
+
+w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                            const uint8_t* a_codes, const uint8_t* a_scales, int64_t m_rows,
+                                            const int32_t* m_indices, uint16_t* out, w4a16_stream_t stream) {
+  w4a16_status st = check_mx_grouped(desc, packed_w, packed_s, a_codes, out);
+  if (st != W4A16_OK) return st;
+  if (m_rows < 0) return fail(W4A16_ERR_ARG, "m_rows < 0");
+  if (m_rows > 0 && (!a_codes || !a_scales || !m_indices || !out)) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (m_rows % 128)
+    return fail(W4A16_ERR_SHAPE, "m_rows=%lld is not a multiple of 128 (segments are 128-row aligned)", (long long)m_rows);
+  st = check_mx_rows(m_rows, desc->K);
+  if (st != W4A16_OK) return st;
+  if (m_rows == 0) return W4A16_OK;
+  const int32_t bm = 128;
+  w4a16::GemmParams p = base_params(desc, packed_w, packed_s, reinterpret_cast<const uint16_t*>(a_codes), out, 4, 4);
+  p.a_scale = a_scales;
+  p.m_indices = m_indices;
+  p.grid_blocks = (int32_t)(m_rows / bm);
+  hipError_t e = w4a16::launch_mx_grouped(w4a16::kRouteContiguous, bm / 16, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "mxfp4_grouped_contiguous launch");
+  return W4A16_OK;
+}
+
+w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                        const uint8_t* a_codes, const uint8_t* a_scales, int32_t max_m,
+                                        const int32_t* masked_m, int32_t expected_m, uint16_t* out,
+                                        w4a16_stream_t stream) {
+  w4a16_status st = check_mx_grouped(desc, packed_w, packed_s, a_codes, out);
+  if (st != W4A16_OK) return st;
+  if (max_m <= 0) return fail(W4A16_ERR_ARG, "max_m must be positive");
+  if (expected_m <= 0) return fail(W4A16_ERR_ARG, "expected_m must be positive");
+  if (!a_codes || !a_scales || !masked_m || !out) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if ((int64_t)desc->E * max_m >= INT32_MAX / 2) return fail(W4A16_ERR_SHAPE, "E * max_m too large");
+  st = check_mx_rows((int64_t)desc->E * max_m, desc->K);
+  if (st != W4A16_OK) return st;
+  const int32_t want = std::min(max_m, expected_m + (expected_m + 3) / 4);
+  const int32_t bm = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+  w4a16::GemmParams p = base_params(desc, packed_w, packed_s, reinterpret_cast<const uint16_t*>(a_codes), out, 4, 4);
+  p.a_scale = a_scales;
+  p.masked_m = masked_m;
+  p.max_m = max_m;
+  p.blocks_per_group = (max_m + bm - 1) / bm;
+  p.grid_blocks = desc->E * p.blocks_per_group;
+  hipError_t e = w4a16::launch_mx_grouped(w4a16::kRouteMasked, bm / 16, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "mxfp4_grouped_masked launch");
+  return W4A16_OK;
+}
+
+// ------------------------------------------------------------ router
+
+w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride,
+                             const float* bias, int32_t topk, int32_t scoring, int32_t renormalize, float scale,
+                             int32_t* topk_ids, float* topk_weights, w4a16_stream_t stream) {
+  if (T < 0 || E <= 0) return fail(W4A16_ERR_ARG, "bad sizes T=%d E=%d", T, E);
+  if (topk <= 0 || topk > E) return fail(W4A16_ERR_ARG, "topk = %d outside [1, E = %d]", topk, E);
+  if (topk > W4A16_ROUTE_MAX_TOPK || E > W4A16_ROUTE_MAX_EXPERTS)
+    return fail(W4A16_ERR_SHAPE, "topk = %d, E = %d: at most %d of %d experts", topk, E, W4A16_ROUTE_MAX_TOPK,
+                W4A16_ROUTE_MAX_EXPERTS);
+  if (dtype != W4A16_DTYPE_F32 && dtype != W4A16_DTYPE_BF16 && dtype != W4A16_DTYPE_F16)
+    return fail(W4A16_ERR_UNSUPPORTED, "logits dtype %d is not W4A16_DTYPE_F32, _BF16 or _F16", dtype);
+  if (scoring != W4A16_SCORE_SOFTMAX && scoring != W4A16_SCORE_SIGMOID)
+    return fail(W4A16_ERR_UNSUPPORTED, "scoring %d is not W4A16_SCORE_SOFTMAX or W4A16_SCORE_SIGMOID", scoring);
+  if (bias && scoring != W4A16_SCORE_SIGMOID)
+    return fail(W4A16_ERR_UNSUPPORTED, "a selection bias is for sigmoid scores only");
+  if (!std::isfinite(scale)) return fail(W4A16_ERR_ARG, "scale must be finite");
+  if (T > 1 && row_stride < E) return fail(W4A16_ERR_ARG, "row_stride = %lld < E = %d", (long long)row_stride, E);
+  if (T == 0) return W4A16_OK;
+  if (!logits || !topk_ids || !topk_weights) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  const uintptr_t size = dtype == W4A16_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(bias) % 4 ||
+      reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
+    return fail(W4A16_ERR_ARG, "a pointer is not aligned to its elements");
+  hipError_t e = w4a16::launch_route(logits, dtype, row_stride, bias, T, E, topk, scoring == W4A16_SCORE_SIGMOID,
+                                     renormalize != 0, scale, topk_ids, topk_weights,
+                                     static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "moe_route launch");
+  return W4A16_OK;
+}
+
+// ------------------------------------------------------------ a layer for a few tokens
+
+size_t w4a16_moe_few_tokens_workspace_bytes(const w4a16_weight_desc* gate_up, int32_t T, int32_t topk) {
+  if (check_desc(gate_up) != W4A16_OK || T <= 0 || topk <= 0 || T > W4A16_FEW_MAX_TOKENS ||
+      topk > W4A16_FEW_MAX_SLOTS / T)
+    return 0;
+  return few_workspace(gate_up->N / 2, T * topk).total();
+}
+
+w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* gate_up_w, const void* gate_up_s,
+                                  const w4a16_weight_desc* down, const void* down_w, const void* down_s,
+                                  const uint16_t* x, int32_t T, int32_t topk, const int32_t* topk_ids,
+                                  const float* topk_weights, int32_t first_expert, uint16_t* out, void* workspace,
+                                  size_t workspace_bytes, w4a16_stream_t stream) {
+  w4a16_status st = check_desc(gate_up);
+  if (st != W4A16_OK) return st;
+  st = check_desc(down);
+  if (st != W4A16_OK) return st;
+  const bool mx = (gate_up->flags & W4A16_DESC_MXFP4) != 0;
+  if (!(gate_up->flags & W4A16_DESC_GATE_UP))
+    return fail(W4A16_ERR_LAYOUT, "the gate/up weight needs gate/up packing (w4a16_..._weight_desc_init_gate_up)");
+  if (down->flags != (mx ? W4A16_DESC_MXFP4 : 0))
+    return fail(W4A16_ERR_LAYOUT, "the down weight needs plain packing in the gate/up weight's format");
+  if (down->E != gate_up->E || down->N != gate_up->K || down->K != gate_up->N / 2)
+    return fail(W4A16_ERR_SHAPE, "weights do not chain: gate/up [%d, %d, %d], down [%d, %d, %d]", gate_up->E, gate_up->N,
+                gate_up->K, down->E, down->N, down->K);
+  if (T < 0 || topk <= 0 || first_expert < 0)
+    return fail(W4A16_ERR_ARG, "bad sizes T=%d topk=%d first_expert=%d", T, topk, first_expert);
+  if ((int64_t)first_expert + gate_up->E > INT32_MAX) return fail(W4A16_ERR_ARG, "first_expert = %d too large", first_expert);
+  if (T > W4A16_FEW_MAX_TOKENS || (int64_t)T * topk > W4A16_FEW_MAX_SLOTS)
+    return fail(W4A16_ERR_SHAPE, "T = %d, topk = %d: at most %d tokens and %d slots (use moe_align and the GEMM calls)", T,
+                topk, W4A16_FEW_MAX_TOKENS, W4A16_FEW_MAX_SLOTS);
+  if (!gate_up_w || !gate_up_s || !down_w || !down_s) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (T > 0 && (!x || !topk_ids || !topk_weights || !out)) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (!aligned16(gate_up_w) || !aligned16(gate_up_s) || !aligned16(down_w) || !aligned16(down_s) || !aligned16(x) ||
+      !aligned16(out))
+    return fail(W4A16_ERR_ARG, "packed weights, activations and output must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
+    return fail(W4A16_ERR_ARG, "topk_ids and topk_weights must be 4-byte aligned");
+  if (T == 0) return W4A16_OK;
+  const FewWorkspace ws = few_workspace(down->K, T * topk);
+  if (!workspace || workspace_bytes < ws.total() || !aligned16(workspace))
+    return fail(W4A16_ERR_WORKSPACE, "this call needs %zu bytes of 16-byte aligned workspace, got %zu", ws.total(),
+                workspace ? workspace_bytes : (size_t)0);
+  char* base = static_cast<char*>(workspace);
+  w4a16::FewParams p;
+  p.w1 = static_cast<const uint8_t*>(gate_up_w);
+  p.s1 = static_cast<const uint8_t*>(gate_up_s);
+  p.w2 = static_cast<const uint8_t*>(down_w);
+  p.s2 = static_cast<const uint8_t*>(down_s);
+  p.x = x;
+  p.topk_ids = topk_ids;
+  p.topk_weights = topk_weights;
+  p.T = T;
+  p.topk = topk;
+  p.first = first_expert;
+  p.E = gate_up->E;
+  p.H = gate_up->K;
+  p.I = down->K;
+  p.KC1 = gate_up->chunks;
+  p.KC2 = down->chunks;
+  p.h = reinterpret_cast<uint16_t*>(base);
+  p.rows = reinterpret_cast<w4a16::FewRow*>(base + ws.h);
+  p.leader = reinterpret_cast<int32_t*>(base + ws.h + ws.rows);
+  p.out = out;
+  hipError_t e = w4a16::launch_few_tokens(mx, p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "moe_few_tokens launch");
   return W4A16_OK;
 }
 

@@ -66,6 +66,19 @@ __device__ __forceinline__ bf16x8_t dequant8(uint32_t d, float s, float c0, floa
   return r;
 }
 
+// The 8 E2M1 codes of one word (element 0 in the lowest nibble) times the
+// power of two `s` as a bf16 MFMA operand.  v_cvt_scalef32_pk_bf16_fp4 takes
+// the scale's exponent field, two codes (one byte) an instruction; the result
+// is exact down to 2^-127, where the products are bf16 subnormals.
+__device__ __forceinline__ bf16x8_t mxfp4_to_bf16x8(uint32_t word, float s) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, s, 0);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, s, 1);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, s, 2);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(word, s, 3);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 // Source row of row i of packed tile `tile`: with gate_up, packed tile 2t is
 // gate tile t (rows 16t..) and packed tile 2t + 1 up tile t (rows N/2 + 16t..)
 // (both weight packers)

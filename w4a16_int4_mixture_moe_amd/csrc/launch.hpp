@@ -142,9 +142,49 @@ hipError_t launch_mx_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* 
 // gate_up: tiles of the gate rows [0, N/2) and up rows [N/2, N) alternate.
 hipError_t launch_mx_pack(const uint8_t* w, const uint8_t* s, int32_t E, int32_t N, int32_t K, int32_t gate_up,
                           uint4* pw, uint8_t* ps, hipStream_t stream);
+// bf16 or fp32 weights [E][N][K] quantised into the same packed layout, and a
+// packed weight's values as bf16; K % 128 == 0
+hipError_t launch_mx_quant_pack(const void* w, bool fp32, int32_t E, int32_t N, int32_t K, int32_t gate_up,
+                                uint32_t* pw, uint8_t* ps, hipStream_t stream);
+hipError_t launch_mx_dequant(const uint32_t* pw, const uint8_t* ps, int32_t E, int32_t N, int32_t K, int32_t gate_up,
+                             uint16_t* out, hipStream_t stream);
+// The grouped layouts (route kRouteContiguous or kRouteMasked), bf16 store;
+// m_tiles: 16-row token tiles per block (1, 2, 4 or 8)
+hipError_t launch_mx_grouped(int route, int m_tiles, const GemmParams& p, hipStream_t stream);
 // Indexed routing only; epilogue kEpiStore, kEpiWeighted or kEpiSiluMx.
 bool mx_gemm_config_supported(int epilogue, int m_tiles, int nr, int waves, int stages);
 hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stages, const GemmParams& p,
                           hipStream_t stream);
+
+
+// ---- router (route.hip): dtype 0 fp32, 1 bf16, 2 fp16 logits
+hipError_t launch_route(const void* logits, int dtype, int64_t row_stride, const float* bias, int32_t T, int32_t E,
+                        int32_t topk, int sigmoid, int renorm, float scale, int32_t* ids, float* weights,
+                        hipStream_t stream);
+
+// ---- a whole layer for a few tokens (few.hip)
+constexpr int kFewMaxTokens = 64;
+constexpr int kFewMaxSlots = 1024;        // T * topk
+
+// one row of a block of an expert's rows: its slot (-1: none) and the token's
+// weight for the expert
+struct FewRow {
+  int32_t slot;
+  float weight;
+};
+
+struct FewParams {
+  const uint8_t *w1, *s1, *w2, *s2;       // packed gate/up and down weights, their scales
+  const uint16_t* x;                      // [T][H]
+  const int32_t* topk_ids;                // [T][topk]
+  const float* topk_weights;
+  int32_t T, topk, first, E;              // experts [first, first + E) are held here
+  int32_t H, I, KC1, KC2;                 // hidden and intermediate width, their 128-wide chunks
+  uint16_t* h;                            // [T * topk][I], rows of local slots
+  FewRow* rows;                           // [T * topk][16], the rows of blocks that lead
+  int32_t* leader;                        // [T * topk]: 1 where the slot leads a block
+  uint16_t* out;                          // [T][H]
+};
+hipError_t launch_few_tokens(bool mxfp4, const FewParams& p, hipStream_t stream);
 
 }  // namespace w4a16

@@ -109,6 +109,120 @@ hipError_t launch_mx_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* 
 
 // ------------------------------------------------------------ weight packing
 
+// Weight quantisation straight into the packed layout: bf16 or fp32 [E, N, K]
+// -> fragments and scale bytes, the conversion of mx_quant_kernel (on fp32
+// the exponent and the rounding are taken from all 24 bits, not from a bf16
+// copy).  One wave per (expert, tile, chunk), 16 rows x 128 K: lane l of step
+// q takes 8 consecutive K of row 4 q + l / 16, so a load instruction covers
+// whole 256-byte (fp32: 512-byte) row pieces and the four lanes of an MX
+// block are neighbours, which share their maximum with two DPP steps.  Each
+// lane's 8 codes are one word of the packed fragment.  HBM-bound: 2 or 4
+// bytes in and 17/32 byte out an element, one pass.
+template <typename T>
+__global__ __launch_bounds__(256) void mx_quant_pack_kernel(const T* __restrict__ w, int64_t tiles, int32_t N,
+                                                             int32_t K, int32_t gate_up,
+                                                             uint32_t* __restrict__ pw, uint8_t* __restrict__ ps) {
+  constexpr int V = 16 / sizeof(T);                      // elements per 16-byte load
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t q0 = (int64_t)blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave;   // (expert, tile, chunk)
+  if (q0 >= tiles) return;
+  const int KC = K / 128, NT = N / 16;
+  const int c = (int)(q0 % KC);
+  const int64_t et = q0 / KC;
+  const int t = (int)(et % NT);
+  const int64_t e = et / NT;
+  const int piece = lane & 15;                           // 8 elements of the chunk: block piece / 4, word piece % 4
+  u32x4_t v[4][8 / V];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = e * N + source_row(t, 4 * q + (lane >> 4), N, gate_up);
+    const u32x4_t* src = reinterpret_cast<const u32x4_t*>(w + n * K + 128 * c + 8 * piece);
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i) v[q][i] = src[i];
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float f[8];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        const uint32_t word = v[q][i / 4][i % 4];          // a copy: bit_cast of a vector's element reads element 0
+        f[i] = __builtin_bit_cast(float, word);
+      } else {
+        const uint32_t pair = v[q][0][i / 2];
+        f[i] = __builtin_bit_cast(float, i & 1 ? pair & 0xFFFF0000u : pair << 16);
+      }
+      amax = max(amax, __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu);
+    }
+    // the four lanes of a block (quad_perm [1,0,3,2], then [2,3,0,1])
+    amax = max(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0xB1, 0xF, 0xF, false));
+    amax = max(amax, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)amax, 0x4E, 0xF, 0xF, false));
+    const uint32_t code = (uint32_t)max((int)(amax >> 23) - 2, 0);
+    const float inv = __builtin_bit_cast(float, (254u - code) << 23);     // 2^(127 - code), exact
+    uint32_t word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, f[0] * inv, f[1] * inv, 1.0f, 0);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[2] * inv, f[3] * inv, 1.0f, 1);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[4] * inv, f[5] * inv, 1.0f, 2);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[6] * inv, f[7] * inv, 1.0f, 3);
+    // fragment of lane 16 g + i: row i, block g of the chunk
+    const int frag = (piece >> 2) * 16 + 4 * q + (lane >> 4);
+    pw[q0 * 256 + frag * 4 + (piece & 3)] = word;
+    if ((piece & 3) == 0) ps[q0 * kWave + frag] = (uint8_t)code;
+  }
+}
+
+hipError_t launch_mx_quant_pack(const void* w, bool fp32, int32_t E, int32_t N, int32_t K, int32_t gate_up,
+                                uint32_t* pw, uint8_t* ps, hipStream_t stream) {
+  const int64_t tiles = (int64_t)E * (N / 16) * (K / 128);
+  const int64_t grid = (tiles + 3) / 4;
+  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (fp32)
+    hipLaunchKernelGGL(mx_quant_pack_kernel<uint32_t>, dim3((unsigned)grid), dim3(256), 0, stream,
+                       static_cast<const uint32_t*>(w), tiles, N, K, gate_up, pw, ps);
+  else
+    hipLaunchKernelGGL(mx_quant_pack_kernel<uint16_t>, dim3((unsigned)grid), dim3(256), 0, stream,
+                       static_cast<const uint16_t*>(w), tiles, N, K, gate_up, pw, ps);
+  return hipGetLastError();
+}
+
+// The packed weight's values as bf16 [E, N, K] (exact: an E2M1 value times a
+// power of two), the same lanes and rows as above: 17/32 byte in, 2 bytes out.
+__global__ __launch_bounds__(256) void mx_dequant_kernel(const uint32_t* __restrict__ pw,
+                                                          const uint8_t* __restrict__ ps, int64_t tiles, int32_t N,
+                                                          int32_t K, int32_t gate_up, uint16_t* __restrict__ out) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t q0 = (int64_t)blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave;
+  if (q0 >= tiles) return;
+  const int KC = K / 128, NT = N / 16;
+  const int c = (int)(q0 % KC);
+  const int64_t et = q0 / KC;
+  const int t = (int)(et % NT);
+  const int64_t e = et / NT;
+  const int piece = lane & 15;
+  uint32_t word[4], code[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int frag = (piece >> 2) * 16 + 4 * q + (lane >> 4);
+    word[q] = pw[q0 * 256 + frag * 4 + (piece & 3)];
+    code[q] = ps[q0 * kWave + frag];
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = e * N + source_row(t, 4 * q + (lane >> 4), N, gate_up);
+    *reinterpret_cast<bf16x8_t*>(out + n * K + 128 * c + 8 * piece) =
+        mxfp4_to_bf16x8(word[q], __builtin_bit_cast(float, code[q] << 23));
+  }
+}
+
+hipError_t launch_mx_dequant(const uint32_t* pw, const uint8_t* ps, int32_t E, int32_t N, int32_t K, int32_t gate_up,
+                             uint16_t* out, hipStream_t stream) {
+  const int64_t tiles = (int64_t)E * (N / 16) * (K / 128);
+  const int64_t grid = (tiles + 3) / 4;
+  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(mx_dequant_kernel, dim3((unsigned)grid), dim3(256), 0, stream, pw, ps, tiles, N, K, gate_up, out);
+  return hipGetLastError();
+}
+
 // One thread per (expert, tile, chunk, lane): row n = 16 tile + lane % 16,
 // block 4 chunk + lane / 16 -> the row's 16 code bytes of that block and its
 // scale byte.
@@ -442,13 +556,13 @@ __device__ __forceinline__ void mx_silu_epilogue(const GemmParams& p, const Smem
   }
 }
 
-template <int MT, int NR, int NW, int D, int EPI>
+template <int MT, int NR, int NW, int D, int EPI, int ROUTE = kRouteIndexed>
 __global__ __launch_bounds__(NW * kWave) void mx_gemm_kernel(const GemmParams p) {
   constexpr bool STAGED = MT >= 4;
   __shared__ std::conditional_t<STAGED, MxStagedSmem<MT>, MxSmem<MT>> sm;
   int mb, nt;
   if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
-  const int expert = setup_rows<MT, NW, kRouteIndexed, EPI>(p, mb, sm);
+  const int expert = setup_rows<MT, NW, ROUTE, EPI>(p, mb, sm);
   if (expert < 0) return;
   __syncthreads();
   const uint32_t tmask = active_tiles<MT>(sm);
@@ -629,6 +743,30 @@ hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stag
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(waves * kWave), 0, stream, q);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ grouped layouts
+
+template <int ROUTE>
+static MxKernel pick_mx_grouped(int m_tiles) {
+  if (m_tiles == 1) return mx_gemm_kernel<1, 4, 4, 4, kEpiStore, ROUTE>;
+  if (m_tiles == 2) return mx_gemm_kernel<2, 4, 4, 4, kEpiStore, ROUTE>;
+  if (m_tiles == 4) return mx_gemm_kernel<4, 4, 4, 2, kEpiStore, ROUTE>;
+  return m_tiles == 8 ? mx_gemm_kernel<8, 4, 4, 2, kEpiStore, ROUTE> : nullptr;
+}
+
+hipError_t launch_mx_grouped(int route, int m_tiles, const GemmParams& p, hipStream_t stream) {
+  const MxKernel k = route == kRouteContiguous ? pick_mx_grouped<kRouteContiguous>(m_tiles)
+                                               : pick_mx_grouped<kRouteMasked>(m_tiles);
+  if (k == nullptr) return hipErrorInvalidValue;
+  GemmParams q = p;
+  q.n_tiles = (p.NT + 15) / 16;                        // 16 weight tiles per workgroup (4 waves x 4)
+  q.xcd_group = 0;
+  const int64_t grid = grid_of(q, q.n_tiles);
+  if (grid <= 0) return hipSuccess;
+  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(4 * kWave), 0, stream, q);
   return hipGetLastError();
 }
 
