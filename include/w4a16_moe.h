@@ -594,6 +594,7 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
 #define W4A16_SCORE_SIGMOID 1
 #define W4A16_ROUTE_MAX_TOPK 32
 #define W4A16_ROUTE_MAX_EXPERTS 1024
+#define W4A16_ROUTE_MAX_STRIDE (1 << 26)   /* elements: 16 rows stay below 4 GiB */
 
 /* logits: T rows of E values of dtype W4A16_DTYPE_*, row_stride elements
  * apart (>= E).  Per row, the topk experts in falling order, the lower expert
@@ -609,7 +610,8 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
  * w4a16_moe_align (validate = 0), the combine and w4a16_moe_few_tokens skip
  * like any expert held elsewhere.
  * topk_ids: int32 [T, topk]; topk_weights: float [T, topk].
- * Sizes: topk <= min(E, W4A16_ROUTE_MAX_TOPK), E <= W4A16_ROUTE_MAX_EXPERTS.
+ * Sizes: topk <= min(E, W4A16_ROUTE_MAX_TOPK), E <= W4A16_ROUTE_MAX_EXPERTS,
+ * row_stride <= W4A16_ROUTE_MAX_STRIDE (not read for a single row).
  * Errors: ERR_ARG, ERR_SHAPE, ERR_UNSUPPORTED (dtype, scoring, or a bias with
  * softmax), ERR_HIP. */
 w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride,

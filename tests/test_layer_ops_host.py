@@ -89,7 +89,7 @@ def test_route_refusals(L):
     assert call(dtype=3) == -4 and call(scoring=2) == -4
     assert call(bias=P) == -4                                            # a bias with softmax
     assert call(scale=float("nan")) == -1 and call(scale=float("inf")) == -1
-    assert call(stride=63) == -1
+    assert call(stride=63) == -1 and call(stride=(1 << 26) + 1) == -2
     assert call(logits=None) == -1 and call(ids=None) == -1 and call(w=None) == -1
     assert call(logits=P + 2) == -1 and call(ids=P + 1) == -1            # not aligned to the element
     assert call(logits=P + 1, dtype=1) == -1

@@ -40,6 +40,15 @@ def _stream(dev: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _launch(dev: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with `dev` current, on its current stream."""
+    if dev.index == torch.cuda.current_device():
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -517,9 +526,8 @@ def quant_pack_mxfp4(w: torch.Tensor, gate_up: bool = False) -> PackedW4:
     d = mxfp4_weight_desc(E, N, K, gate_up)
     pw = torch.empty(d.w_bytes, dtype=torch.uint8, device=w.device)
     ps = torch.empty(d.s_bytes, dtype=torch.uint8, device=w.device)
-    with torch.cuda.device(w.device):
-        check(load().w4a16_mxfp4_quant_pack(w.data_ptr(), _WEIGHT_DTYPES[w.dtype], ctypes.byref(d), pw.data_ptr(),
-                                            ps.data_ptr(), _stream(w.device)))
+    _launch(w.device, load().w4a16_mxfp4_quant_pack, w.data_ptr(), _WEIGHT_DTYPES[w.dtype], ctypes.byref(d),
+                pw.data_ptr(), ps.data_ptr())
     return PackedW4(d, pw, ps)
 
 
@@ -536,9 +544,8 @@ def dequant_mxfp4(packed: PackedW4, out: Optional[torch.Tensor] = None) -> torch
         if tuple(out.shape) != shape:
             raise ValueError(f"out must be {list(shape)}")
     _same_device(packed.w, w=packed.w, s=packed.s, out=out)
-    with torch.cuda.device(out.device):
-        check(load().w4a16_mxfp4_dequant(ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(),
-                                         out.data_ptr(), _stream(out.device)))
+    _launch(out.device, load().w4a16_mxfp4_dequant, ctypes.byref(packed.desc), packed.w.data_ptr(),
+                packed.s.data_ptr(), out.data_ptr())
     return out
 
 
@@ -581,11 +588,9 @@ def grouped_mxfp4_contiguous(a: MXRows, packed: PackedW4, m_indices: torch.Tenso
     m_indices int32 [m] (-1 on padding) -> out bf16 [m, N]; padding rows are
     left as they are (zero in an out made here)."""
     out = _grouped_mx_args(a, packed, m_indices, "m_indices", m_indices.shape[0], out)
-    with torch.cuda.device(out.device):
-        check(load().w4a16_mxfp4_grouped_contiguous(ctypes.byref(packed.desc), packed.w.data_ptr(),
-                                                    packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(),
-                                                    a.rows, m_indices.data_ptr(), out.data_ptr(),
-                                                    _stream(out.device)))
+    _launch(out.device, load().w4a16_mxfp4_grouped_contiguous, ctypes.byref(packed.desc), packed.w.data_ptr(),
+                packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), a.rows, m_indices.data_ptr(),
+                out.data_ptr())
     return out
 
 
@@ -599,11 +604,9 @@ def grouped_mxfp4_masked(a: MXRows, packed: PackedW4, masked_m: torch.Tensor, ex
     out = _grouped_mx_args(a, packed, masked_m, "masked_m", a.rows, out)
     if masked_m.shape[0] != packed.E:
         raise ValueError(f"masked_m has {masked_m.shape[0]} entries, the weight {packed.E} experts")
-    with torch.cuda.device(out.device):
-        check(load().w4a16_mxfp4_grouped_masked(ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(),
-                                                a.codes.data_ptr(), a.scales.data_ptr(), a.rows // packed.E,
-                                                masked_m.data_ptr(), int(expected_m), out.data_ptr(),
-                                                _stream(out.device)))
+    _launch(out.device, load().w4a16_mxfp4_grouped_masked, ctypes.byref(packed.desc), packed.w.data_ptr(),
+                packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), a.rows // packed.E,
+                masked_m.data_ptr(), int(expected_m), out.data_ptr())
     return out
 
 
@@ -639,11 +642,9 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
     dev = logits.device
     ids = torch.empty(T, max(int(topk), 0), dtype=torch.int32, device=dev)
     weights = torch.empty(T, max(int(topk), 0), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        check(load().w4a16_moe_route(logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E,
-                                     logits.stride(0) if T > 1 else E, _ptr(bias), int(topk), _SCORINGS[scoring],
-                                     int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(),
-                                     _stream(dev)))
+    _launch(dev, load().w4a16_moe_route, logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E, logits.stride(0) if T
+                > 1 else E, _ptr(bias), int(topk), _SCORINGS[scoring], int(bool(renormalize)), float(scale),
+                ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -683,10 +684,8 @@ def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids:
             workspace = torch.empty(nws, dtype=torch.uint8, device=dev)
     _same_device(x, gate_up=gate_up.w, gate_up_scales=gate_up.s, down=down.w, down_scales=down.s, topk_ids=topk_ids,
                  topk_weights=topk_weights, out=out, workspace=workspace)
-    with torch.cuda.device(dev):
-        check(load().w4a16_moe_few_tokens(ctypes.byref(gate_up.desc), gate_up.w.data_ptr(), gate_up.s.data_ptr(),
-                                          ctypes.byref(down.desc), down.w.data_ptr(), down.s.data_ptr(), x.data_ptr(),
-                                          T, k, topk_ids.data_ptr(), topk_weights.data_ptr(), int(first_expert),
-                                          out.data_ptr(), _ptr(workspace),
-                                          0 if workspace is None else workspace.numel(), _stream(dev)))
+    _launch(dev, load().w4a16_moe_few_tokens, ctypes.byref(gate_up.desc), gate_up.w.data_ptr(),
+                gate_up.s.data_ptr(), ctypes.byref(down.desc), down.w.data_ptr(), down.s.data_ptr(), x.data_ptr(),
+                T, k, topk_ids.data_ptr(), topk_weights.data_ptr(), int(first_expert), out.data_ptr(),
+                _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out

@@ -1409,13 +1409,15 @@ w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32
     return fail(W4A16_ERR_UNSUPPORTED, "a selection bias is for sigmoid scores only");
   if (!std::isfinite(scale)) return fail(W4A16_ERR_ARG, "scale must be finite");
   if (T > 1 && row_stride < E) return fail(W4A16_ERR_ARG, "row_stride = %lld < E = %d", (long long)row_stride, E);
+  if (T > 1 && row_stride > W4A16_ROUTE_MAX_STRIDE)
+    return fail(W4A16_ERR_SHAPE, "row_stride = %lld above %d", (long long)row_stride, W4A16_ROUTE_MAX_STRIDE);
   if (T == 0) return W4A16_OK;
   if (!logits || !topk_ids || !topk_weights) return fail(W4A16_ERR_ARG, "NULL pointer argument");
   const uintptr_t size = dtype == W4A16_DTYPE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(bias) % 4 ||
       reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
     return fail(W4A16_ERR_ARG, "a pointer is not aligned to its elements");
-  hipError_t e = w4a16::launch_route(logits, dtype, row_stride, bias, T, E, topk, scoring == W4A16_SCORE_SIGMOID,
+  hipError_t e = w4a16::launch_route(logits, dtype, T > 1 ? row_stride : E, bias, T, E, topk, scoring == W4A16_SCORE_SIGMOID,
                                      renormalize != 0, scale, topk_ids, topk_weights,
                                      static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "moe_route launch");

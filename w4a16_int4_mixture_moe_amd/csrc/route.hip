@@ -9,20 +9,25 @@
 // logit (or bias) is -inf or NaN is masked; a slot for which no expert is
 // left gets id -1 and weight 0.
 //
-// One wave per token.  Lane l holds experts [l V, l V + V) in registers as
-// order-preserving 32-bit integers, so the wave's maximum is four DPP steps
-// and four lane reads, and the winner of equal keys -- the lowest expert --
-// is the lowest set bit of a ballot.  k rounds; a round costs about 3 V + 20
-// instructions.  The bytes that have to move are the logits, read once; each
-// row is read by one wave, and the weights are worked out by lanes 0 .. k - 1
-// at the end.
+// A group of L lanes holds one token, V = ceil(E / L) keys a lane (expert
+// i L + lane, so loads are coalesced).  What bounds a long batch is the
+// number of vector instructions a token, not its bytes, so the k winners are
+// not taken out one by one:
+//   1. each lane's maximum; the k-th largest of those L maxima is a lower
+//      bound of the k-th largest key (k rounds of a DPP maximum over the
+//      group, equal maxima leaving together);
+//   2. every expert at or above the bound is appended to a list in LDS: k
+//      of them and a few more (L sum_{i<k} 1 / (L - i) expected: 11 at k = 8,
+//      L = 16; 18 at k = 16, L = 64);
+//   3. each listed expert counts the listed ones that come before it (larger
+//      key, or equal and lower index): its rank, whatever the list's order.
+// A list that overflows (many equal keys) falls back to k passes over the
+// row.
 //
 // Order with a bias.  s_e + b_e in 32 bits carries an error of a few 2^-24,
-// enough to swap two experts that nearly tie.  After k + 1 rounds the gaps
-// between consecutive winners are compared with that error's bound; where one
-// is too small the wave forms s_e + b_e in 64 bits for the candidates (every
-// expert whose 32-bit key could be among the top k) and picks again from
-// those.  About one token in a hundred takes that path at 384 experts.
+// enough to swap two experts that nearly tie.  The list's bound is lowered by
+// that error, and where two of its keys are closer than it the group ranks
+// the list again by s_e + b_e in 64 bits.
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -30,61 +35,97 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kRouteWaves = 4;      // tokens per workgroup
+constexpr int kRouteThreads = 256;
 constexpr float kMaxFinite = 3.402823466e+38f;
 
+// +inf counts as the largest finite value; a NaN stays one
 template <typename T>
-__device__ __forceinline__ float logit_value(const T* p);
-template <>
-__device__ __forceinline__ float logit_value<float>(const float* p) { return *p; }
-template <>
-__device__ __forceinline__ float logit_value<_Float16>(const _Float16* p) { return (float)*p; }
-template <>
-__device__ __forceinline__ float logit_value<__bf16>(const __bf16* p) { return (float)*p; }
-
-// Ordered key of a value that is not NaN: u < v as integers exactly when
-// a < b as floats; -0 counts as +0.  0 is below every value's key.
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
-  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float from_ordered(uint32_t u) {
-  return __builtin_bit_cast(float, u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
+__device__ __forceinline__ float logit_value(T v) {
+  const float x = (float)v;
+  return x > kMaxFinite ? kMaxFinite : x;
 }
 
 template <int kCtrl>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false));
+__device__ __forceinline__ float max_dpp(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, false);
+  return fmaxf(v, __builtin_bit_cast(float, o));
 }
 
-// maximum over the wave, in every lane (a scalar): rotate within rows of 16
-// lanes (row_ror 1, 2, 4, 8), then the four rows
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+// maximum over the group of L lanes, in each of them: rotations within rows
+// of 16 lanes, then (L = 64) rows and halves exchanged
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
   v = max_dpp<0x121>(v);
   v = max_dpp<0x122>(v);
   v = max_dpp<0x124>(v);
   v = max_dpp<0x128>(v);
-  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
-  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-  return max(max(a, b), max(c, d));
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m);
+  if constexpr (L == 64) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t r0 = r[0], r1 = r[1];
+    const uint32_t b = __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1)));
+    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t q0 = q[0], q1 = q[1];
+    v = fmaxf(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
+  }
   return v;
 }
 
-__device__ __forceinline__ double wave_max_f64(double v) {
+template <int kCtrl>
+__device__ __forceinline__ double add_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, kCtrl, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kCtrl, 0xF, 0xF, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// sum over the group, the same bits in each of its lanes: neighbours, pairs
+// (quad_perm), mirrored halves and rows, then (L = 64) rows
+template <int L>
+__device__ __forceinline__ double group_sum(double v) {
+  v = add_dpp<0xB1>(v);
+  v = add_dpp<0x4E>(v);
+  v = add_dpp<0x141>(v);
+  v = add_dpp<0x140>(v);
 #pragma unroll
-  for (int m = 1; m < kWave; m *= 2) v = fmax(v, __shfl_xor(v, m));
+  for (int m = 16; m < L; m *= 2) v += __shfl_xor(v, m);
   return v;
 }
 
-// 1 / (1 + exp(-x)), without overflow at either end
+// sum over the lanes of the group before this one (row_shr 1, 2, 4, 8 inside
+// a row; then the rows before)
+template <int L>
+__device__ __forceinline__ int group_prefix(int v) {
+  int s = v;
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, true);
+  if constexpr (L == 64) {
+    const int a = __builtin_amdgcn_readlane(s, 15), b = __builtin_amdgcn_readlane(s, 31);
+    const int c = __builtin_amdgcn_readlane(s, 47);
+    const int row = (threadIdx.x % 64) / 16;
+    s += (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
+  }
+  return s - v;
+}
+
+// 1 / (1 + exp(-x)), without overflow at either end, within a few 2^-24
 __device__ __forceinline__ float sigmoid32(float x) {
   const float z = expf(-fabsf(x));
   return (x >= 0.f ? 1.f : z) / (1.f + z);
+}
+
+// the same within 2^-22 absolutely (exp and reciprocal instructions; the
+// exponent's rounding moves the result by at most |x| e^-|x| 2^-24 more)
+__device__ __forceinline__ float sigmoid_key(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+
+// keys of two experts further apart than this are in true order: each is off
+// by at most 2^-22 (sigmoid) + half a unit of the sum
+__device__ __forceinline__ float key_error(float c) { return 0x1p-21f + 0x1p-23f * (fabsf(c) + 1.f); }
+
+__device__ __forceinline__ double exact_key(float x, float b) {
+  return fmin(1.0 / (1.0 + exp(-(double)x)) + (double)b, 1.7976931348623157e308);
 }
 
 struct RouteArgs {
@@ -98,147 +139,239 @@ struct RouteArgs {
   float* weights;
 };
 
-template <typename T, int V, bool kSigmoid>
-__global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(const RouteArgs p) {
-  extern __shared__ double exact_keys[];                  // kRouteWaves x 64 V, only with a bias
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t >= p.T) return;                                   // whole waves; the workgroup never synchronises
-  const T* row = static_cast<const T*>(p.logits) + t * p.row_stride;
-  const int e0 = lane * V;
+struct Candidate {
+  float key;
+  int32_t expert;
+};
+
+// in order of choice: larger key first, the lower expert of equals
+template <typename K>
+__device__ __forceinline__ bool before(K a, int ea, K b, int eb) { return a > b || (a == b && ea < eb); }
+
+template <int L>
+struct RouteSmem {
+  static constexpr int G = kRouteThreads / L;      // tokens per workgroup
+  static constexpr int CAP = 2 * (L < 32 ? 16 : L);  // listed experts a token, at most
+  Candidate list[G][CAP + 4];                       // read four at a time
+  float logit[G][CAP];                              // with a bias
+  double exact[G][CAP];
+  int count[G];
+};
+
+template <typename T, int L, int V, bool kSigmoid>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p) {
+  using Smem = RouteSmem<L>;
+  constexpr int OWN = Smem::CAP / L;                // listed experts a lane looks after
+  __shared__ Smem sm;
+  const int g = threadIdx.x / L, l = threadIdx.x % L;
+  // groups past the last token follow it and store nothing
+  const int64_t t0 = (int64_t)blockIdx.x * Smem::G;
+  const int follow = (int)min((int64_t)g, p.T - 1 - t0);
+  const bool real = follow == g;
+  const int64_t t = t0 + follow;
+  // the workgroup's rows: a uniform base and 32-bit offsets (the launcher bounds the stride)
+  const T* rows = static_cast<const T*>(p.logits) + t0 * p.row_stride;
+  const uint32_t row0 = (uint32_t)follow * (uint32_t)p.row_stride;
   const bool biased = kSigmoid && p.bias != nullptr;
 
-  // masked experts: key 0; a +inf logit counts as the largest finite value
-  float x[V], b[V];
+  // keys; -inf: masked or past E
+  float x[V], key[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = min(e0 + i, p.E - 1);
-    x[i] = logit_value<T>(row + e);
-    b[i] = 0.f;
-    if (biased) b[i] = p.bias[e];
-  }
-  uint32_t key[V];
-  float top = -kMaxFinite;
+  for (int i = 0; i < V; ++i) x[i] = logit_value(rows[min(row0 + i * L + l, row0 + p.E - 1)]);
   double sum = 0.0;
+  float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const bool live = e0 + i < p.E && x[i] > -INFINITY && b[i] > -INFINITY;   // false for NaN
-    const float v = fminf(x[i], kMaxFinite);
-    key[i] = 0u;
-    if (live) {
-      key[i] = ordered(biased ? fminf(sigmoid32(v) + b[i], kMaxFinite) : v);
-      top = fmaxf(top, v);
-    }
-  }
-  if (!kSigmoid && !p.renorm) {                            // softmax over every live expert
-    top = from_ordered(wave_max(ordered(top)));
+  for (int i = 0; i < V; ++i) key[i] = i * L + l < p.E && x[i] > -INFINITY ? x[i] : -INFINITY;   // a NaN compares false
+  if (biased) {
+    float b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = p.bias[min((uint32_t)(i * L + l), (uint32_t)p.E - 1u)];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i]) sum += (double)expf(fminf(x[i], kMaxFinite) - top);
-    sum = wave_sum(sum);
+      key[i] = key[i] > -INFINITY && b[i] > -INFINITY ? fminf(sigmoid_key(key[i]) + b[i], kMaxFinite) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = fmaxf(m, key[i]);
+  const float top = group_max<L>(m);
+  if (!kSigmoid && !p.renorm) {                     // softmax over every live expert
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] > -INFINITY) sum += (double)expf(key[i] - top);
+    sum = group_sum<L>(sum);
   }
 
-  // k rounds; lane j keeps the j-th winner.  With a bias one round more, and
-  // the smallest gap between neighbours against the error of their keys.
-  int win = -1;
-  uint32_t prev = 0;
+  // the k-th largest lane maximum
+  float bound = top;
+  {
+    float rest = m;
+    for (int j = 1; j < p.topk; ++j) {
+      rest = rest == bound ? -INFINITY : rest;
+      bound = group_max<L>(rest);
+    }
+  }
+  if (biased) bound -= key_error(bound);
+  bound = fmaxf(bound, -kMaxFinite);                // fewer lanes than k hold an expert: every live one (NaN: as well)
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine += key[i] >= bound ? 1 : 0;
+  int at = group_prefix<L>(mine);
+  if (l == L - 1) sm.count[g] = at + mine;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (key[i] >= bound) {
+      if (at < Smem::CAP) {
+        sm.list[g][at] = Candidate{key[i], i * L + l};
+        if (biased) sm.logit[g][at] = x[i];
+      }
+      ++at;
+    }
+  __builtin_amdgcn_wave_barrier();
+  const int listed = sm.count[g];
+  const int n = min(listed, Smem::CAP);
+
+  int expert[OWN], rank[OWN];
+  float logit[OWN];
   bool close = false;
-  uint32_t threshold = 1u;
-  const int rounds = p.topk + (biased ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t m = key[0];
+  {
+    float own[OWN];
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, key[i]);
-    const uint32_t best = wave_max(m);
-    if (best == 0u) break;                                 // no live expert left
-    if (biased) {
-      const float c = from_ordered(best), a = from_ordered(prev);
-      // each key: the sigmoid within 2^-22, the sum within half a unit
-      const float err = 0x1p-21f + 0x1p-23f * fmaxf(fabsf(c), fabsf(a));
-      close = close || (j > 0 && !(a - c > err));
-      threshold = ordered(c - err);
-      if (j == p.topk) break;                              // only its gap was wanted
+    for (int q = 0; q < OWN; ++q) {
+      const Candidate c = sm.list[g][l + q * L];
+      expert[q] = l + q * L < n ? c.expert : -1;
+      own[q] = logit[q] = c.key;
+      if (biased) logit[q] = sm.logit[g][l + q * L];
+      rank[q] = 0;
     }
-    const int src = __builtin_ctzll(__ballot(m == best));
-    int slot = V - 1;
+    for (int j = 0; j < n; j += 4) {
+      Candidate c[4];
 #pragma unroll
-    for (int i = V - 2; i >= 0; --i) slot = key[i] == best ? i : slot;
-    const int e = __builtin_amdgcn_readlane(e0 + slot, src);
-    if (lane == j) win = e;
+      for (int i = 0; i < 4; ++i) c[i] = sm.list[g][j + i];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane == src && i == slot) key[i] = 0u;
-    prev = best;
-  }
-
-  if (biased && close) {
-    // The winners of the rounds above were taken out of `key`; the keys are
-    // formed again in 64 bits for every expert that can be among the top k.
-    double* mine = exact_keys + wave * (kWave * V) + lane * V;
+      for (int i = 0; i < 4; ++i) {
+        const bool there = j + i < n;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool live = e0 + i < p.E && x[i] > -INFINITY && b[i] > -INFINITY;
-      const float v = fminf(x[i], kMaxFinite);
-      double c = -HUGE_VAL;
-      if (live && ordered(fminf(sigmoid32(v) + b[i], kMaxFinite)) >= threshold)
-        c = fmin(1.0 / (1.0 + exp(-(double)v)) + (double)b[i], 1.7976931348623157e308);
-      mine[i] = c;
-    }
-    win = -1;
-    for (int j = 0; j < p.topk; ++j) {
-      double m = mine[0];
-      int slot = 0;
-      for (int i = 1; i < V; ++i) {
-        const double c = mine[i];
-        if (c > m) {
-          m = c;
-          slot = i;
+        for (int q = 0; q < OWN; ++q) {
+          rank[q] += there && before(c[i].key, c[i].expert, own[q], expert[q]) ? 1 : 0;
+          if (biased)
+            close = close || (there && expert[q] >= 0 && c[i].expert != expert[q] &&
+                              fabsf(c[i].key - own[q]) <= key_error(own[q]));
         }
       }
-      const double best = wave_max_f64(m);
-      if (best == -HUGE_VAL) break;
-      const int src = __builtin_ctzll(__ballot(m == best));
-      const int e = __builtin_amdgcn_readlane(e0 + slot, src);
-      if (lane == j) win = e;
-      if (lane == src) mine[slot] = -HUGE_VAL;             // read again by this lane only
+    }
+  }
+  if (biased && __ballot(close)) {                  // any group of the wave
+    double own[OWN];
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+      own[q] = -HUGE_VAL;
+      if (expert[q] >= 0) {
+        own[q] = exact_key(logit[q], p.bias[expert[q]]);
+        sm.exact[g][l + q * L] = own[q];
+      }
+      rank[q] = 0;
+    }
+    __builtin_amdgcn_wave_barrier();
+    for (int j = 0; j < n; ++j) {
+      const double c = sm.exact[g][j];
+      const int e = sm.list[g][j].expert;
+#pragma unroll
+      for (int q = 0; q < OWN; ++q) rank[q] += before(c, e, own[q], expert[q]) ? 1 : 0;
+    }
+  }
+  if (__ballot(listed > Smem::CAP)) {
+    // more equal keys than the list holds: k passes, each the best after the last
+    double last = HUGE_VAL;
+    int last_e = -1;
+    int found[OWN];
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) found[q] = -1;
+    for (int j = 0; j < p.topk; ++j) {
+      double best = -HUGE_VAL;
+      int best_e = p.E;
+      for (int e = l; e < p.E; e += L) {
+        const float v = logit_value(rows[row0 + e]);
+        const float b = biased ? p.bias[e] : 0.f;
+        if (!(v > -INFINITY && b > -INFINITY)) continue;
+        const double c = biased ? exact_key(v, b) : (double)v;
+        if (before(last, last_e, c, e) && before(c, e, best, best_e)) {
+          best = c;
+          best_e = e;
+        }
+      }
+#pragma unroll
+      for (int s = 1; s < L; s *= 2) {
+        const double c = __shfl_xor(best, s);
+        const int e = __shfl_xor(best_e, s);
+        if (before(c, e, best, best_e)) {
+          best = c;
+          best_e = e;
+        }
+      }
+      last = best;
+      last_e = best_e;
+#pragma unroll
+      for (int q = 0; q < OWN; ++q)
+        if (j == l + q * L && best > -HUGE_VAL) found[q] = best_e;
+    }
+    if (listed > Smem::CAP) {
+#pragma unroll
+      for (int q = 0; q < OWN; ++q) {
+        expert[q] = found[q];
+        rank[q] = found[q] >= 0 ? l + q * L : p.topk;
+        if (found[q] >= 0) logit[q] = logit_value(rows[row0 + found[q]]);
+      }
     }
   }
 
-  // weights of the winners, lane j's own; sums in 64 bits
-  float w = 0.f;
-  if constexpr (kSigmoid) {
-    if (win >= 0) w = sigmoid32(fminf(logit_value<T>(row + win), kMaxFinite));
-    if (p.renorm) sum = wave_sum((double)w) + 1e-20;
-  } else {
-    float v = -kMaxFinite;
-    if (win >= 0) v = fminf(logit_value<T>(row + win), kMaxFinite);
-    // the first winner holds the largest logit
-    const float first = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 0));
-    if (win >= 0) w = expf(v - first);
-    if (p.renorm) sum = wave_sum((double)w);
+  // weights of the chosen, each by the lane that ranked it; sums in 64 bits
+  float w[OWN];
+  double chosen = 0.0;
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    w[q] = 0.f;
+    if (expert[q] >= 0 && rank[q] < p.topk) w[q] = kSigmoid ? sigmoid32(logit[q]) : expf(logit[q] - top);
+    chosen += (double)w[q];
   }
-  if (lane < p.topk) {
-    const bool divide = !kSigmoid || p.renorm;
-    const double q = win < 0 ? 0.0 : (divide ? (double)w / sum : (double)w) * (double)p.scale;
-    p.ids[t * p.topk + lane] = win;
-    p.weights[t * p.topk + lane] = (float)q;
+  if (p.renorm) sum = group_sum<L>(chosen) + (kSigmoid ? 1e-20 : 0.0);
+  if (!real) return;
+  const bool divide = !kSigmoid || p.renorm;
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    if (expert[q] >= 0 && rank[q] < p.topk) {
+      p.ids[t * p.topk + rank[q]] = expert[q];
+      p.weights[t * p.topk + rank[q]] = (float)((divide ? (double)w[q] / sum : (double)w[q]) * (double)p.scale);
+    }
+  }
+  // slots for which no expert was left (an overflowing list never leaves any)
+  for (int j = n + l; j < p.topk; j += L) {
+    p.ids[t * p.topk + j] = -1;
+    p.weights[t * p.topk + j] = 0.f;
   }
 }
 
+// Lanes per token: 16 lanes share every instruction of the search with three
+// other tokens, 64 lanes finish a token sooner; and a 16-lane list stays short
+// only while k is well below 16.  Measured on MI355X, graph replays, 384
+// experts, top 8, 64 / 16 lanes: fp32 sigmoid + bias 4096 tokens 9.6 / 11.1 us,
+// 8192 13.4 / 12.2 us, 16384 22.6 / 17.1 us (1.5 TB/s of logits; an empty
+// launch is about 4.5 us); bf16 softmax 4096 7.6 / 8.0 us, 8192 10.9 / 8.7 us.
+// (Taking the k winners out one by one, 64 lanes: 16384 tokens 25 us.)
+constexpr int kNarrowMaxTopk = 10;
+constexpr int kNarrowMinTokens = 6144;
+
 template <typename T, bool kSigmoid>
 hipError_t launch_typed(const RouteArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
-  const int v = (a.E + kWave - 1) / kWave;
-  // experts per lane rounded up to a built width
-#define W4A16_ROUTE_CASE(V_)                                                                              \
-  if (v <= V_) {                                                                                          \
-    const size_t lds = a.bias != nullptr ? sizeof(double) * kRouteWaves * kWave * V_ : 0;                  \
-    hipLaunchKernelGGL((route_kernel<T, V_, kSigmoid>), grid, block, lds, stream, a);                      \
-    return hipGetLastError();                                                                             \
-  }
-  W4A16_ROUTE_CASE(1) W4A16_ROUTE_CASE(2) W4A16_ROUTE_CASE(4) W4A16_ROUTE_CASE(6) W4A16_ROUTE_CASE(8)
-  W4A16_ROUTE_CASE(12) W4A16_ROUTE_CASE(14) W4A16_ROUTE_CASE(16)
+  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens;
+  const int lanes = narrow ? 16 : 64;
+  const int v = (a.E + lanes - 1) / lanes;
+  const int per = kRouteThreads / lanes;
+  const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kRouteThreads);
+  // keys per lane rounded up to a built width
+#define W4A16_ROUTE_CASE(L_, V_)                                                                  if (lanes == L_ && v <= V_) {                                                                     hipLaunchKernelGGL((route_kernel<T, L_, V_, kSigmoid>), grid, block, 0, stream, a);              return hipGetLastError();                                                                     }
+  W4A16_ROUTE_CASE(16, 8) W4A16_ROUTE_CASE(16, 16) W4A16_ROUTE_CASE(16, 24) W4A16_ROUTE_CASE(16, 32)
+  W4A16_ROUTE_CASE(16, 56) W4A16_ROUTE_CASE(16, 64)
+  W4A16_ROUTE_CASE(64, 2) W4A16_ROUTE_CASE(64, 4) W4A16_ROUTE_CASE(64, 6) W4A16_ROUTE_CASE(64, 8)
+  W4A16_ROUTE_CASE(64, 14) W4A16_ROUTE_CASE(64, 16)
 #undef W4A16_ROUTE_CASE
   return hipErrorInvalidValue;
 }
