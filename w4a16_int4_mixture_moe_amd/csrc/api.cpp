@@ -1074,17 +1074,17 @@ w4a16_status check_mx_rows(int64_t rows, int32_t K) {
   return W4A16_OK;
 }
 
-// ---- workspace of the few-token layer: [h, bf16 slots x I][rows][leaders]
+// ---- workspace of the few-token layer: [h, bf16 slots x I][rows][experts][blocks]
 struct FewWorkspace {
-  size_t h = 0, rows = 0, leaders = 0;
-  size_t total() const { return h + rows + leaders; }
+  size_t h = 0, rows = 0, experts = 0;
+  size_t total() const { return h + rows + experts + 256; }
 };
 
 FewWorkspace few_workspace(int32_t I, int32_t slots) {
   FewWorkspace w;
   w.h = al256((size_t)slots * I * 2);
   w.rows = al256((size_t)slots * 16 * sizeof(w4a16::FewRow));
-  w.leaders = al256((size_t)slots * 4);
+  w.experts = al256((size_t)slots * 4);
   return w;
 }
 
@@ -1453,6 +1453,8 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
   if (T < 0 || topk <= 0 || first_expert < 0)
     return fail(W4A16_ERR_ARG, "bad sizes T=%d topk=%d first_expert=%d", T, topk, first_expert);
   if ((int64_t)first_expert + gate_up->E > INT32_MAX) return fail(W4A16_ERR_ARG, "first_expert = %d too large", first_expert);
+  if (gate_up->E > W4A16_FEW_MAX_EXPERTS)
+    return fail(W4A16_ERR_SHAPE, "%d local experts, at most %d", gate_up->E, W4A16_FEW_MAX_EXPERTS);
   if (T > W4A16_FEW_MAX_TOKENS || (int64_t)T * topk > W4A16_FEW_MAX_SLOTS)
     return fail(W4A16_ERR_SHAPE, "T = %d, topk = %d: at most %d tokens and %d slots (use moe_align and the GEMM calls)", T,
                 topk, W4A16_FEW_MAX_TOKENS, W4A16_FEW_MAX_SLOTS);
@@ -1487,7 +1489,8 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
   p.KC2 = down->chunks;
   p.h = reinterpret_cast<uint16_t*>(base);
   p.rows = reinterpret_cast<w4a16::FewRow*>(base + ws.h);
-  p.leader = reinterpret_cast<int32_t*>(base + ws.h + ws.rows);
+  p.experts = reinterpret_cast<int32_t*>(base + ws.h + ws.rows);
+  p.blocks = reinterpret_cast<int32_t*>(base + ws.h + ws.rows + ws.experts);
   p.out = out;
   hipError_t e = w4a16::launch_few_tokens(mx, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "moe_few_tokens launch");

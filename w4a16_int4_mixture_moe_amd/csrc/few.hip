@@ -17,9 +17,15 @@
 // gfx950's v_cvt_scalef32_pk_bf16_fp4, exact (an E2M1 value times a power of
 // two is a bf16 number).
 //
-// Rows.  The routed slots of expert e are taken 16 at a time in slot order;
-// the first slot of each such block is its leader and stands for the block.
-// A token that lists an expert twice is one row whose weights add up.
+// Rows.  An expert's tokens are taken 16 at a time in token order; each such
+// block of rows is one MFMA operand, and its weights are read once.  A token
+// that lists an expert twice is one row whose weights add up.  Every
+// workgroup of the first kernel works the blocks out for itself from the ids
+// (in LDS, from one read of them), so no launch goes before it; workgroup 0
+// leaves them in the workspace for the second kernel.
+#include <algorithm>
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "tile_common.hpp"
@@ -32,6 +38,8 @@ constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kFewWaves * kWave;
 constexpr int kSlotWords = kFewMaxSlots / kWave;       // ballot words over the slots
 static_assert(kFewMaxSlots == 2 * kFewThreads, "two slots a thread");
+// workgroups of the gate/up kernel: two on each of 256 CUs
+constexpr int kFewGroups = 512;
 
 // ---- the two weight kinds: K chunk c of one packed 16-row tile
 
@@ -75,176 +83,260 @@ __device__ __forceinline__ void load_rows(gptr_t row, int c, bool on, bf16x8_t (
 // ------------------------------------------------------------ gate / up
 
 struct GateUpSmem {
-  unsigned long long match[kSlotWords];                 // slots of this expert, one bit each
-  int row[16];                                          // slot of each column, -1 = none
-  f32x4_t red[kFewWaves][2][kWave];
+  int16_t key[kFewMaxSlots];                            // local expert of each slot, -1 = none
+  unsigned long long lead[kSlotWords];                  // slots that start a block, one bit each
+  uint32_t count[kFewMaxSlots];                       // rows of each block
+  int16_t expert[kFewMaxSlots];                         // of each block
+  int16_t row[kFewMaxSlots][16];                        // slots of each block
+  f32x4_t red[2][kFewWaves][2][kWave];
 };
 
-// Workgroup (tile pair, slot): if the slot leads a block of its expert, the
-// block's 16 gate and 16 up columns over all of K, the waves splitting the K
-// chunks; their sums meet in LDS in wave order.  The workgroups of pair 0
-// also leave the block's rows and weights for the down kernel.
-template <typename Weights>
-__global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(const FewParams p) {
-  constexpr int KB = 4;                                 // chunks in flight per wave
-  __shared__ GateUpSmem sm;
-  const int pair = blockIdx.x, s = blockIdx.y;
+// The blocks of rows, from the ids: rank of a slot = tokens before it that
+// list its expert; a slot starts a block where its rank is a multiple of 16;
+// blocks are numbered by the slot that starts them.  Returns their number.
+__device__ __forceinline__ int find_blocks(const FewParams& p, GateUpSmem& sm) {
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int S = p.T * p.topk;
-  const int id = p.topk_ids[s];
-  const int expert = __builtin_amdgcn_readfirstlane(id - p.first);
-  if ((unsigned)expert >= (unsigned)p.E) {              // not held here
-    if (pair == 0 && tid == 0) p.leader[s] = 0;
-    return;
-  }
-  // this expert's slots, the first of each token only
-  bool hit[2];
+  int key[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = tid + q * kFewThreads;
-    hit[q] = i < S && p.topk_ids[i] == id;
-    if (hit[q])
-      for (int j = i - i % p.topk; j < i; ++j)
-        if (p.topk_ids[j] == id) hit[q] = false;
-    const unsigned long long m = __ballot(hit[q]);
-    if (lane == 0) sm.match[q * kFewWaves + wave] = m;
+    const int e = i < S ? p.topk_ids[i] - p.first : -1;
+    key[q] = (unsigned)e < (unsigned)p.E ? e : -1;
+    sm.key[i] = (int16_t)key[q];
+    sm.count[i] = 0;
   }
-  if (tid < 16) sm.row[tid] = -1;
   __syncthreads();
-  auto position = [&](int i) {                          // slots of this expert before slot i
-    int n = 0;
-    for (int q = 0; q < i / kWave; ++q) n += __popcll(sm.match[q]);
-    return n + __popcll(sm.match[i / kWave] & ((1ull << (i % kWave)) - 1ull));
-  };
-  const int rank = position(s);
-  const bool lead = ((sm.match[s / kWave] >> (s % kWave)) & 1ull) && rank % 16 == 0;
-  if (!lead) {
-    if (pair == 0 && tid == 0) p.leader[s] = 0;
-    return;
-  }
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if (hit[q]) {
-      const int i = tid + q * kFewThreads;
-      const int n = position(i) - rank;
-      if (n >= 0 && n < 16) sm.row[n] = i;
-    }
-  __syncthreads();
-  const int slot = sm.row[lane & 15];
-  if (pair == 0 && tid < 16) {
-    float w = 0.f;
-    if (slot >= 0) {
-      const int i0 = slot - slot % p.topk;
-      for (int j = i0; j < i0 + p.topk; ++j)
-        if (p.topk_ids[j] == id) w += p.topk_weights[j];
-    }
-    p.rows[s * 16 + tid] = FewRow{slot, w};
-    if (tid == 0) p.leader[s] = 1;
-  }
-
-  const int KC = p.KC1;
-  const int c0 = (int)((int64_t)wave * KC / kFewWaves), c1 = (int)((int64_t)(wave + 1) * KC / kFewWaves);
-  gptr_t wbase[2], sbase[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int64_t tile = (int64_t)expert * (p.I / 8) + 2 * pair + r;
-    wbase[r] = uniform_ptr(p.w1 + tile * KC * (kWave * 16)) + lane * 16;
-    sbase[r] = uniform_ptr(p.s1 + tile * Weights::scale_tile_bytes(KC));
-  }
-  const int g = lane >> 4;
-  const gptr_t xrow = uniform_ptr(p.x) + (int64_t)(max(slot, 0) / p.topk) * p.H * 2 + g * 64;
-  const Weights weights;
-  f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-  for (int cb = c0; cb < c1; cb += KB) {
-    u32x4_t w[KB][2];
-    uint32_t sw[KB][2];
-    bf16x8_t x[KB][4];
-#pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      const int c = min(cb + i, c1 - 1);               // past c1: a repeated load, multiplied by zeros
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        w[i][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16));
-        sw[i][r] = Weights::load_scale(sbase[r], c, lane);
-      }
-      load_rows(xrow, c, slot >= 0 && cb + i < c1 && c * kChunk + g * kGroup < p.H, x[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      if (cb + i >= c1) break;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        bf16x8_t A[4];
-        weights.operands(w[i][r], sw[i][r], cb + i, A);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], x[i][j], acc[r], 0, 0, 0);
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) sm.red[wave][r][lane] = acc[r];
-  __syncthreads();
-  if (wave != 0 || slot < 0) return;
-  f32x4_t gu[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    gu[r] = sm.red[0][r][lane];
-#pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) gu[r] += sm.red[v][r][lane];
-  }
-  // one rounding, to the bf16 the down product's operand holds
-  uint2 o;
-  o.x = pack_bf16x2(silu_mul(gu[0][0], gu[1][0]), silu_mul(gu[0][1], gu[1][1]));
-  o.y = pack_bf16x2(silu_mul(gu[0][2], gu[1][2]), silu_mul(gu[0][3], gu[1][3]));
-  *reinterpret_cast<uint2*>(p.h + (int64_t)slot * p.I + pair * kRowTile + 4 * g) = o;
-}
-
-// ------------------------------------------------------------ down
-
-template <int MT>
-struct DownSmem {
-  unsigned long long lead[kSlotWords];
-  int list[kFewMaxSlots];                               // leaders in slot order
-  f32x4_t red[kFewWaves][MT][kWave];
-};
-
-// Workgroup n: 16 output columns of every token.  The (block, K chunk) units
-// of all blocks are split evenly over the waves; a wave adds each of its
-// blocks' rows, times the row's weight, to its totals (token t in column
-// t % 16 of total t / 16), and the waves' totals meet in LDS in wave order.
-template <typename Weights, int MT>
-__global__ __launch_bounds__(kFewThreads) void few_down_kernel(const FewParams p) {
-  constexpr int KB = 4;                                 // units in flight per wave
-  __shared__ DownSmem<MT> sm;
-  const int nt = blockIdx.x;
-  const int tid = threadIdx.x;
-  const int lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int S = p.T * p.topk;
-  bool lead[2];
+  int rank[2], start[2];                                // start: the slot that starts this slot's block
+  bool row[2];                                          // this slot is a row: local, the token's first of its expert
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = tid + q * kFewThreads;
-    lead[q] = i < S && p.leader[i] != 0;
-    const unsigned long long m = __ballot(lead[q]);
+    rank[q] = 0;
+    start[q] = i;
+    row[q] = key[q] >= 0;
+    unsigned long long m = 0;
+    if (q * kFewThreads + wave * kWave < S) {           // wave-uniform
+      const int t = i / p.topk;
+      for (int u = 0, j = 0; u <= min(p.T - 1, (q * kFewThreads + wave * kWave + kWave - 1) / p.topk); ++u) {
+        int hit = -1;
+        for (int k = 0; k < p.topk; ++k, ++j)
+          if (sm.key[j] == key[q] && hit < 0) hit = j;
+        if (u == t && hit != i) row[q] = false;         // an earlier slot of the token stands for it
+        if (u < t && hit >= 0) {
+          if (rank[q] % 16 == 0) start[q] = hit;
+          ++rank[q];
+        }
+      }
+      if (rank[q] % 16 == 0) start[q] = i;
+      m = __ballot(row[q] && rank[q] % 16 == 0);
+    }
     if (lane == 0) sm.lead[q * kFewWaves + wave] = m;
   }
   __syncthreads();
   int blocks = 0;
+  for (int w = 0; w < kSlotWords; ++w) blocks += __popcll(sm.lead[w]);
 #pragma unroll
-  for (int q = 0; q < kSlotWords; ++q) {
-    const unsigned long long m = sm.lead[q];
-    if (q % kFewWaves == wave && lead[q / kFewWaves])
-      sm.list[blocks + __popcll(m & ((1ull << lane) - 1ull))] = tid + (q / kFewWaves) * kFewThreads;
-    blocks += __popcll(m);
-  }
-  blocks = __builtin_amdgcn_readfirstlane(blocks);
+  for (int q = 0; q < 2; ++q)
+    if (row[q]) {
+      const int i = tid + q * kFewThreads;
+      int b = 0;
+      for (int w = 0; w < start[q] / kWave; ++w) b += __popcll(sm.lead[w]);
+      b += __popcll(sm.lead[start[q] / kWave] & ((1ull << (start[q] % kWave)) - 1ull));
+      sm.row[b][rank[q] % 16] = (int16_t)i;
+      atomicAdd(&sm.count[b], 1u);                    // a count: the order of the additions is nothing
+      if (start[q] == i) sm.expert[b] = (int16_t)key[q];
+    }
   __syncthreads();
+  return __builtin_amdgcn_readfirstlane(blocks);
+}
 
+// The blocks for the down kernel: number, expert of each, and each row's
+// slot and weight (-1, 0 past a block's rows).
+__device__ __forceinline__ void leave_plan(const FewParams& p, const GateUpSmem& sm, int blocks) {
+  for (int i = threadIdx.x; i < blocks * 16; i += kFewThreads) {
+    const int b = i / 16, r = i % 16;
+    FewRow row{-1, 0.f};
+    if (r < (int)sm.count[b]) {
+      row.slot = sm.row[b][r];
+      const int j0 = row.slot - row.slot % p.topk;
+      for (int j = j0; j < j0 + p.topk; ++j)
+        if (sm.key[j] == sm.expert[b]) row.weight += p.topk_weights[j];
+    }
+    p.rows[i] = row;
+    if (r == 0) p.experts[b] = sm.expert[b];
+  }
+  if (threadIdx.x == 0) *p.blocks = blocks;
+}
+
+// A barrier for LDS alone: the loads in flight for later chunks stay in
+// flight (__syncthreads waits for every one of them).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Calls step(0), step(1), ..., step(D - 1) over and over, the index a
+// compile-time constant (a ring of registers has no other), until one
+// returns true.
+template <int D, typename Step>
+__device__ __forceinline__ void ring_loop(Step&& step) {
+  for (;;) {
+    if (step(std::integral_constant<int, 0>{})) return;
+    if constexpr (D > 1)
+      if (step(std::integral_constant<int, 1>{})) return;
+    if constexpr (D > 2)
+      if (step(std::integral_constant<int, 2>{})) return;
+    if constexpr (D > 3)
+      if (step(std::integral_constant<int, 3>{})) return;
+    if constexpr (D > 4)
+      if (step(std::integral_constant<int, 4>{})) return;
+    if constexpr (D > 5)
+      if (step(std::integral_constant<int, 5>{})) return;
+    if constexpr (D > 6)
+      if (step(std::integral_constant<int, 6>{})) return;
+    static_assert(D <= 7, "ring depth");
+  }
+}
+
+// Items (block, tile pair), dealt round robin: 16 gate and 16 up columns of
+// the block's rows over all of K, the waves splitting the K chunks; their
+// sums meet in LDS in wave order, and the waves take turns finishing.  A wave
+// sees its chunks of all its items as one sequence and keeps D of them in
+// flight across the items' ends.
+template <typename Weights, int D, int kPerCU>
+__global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(const FewParams p) {
+  __shared__ GateUpSmem sm;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int g = lane >> 4;
+  const int blocks = find_blocks(p, sm);
+  if (blockIdx.x == 0) leave_plan(p, sm, blocks);
+  const int pairs = p.I / kRowTile;
+  const int total = blocks * pairs, grid = gridDim.x;
+  if ((int)blockIdx.x >= total) return;
+  const int items = (total - 1 - (int)blockIdx.x) / grid + 1;
+  const int KC = p.KC1;
+  const int c0 = (int)((int64_t)wave * KC / kFewWaves);
+  const int share = (int)((int64_t)(wave + 1) * KC / kFewWaves) - c0;
+  const int nc = max(share, 1);                         // a wave without a chunk multiplies one by zeros
+  const gptr_t xbase = uniform_ptr(p.x);
+  const Weights weights;
+
+  // the chunk to load next
+  gptr_t wbase[2], sbase[2], xrow;
+  bool on;
+  int next = 0, next_item = blockIdx.x;
+  auto seek = [&](int item) {
+    const int b = item / pairs, pair = item - b * pairs;
+    const int expert = __builtin_amdgcn_readfirstlane(sm.expert[b]);
+    on = (lane & 15) < (int)sm.count[b];
+    const int slot = on ? sm.row[b][lane & 15] : 0;
+    xrow = xbase + (int64_t)(slot / p.topk) * p.H * 2 + g * 64;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t tile = (int64_t)expert * (p.I / 8) + 2 * pair + r;
+      wbase[r] = uniform_ptr(p.w1 + tile * KC * (kWave * 16));
+      sbase[r] = uniform_ptr(p.s1 + tile * Weights::scale_tile_bytes(KC));
+    }
+    on = on && share > 0;
+  };
+  u32x4_t w[D][2];
+  uint32_t sw[D][2];
+  bf16x8_t x[D][4];
+  auto issue = [&](auto st_) {
+    constexpr int st = decltype(st_)::value;
+    const int c = c0 + next;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      w[st][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16) + lane * 16);
+      sw[st][r] = Weights::load_scale(sbase[r], c, lane);
+    }
+    load_rows(xrow, c, on && c * kChunk + g * kGroup < p.H, x[st]);
+    __builtin_amdgcn_sched_barrier(0);
+    if (++next == nc) {                                 // past the last item its chunks come again, not used
+      next = 0;
+      next_item += grid;
+      if (next_item < total) seek(next_item);
+    }
+  };
+
+  f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  int c = 0, n = 0;
+  // the item's last chunk is done: two buffers and one barrier an item (the
+  // buffer written here was last read before the previous item's barrier)
+  auto finish = [&]() {
+    f32x4_t (&red)[kFewWaves][2][kWave] = sm.red[n & 1];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      red[wave][r][lane] = acc[r];
+      acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    lds_barrier();
+    if (wave != n % kFewWaves) return;
+    const int item = blockIdx.x + n * grid;
+    const int b = item / pairs, pair = item - b * pairs;
+    if ((lane & 15) >= (int)sm.count[b]) return;
+    const int slot = sm.row[b][lane & 15];
+    f32x4_t gu[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      gu[r] = red[0][r][lane];
+#pragma unroll
+      for (int v = 1; v < kFewWaves; ++v) gu[r] += red[v][r][lane];
+    }
+    // one rounding, to the bf16 the down product's operand holds
+    uint2 o;
+    o.x = pack_bf16x2(silu_mul(gu[0][0], gu[1][0]), silu_mul(gu[0][1], gu[1][1]));
+    o.y = pack_bf16x2(silu_mul(gu[0][2], gu[1][2]), silu_mul(gu[0][3], gu[1][3]));
+    *reinterpret_cast<uint2*>(p.h + (int64_t)slot * p.I + pair * kRowTile + 4 * g) = o;
+  };
+  seek(blockIdx.x);
+  {
+    int st = 0;
+    ring_loop<D>([&](auto st_) {
+      issue(st_);
+      return ++st == D;
+    });
+  }
+  ring_loop<D>([&](auto st_) {
+    constexpr int st = decltype(st_)::value;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      bf16x8_t A[4];
+      weights.operands(w[st][r], sw[st][r], c0 + c, A);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], x[st][j], acc[r], 0, 0, 0);
+    }
+    issue(st_);
+    if (++c == nc) {
+      c = 0;
+      finish();
+      if (++n == items) return true;
+    }
+    return false;
+  });
+}
+
+// ------------------------------------------------------------ down
+
+// Workgroup n: 16 output columns of every token.  The (block, K chunk) units
+// of all blocks are split evenly over the waves, which keep D of theirs in
+// flight; a wave adds each of its blocks' rows, times the row's weight, to
+// its totals (token t in column t % 16 of total t / 16), and the waves'
+// totals meet in LDS in wave order.
+template <typename Weights, int MT, int D>
+__global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParams p) {
+  __shared__ f32x4_t red[kFewWaves][MT][kWave];
+  const int nt = blockIdx.x;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int KC = p.KC2;
-  const int64_t units = (int64_t)blocks * KC;
+  const int64_t units = (int64_t)*p.blocks * KC;
   const int u0 = (int)(wave * units / kFewWaves), u1 = (int)((wave + 1) * units / kFewWaves);
   const int g = lane >> 4, col = lane & 15;
   const gptr_t hbase = uniform_ptr(p.h);
@@ -252,59 +344,91 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(const FewParams p
   f32x4_t tot[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) tot[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int ub = u0; ub < u1; ub += KB) {
-    u32x4_t w[KB];
-    uint32_t sw[KB];
-    FewRow row[KB];
-    int chunk[KB];
-    bf16x8_t x[KB][4];
-#pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      const int u = min(ub + i, u1 - 1);               // past u1: a repeated load, not used
-      const int blk = u / KC;
-      chunk[i] = u - blk * KC;
-      const int s = __builtin_amdgcn_readfirstlane(sm.list[blk]);
-      const int64_t tile = (int64_t)(p.topk_ids[s] - p.first) * (p.H / kRowTile) + nt;
-      w[i] = gload_u32x4(uniform_ptr(p.w2 + (tile * KC + chunk[i]) * (kWave * 16)) + lane * 16);
-      sw[i] = Weights::load_scale(uniform_ptr(p.s2 + tile * Weights::scale_tile_bytes(KC)), chunk[i], lane);
-      row[i] = p.rows[s * 16 + col];
+  if (u0 < u1) {
+    // the unit to load next, and the block after its own (read ahead: its
+    // rows' addresses hang on it)
+    const int last = (u1 - 1) / KC;
+    int blk = u0 / KC, next = u0 - blk * KC;
+    gptr_t wbase, sbase, hrow;
+    FewRow row = p.rows[blk * 16 + col], row_ahead;
+    int expert = p.experts[blk], expert_ahead;
+    auto seek = [&]() {                                 // blk, row and expert are set
+      const int64_t tile = (int64_t)__builtin_amdgcn_readfirstlane(expert) * (p.H / kRowTile) + nt;
+      wbase = uniform_ptr(p.w2 + tile * KC * (kWave * 16));
+      sbase = uniform_ptr(p.s2 + tile * Weights::scale_tile_bytes(KC));
+      hrow = hbase + (int64_t)max(row.slot, 0) * p.I * 2 + g * 64;
+      const int a = min(blk + 1, last);
+      row_ahead = p.rows[a * 16 + col];
+      expert_ahead = p.experts[a];
+    };
+    u32x4_t w[D];
+    uint32_t sw[D];
+    FewRow rows[D];
+    bf16x8_t x[D][4];
+    auto issue = [&](auto st_) {
+      constexpr int st = decltype(st_)::value;
+      __builtin_amdgcn_sched_barrier(0);
+      w[st] = gload_u32x4(wbase + (int64_t)next * (kWave * 16) + lane * 16);
+      sw[st] = Weights::load_scale(sbase, next, lane);
+      load_rows(hrow, next, row.slot >= 0 && next * kChunk + g * kGroup < p.I, x[st]);
+      rows[st] = row;
+      __builtin_amdgcn_sched_barrier(0);
+      if (++next == KC) {                               // past the last block its chunks come again, not used
+        next = 0;
+        if (blk < last) {
+          ++blk;
+          row = row_ahead;
+          expert = expert_ahead;
+          seek();
+        }
+      }
+    };
+    seek();
+    {
+      int st = 0;
+      ring_loop<D>([&](auto st_) {
+        issue(st_);
+        return ++st == D;
+      });
     }
-#pragma unroll
-    for (int i = 0; i < KB; ++i)
-      load_rows(hbase + (int64_t)max(row[i].slot, 0) * p.I * 2 + g * 64, chunk[i],
-                row[i].slot >= 0 && chunk[i] * kChunk + g * kGroup < p.I, x[i]);
-#pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      if (ub + i >= u1) break;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    int u = u0, c = u0 % KC;
+    ring_loop<D>([&](auto st_) {
+      constexpr int st = decltype(st_)::value;
       bf16x8_t A[4];
-      weights.operands(w[i], sw[i], chunk[i], A);
+      weights.operands(w[st], sw[st], c, A);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], x[i][j], acc, 0, 0, 0);
-      if (chunk[i] == KC - 1 || ub + i == u1 - 1) {     // the block's (or the wave's) last chunk
-        const int token = row[i].slot / p.topk;         // of this lane's column, where slot >= 0
-        const int rows = __popcll(__ballot(row[i].slot >= 0)) / 4;
-        for (int r = 0; r < rows; ++r) {                // valid rows come first
+      for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], x[st][j], acc, 0, 0, 0);
+      const FewRow mine = rows[st];
+      issue(st_);
+      ++u;
+      if (++c == KC || u == u1) {                       // the block's (or the wave's) last chunk
+        c = 0;
+        const int token = mine.slot / p.topk;           // of this lane's column, where slot >= 0
+        const int n = __popcll(__ballot(mine.slot >= 0)) / 4;
+        for (int r = 0; r < n; ++r) {                   // valid rows come first
           const int t = __builtin_amdgcn_readlane(token, r);
-          const float wt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, row[i].weight), r));
+          const float wt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine.weight), r));
           f32x4_t v;
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = __shfl(acc[q], 16 * g + r);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
-            if (m == t / 16 && col == t % 16) tot[m] += wt * v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tot[m][q] += m == t / 16 && col == t % 16 ? wt * v[q] : 0.f;
         }
         acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-    }
+      return u == u1;
+    });
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) sm.red[wave][m][lane] = tot[m];
+  for (int m = 0; m < MT; ++m) red[wave][m][lane] = tot[m];
   __syncthreads();
   if (wave >= MT) return;
-  f32x4_t y = sm.red[0][wave][lane];
+  f32x4_t y = red[0][wave][lane];
 #pragma unroll
-  for (int v = 1; v < kFewWaves; ++v) y += sm.red[v][wave][lane];
+  for (int v = 1; v < kFewWaves; ++v) y += red[v][wave][lane];
   const int t = 16 * wave + col;
   if (t >= p.T) return;
   uint2 o;
@@ -315,16 +439,20 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(const FewParams p
 
 template <typename Weights>
 hipError_t launch_kind(const FewParams& p, hipStream_t stream) {
-  const dim3 up(p.I / kRowTile, p.T * p.topk), down(p.H / kRowTile), block(kFewThreads);
-  hipLaunchKernelGGL(few_gate_up_kernel<Weights>, up, block, 0, stream, p);
+  const int64_t items = (int64_t)p.I / kRowTile * p.T * p.topk;
+  const dim3 up((unsigned)std::min<int64_t>(items, kFewGroups)), down(p.H / kRowTile), block(kFewThreads);
+  if (items <= kFewGroups / 2)
+    hipLaunchKernelGGL((few_gate_up_kernel<Weights, 7, 1>), up, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((few_gate_up_kernel<Weights, 3, 2>), up, block, 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.T <= 16)
-    hipLaunchKernelGGL((few_down_kernel<Weights, 1>), down, block, 0, stream, p);
+    hipLaunchKernelGGL((few_down_kernel<Weights, 1, 3>), down, block, 0, stream, p);
   else if (p.T <= 32)
-    hipLaunchKernelGGL((few_down_kernel<Weights, 2>), down, block, 0, stream, p);
+    hipLaunchKernelGGL((few_down_kernel<Weights, 2, 3>), down, block, 0, stream, p);
   else
-    hipLaunchKernelGGL((few_down_kernel<Weights, 4>), down, block, 0, stream, p);
+    hipLaunchKernelGGL((few_down_kernel<Weights, 4, 3>), down, block, 0, stream, p);
   return hipGetLastError();
 }
 

@@ -181,8 +181,10 @@ struct FewParams {
   int32_t T, topk, first, E;              // experts [first, first + E) are held here
   int32_t H, I, KC1, KC2;                 // hidden and intermediate width, their 128-wide chunks
   uint16_t* h;                            // [T * topk][I], rows of local slots
-  FewRow* rows;                           // [T * topk][16], the rows of blocks that lead
-  int32_t* leader;                        // [T * topk]: 1 where the slot leads a block
+  // left by the gate/up kernel for the down kernel: at most T * topk blocks
+  int32_t* blocks;                        // their number
+  int32_t* experts;                       // [blocks]
+  FewRow* rows;                           // [blocks][16]
   uint16_t* out;                          // [T][H]
 };
 hipError_t launch_few_tokens(bool mxfp4, const FewParams& p, hipStream_t stream);
