@@ -626,7 +626,7 @@ w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32
 
 #define W4A16_FEW_MAX_TOKENS 64
 #define W4A16_FEW_MAX_SLOTS 1024   /* T * topk */
-#define W4A16_FEW_MAX_EXPERTS 32767
+#define W4A16_FEW_MAX_EXPERTS 1024
 
 /* x bf16 [T, H] -> out bf16 [T, H],
  *   out[t] = sum over j with first_expert <= topk_ids[t][j] < first_expert + E

@@ -1074,21 +1074,22 @@ w4a16_status check_mx_rows(int64_t rows, int32_t K) {
   return W4A16_OK;
 }
 
-// ---- workspace of the few-token layer: [h, bf16 slots x I][rows][experts][blocks]
+// ---- workspace of the few-token layer: [h, bf16 slots x I][rows][plan][blocks]
 struct FewWorkspace {
-  size_t h = 0, rows = 0, experts = 0;
-  size_t total() const { return h + rows + experts + 256; }
+  size_t h = 0, rows = 0, plan = 0;
+  size_t total() const { return h + rows + plan + 256; }
 };
 
 FewWorkspace few_workspace(int32_t I, int32_t slots) {
   FewWorkspace w;
   w.h = al256((size_t)slots * I * 2);
   w.rows = al256((size_t)slots * 16 * sizeof(w4a16::FewRow));
-  w.experts = al256((size_t)slots * 4);
+  w.plan = al256((size_t)slots * sizeof(w4a16::FewBlock));
   return w;
 }
 
-static_assert(W4A16_FEW_MAX_TOKENS == w4a16::kFewMaxTokens && W4A16_FEW_MAX_SLOTS == w4a16::kFewMaxSlots,
+static_assert(W4A16_FEW_MAX_TOKENS == w4a16::kFewMaxTokens && W4A16_FEW_MAX_SLOTS == w4a16::kFewMaxSlots &&
+                  W4A16_FEW_MAX_EXPERTS == w4a16::kFewMaxExperts,
               "the header's limits are the kernels'");
 
 }  // namespace
@@ -1489,8 +1490,8 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
   p.KC2 = down->chunks;
   p.h = reinterpret_cast<uint16_t*>(base);
   p.rows = reinterpret_cast<w4a16::FewRow*>(base + ws.h);
-  p.experts = reinterpret_cast<int32_t*>(base + ws.h + ws.rows);
-  p.blocks = reinterpret_cast<int32_t*>(base + ws.h + ws.rows + ws.experts);
+  p.plan = reinterpret_cast<w4a16::FewBlock*>(base + ws.h + ws.rows);
+  p.blocks = reinterpret_cast<int32_t*>(base + ws.h + ws.rows + ws.plan);
   p.out = out;
   hipError_t e = w4a16::launch_few_tokens(mx, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "moe_few_tokens launch");

@@ -17,12 +17,12 @@
 // gfx950's v_cvt_scalef32_pk_bf16_fp4, exact (an E2M1 value times a power of
 // two is a bf16 number).
 //
-// Rows.  An expert's tokens are taken 16 at a time in token order; each such
-// block of rows is one MFMA operand, and its weights are read once.  A token
-// that lists an expert twice is one row whose weights add up.  Every
-// workgroup of the first kernel works the blocks out for itself from the ids
-// (in LDS, from one read of them), so no launch goes before it; workgroup 0
-// leaves them in the workspace for the second kernel.
+// Rows.  An expert's tokens are a 64-bit mask (at most 64 tokens), so a token
+// that lists an expert twice is one row, whose weights add up; the rows are
+// taken 16 at a time in token order, each such block is one MFMA operand, and
+// a block's weights are read once.  Every workgroup of the first kernel works
+// the blocks out for itself from the ids (one read of them, then LDS), so no
+// launch goes before it; it leaves them in the workspace for the second.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,8 +36,7 @@ namespace {
 
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kFewWaves * kWave;
-constexpr int kSlotWords = kFewMaxSlots / kWave;       // ballot words over the slots
-static_assert(kFewMaxSlots == 2 * kFewThreads, "two slots a thread");
+static_assert(kFewMaxSlots == 2 * kFewThreads && kFewMaxTokens <= 64, "two slots a thread, a bit a token");
 // workgroups of the gate/up kernel: two on each of 256 CUs
 constexpr int kFewGroups = 512;
 
@@ -83,92 +82,74 @@ __device__ __forceinline__ void load_rows(gptr_t row, int c, bool on, bf16x8_t (
 // ------------------------------------------------------------ gate / up
 
 struct GateUpSmem {
-  int16_t key[kFewMaxSlots];                            // local expert of each slot, -1 = none
-  unsigned long long lead[kSlotWords];                  // slots that start a block, one bit each
-  uint32_t count[kFewMaxSlots];                       // rows of each block
-  int16_t expert[kFewMaxSlots];                         // of each block
-  int16_t row[kFewMaxSlots][16];                        // slots of each block
+  unsigned long long tokens[kFewMaxExperts];            // of each expert held here, one bit each
+  uint32_t wave_sum[kFewWaves];
+  FewBlock block[kFewMaxSlots];
+  uint8_t count[kFewMaxSlots];                          // rows of each block
+  uint8_t token[kFewMaxSlots][16];                      // their tokens
   f32x4_t red[2][kFewWaves][2][kWave];
 };
 
-// The blocks of rows, from the ids: rank of a slot = tokens before it that
-// list its expert; a slot starts a block where its rank is a multiple of 16;
-// blocks are numbered by the slot that starts them.  Returns their number.
+// The blocks of rows, from the ids: numbered by expert, then by token.
+// Returns their number.
 __device__ __forceinline__ int find_blocks(const FewParams& p, GateUpSmem& sm) {
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int S = p.T * p.topk;
-  int key[2];
+  static_assert(kFewMaxExperts == 2 * kFewThreads, "two experts a thread");
+  int expert[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = tid + q * kFewThreads;
-    const int e = i < S ? p.topk_ids[i] - p.first : -1;
-    key[q] = (unsigned)e < (unsigned)p.E ? e : -1;
-    sm.key[i] = (int16_t)key[q];
-    sm.count[i] = 0;
+    expert[q] = i < S ? p.topk_ids[i] - p.first : -1;
+    sm.tokens[i] = 0;
   }
   __syncthreads();
-  int rank[2], start[2];                                // start: the slot that starts this slot's block
-  bool row[2];                                          // this slot is a row: local, the token's first of its expert
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int i = tid + q * kFewThreads;
-    rank[q] = 0;
-    start[q] = i;
-    row[q] = key[q] >= 0;
-    unsigned long long m = 0;
-    if (q * kFewThreads + wave * kWave < S) {           // wave-uniform
-      const int t = i / p.topk;
-      for (int u = 0, j = 0; u <= min(p.T - 1, (q * kFewThreads + wave * kWave + kWave - 1) / p.topk); ++u) {
-        int hit = -1;
-        for (int k = 0; k < p.topk; ++k, ++j)
-          if (sm.key[j] == key[q] && hit < 0) hit = j;
-        if (u == t && hit != i) row[q] = false;         // an earlier slot of the token stands for it
-        if (u < t && hit >= 0) {
-          if (rank[q] % 16 == 0) start[q] = hit;
-          ++rank[q];
-        }
-      }
-      if (rank[q] % 16 == 0) start[q] = i;
-      m = __ballot(row[q] && rank[q] % 16 == 0);
-    }
-    if (lane == 0) sm.lead[q * kFewWaves + wave] = m;
-  }
-  __syncthreads();
-  int blocks = 0;
-  for (int w = 0; w < kSlotWords; ++w) blocks += __popcll(sm.lead[w]);
 #pragma unroll
   for (int q = 0; q < 2; ++q)
-    if (row[q]) {
-      const int i = tid + q * kFewThreads;
-      int b = 0;
-      for (int w = 0; w < start[q] / kWave; ++w) b += __popcll(sm.lead[w]);
-      b += __popcll(sm.lead[start[q] / kWave] & ((1ull << (start[q] % kWave)) - 1ull));
-      sm.row[b][rank[q] % 16] = (int16_t)i;
-      atomicAdd(&sm.count[b], 1u);                    // a count: the order of the additions is nothing
-      if (start[q] == i) sm.expert[b] = (int16_t)key[q];
-    }
+    if ((unsigned)expert[q] < (unsigned)p.E)            // bits, not a sum: the order of the updates is nothing
+      atomicOr(&sm.tokens[expert[q]], 1ull << ((tid + q * kFewThreads) / p.topk));
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(blocks);
-}
-
-// The blocks for the down kernel: number, expert of each, and each row's
-// slot and weight (-1, 0 past a block's rows).
-__device__ __forceinline__ void leave_plan(const FewParams& p, const GateUpSmem& sm, int blocks) {
-  for (int i = threadIdx.x; i < blocks * 16; i += kFewThreads) {
-    const int b = i / 16, r = i % 16;
-    FewRow row{-1, 0.f};
-    if (r < (int)sm.count[b]) {
-      row.slot = sm.row[b][r];
-      const int j0 = row.slot - row.slot % p.topk;
-      for (int j = j0; j < j0 + p.topk; ++j)
-        if (sm.key[j] == sm.expert[b]) row.weight += p.topk_weights[j];
-    }
-    p.rows[i] = row;
-    if (r == 0) p.experts[b] = sm.expert[b];
+  // blocks (high half) and rows (low half) of the experts before this thread's two
+  unsigned long long mask[2];
+  uint32_t own[2], before = 0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    mask[q] = sm.tokens[2 * tid + q];
+    const uint32_t rows = __popcll(mask[q]);
+    own[q] = (rows + 15) / 16 << 16 | rows;
+    before += own[q];
   }
-  if (threadIdx.x == 0) *p.blocks = blocks;
+  const uint32_t both = before;
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const uint32_t v = __shfl_up(before, d);
+    if (lane >= d) before += v;
+  }
+  if (lane == kWave - 1) sm.wave_sum[wave] = before;
+  before -= both;
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) {
+    if (w < wave) before += sm.wave_sum[w];
+    total += sm.wave_sum[w];
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    int b = before >> 16, row = before & 0xFFFF;
+    unsigned long long m = mask[q];
+    for (int left = __popcll(m); left > 0; left -= 16, ++b) {
+      const int n = min(left, 16);
+      sm.block[b] = FewBlock{2 * tid + q, row};
+      sm.count[b] = (uint8_t)n;
+      for (int r = 0; r < n; ++r, ++row, m &= m - 1) sm.token[b][r] = (uint8_t)__builtin_ctzll(m);
+    }
+    before += own[q];
+  }
+  __syncthreads();
+  return (int)(__builtin_amdgcn_readfirstlane(total) >> 16);
 }
 
 // A barrier for LDS alone: the loads in flight for later chunks stay in
@@ -214,7 +195,7 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int g = lane >> 4;
   const int blocks = find_blocks(p, sm);
-  if (blockIdx.x == 0) leave_plan(p, sm, blocks);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.blocks = blocks;
   const int pairs = p.I / kRowTile;
   const int total = blocks * pairs, grid = gridDim.x;
   if ((int)blockIdx.x >= total) return;
@@ -232,10 +213,9 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
   int next = 0, next_item = blockIdx.x;
   auto seek = [&](int item) {
     const int b = item / pairs, pair = item - b * pairs;
-    const int expert = __builtin_amdgcn_readfirstlane(sm.expert[b]);
+    const int expert = __builtin_amdgcn_readfirstlane(sm.block[b].expert);
     on = (lane & 15) < (int)sm.count[b];
-    const int slot = on ? sm.row[b][lane & 15] : 0;
-    xrow = xbase + (int64_t)(slot / p.topk) * p.H * 2 + g * 64;
+    xrow = xbase + (int64_t)(on ? sm.token[b][lane & 15] : 0) * p.H * 2 + g * 64;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int64_t tile = (int64_t)expert * (p.I / 8) + 2 * pair + r;
@@ -280,8 +260,26 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
     if (wave != n % kFewWaves) return;
     const int item = blockIdx.x + n * grid;
     const int b = item / pairs, pair = item - b * pairs;
-    if ((lane & 15) >= (int)sm.count[b]) return;
-    const int slot = sm.row[b][lane & 15];
+    const int r = lane & 15;
+    const bool valid = r < (int)sm.count[b];
+    const FewBlock blk = sm.block[b];
+    if (pair == 0 && lane < 16) {
+      // the block for the down kernel: each row's token and its weight for the expert
+      FewRow row{-1, 0.f};
+      if (valid) {
+        row.token = sm.token[b][r];
+        const int32_t* ids = p.topk_ids + row.token * p.topk;
+        const float* wts = p.topk_weights + row.token * p.topk;
+#pragma unroll 4
+        for (int j = 0; j < p.topk; ++j) {
+          const float wt = wts[j];
+          row.weight += ids[j] - p.first == blk.expert ? wt : 0.f;
+        }
+      }
+      p.rows[b * 16 + r] = row;
+      if (lane == 0) p.plan[b] = blk;
+    }
+    if (!valid) return;
     f32x4_t gu[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -293,7 +291,7 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
     uint2 o;
     o.x = pack_bf16x2(silu_mul(gu[0][0], gu[1][0]), silu_mul(gu[0][1], gu[1][1]));
     o.y = pack_bf16x2(silu_mul(gu[0][2], gu[1][2]), silu_mul(gu[0][3], gu[1][3]));
-    *reinterpret_cast<uint2*>(p.h + (int64_t)slot * p.I + pair * kRowTile + 4 * g) = o;
+    *reinterpret_cast<uint2*>(p.h + (int64_t)(blk.h_row + r) * p.I + pair * kRowTile + 4 * g) = o;
   };
   seek(blockIdx.x);
   {
@@ -329,9 +327,18 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
 // flight; a wave adds each of its blocks' rows, times the row's weight, to
 // its totals (token t in column t % 16 of total t / 16), and the waves'
 // totals meet in LDS in wave order.
+constexpr int kStage = 16;                              // blocks staged at a time
+
+template <int MT>
+struct DownSmem {
+  FewRow rows[kFewWaves][kStage * 16];                  // of each wave's next blocks
+  FewBlock block[kFewWaves][kStage];
+  f32x4_t red[kFewWaves][MT][kWave];
+};
+
 template <typename Weights, int MT, int D>
 __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParams p) {
-  __shared__ f32x4_t red[kFewWaves][MT][kWave];
+  __shared__ DownSmem<MT> sm;
   const int nt = blockIdx.x;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -345,22 +352,32 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParam
 #pragma unroll
   for (int t = 0; t < MT; ++t) tot[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (u0 < u1) {
-    // the unit to load next, and the block after its own (read ahead: its
-    // rows' addresses hang on it)
     const int last = (u1 - 1) / KC;
-    int blk = u0 / KC, next = u0 - blk * KC;
+    int blk = u0 / KC, next = u0 - blk * KC;            // the unit to load next
+    int staged = blk;                                   // blocks [staged, staged + kStage) are in LDS
     gptr_t wbase, sbase, hrow;
-    FewRow row = p.rows[blk * 16 + col], row_ahead;
-    int expert = p.experts[blk], expert_ahead;
-    auto seek = [&]() {                                 // blk, row and expert are set
-      const int64_t tile = (int64_t)__builtin_amdgcn_readfirstlane(expert) * (p.H / kRowTile) + nt;
+    FewRow row;
+    // the wave's own part of LDS: its accesses stay in order, no barrier
+    auto stage = [&]() {
+      const int n = min(kStage, last + 1 - staged);
+      for (int i = lane; i < n * 16; i += kWave) sm.rows[wave][i] = p.rows[staged * 16 + i];
+      if (lane < n) sm.block[wave][lane] = p.plan[staged + lane];
+      __builtin_amdgcn_wave_barrier();
+    };
+    auto seek = [&]() {
+      if (blk == staged + kStage) {
+        staged = blk;
+        __builtin_amdgcn_wave_barrier();
+        stage();
+      }
+      row = sm.rows[wave][(blk - staged) * 16 + col];
+      const FewBlock block = sm.block[wave][blk - staged];
+      const int64_t tile = (int64_t)__builtin_amdgcn_readfirstlane(block.expert) * (p.H / kRowTile) + nt;
       wbase = uniform_ptr(p.w2 + tile * KC * (kWave * 16));
       sbase = uniform_ptr(p.s2 + tile * Weights::scale_tile_bytes(KC));
-      hrow = hbase + (int64_t)max(row.slot, 0) * p.I * 2 + g * 64;
-      const int a = min(blk + 1, last);
-      row_ahead = p.rows[a * 16 + col];
-      expert_ahead = p.experts[a];
+      hrow = hbase + (int64_t)(block.h_row + col) * p.I * 2 + g * 64;
     };
+    stage();
     u32x4_t w[D];
     uint32_t sw[D];
     FewRow rows[D];
@@ -370,15 +387,13 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParam
       __builtin_amdgcn_sched_barrier(0);
       w[st] = gload_u32x4(wbase + (int64_t)next * (kWave * 16) + lane * 16);
       sw[st] = Weights::load_scale(sbase, next, lane);
-      load_rows(hrow, next, row.slot >= 0 && next * kChunk + g * kGroup < p.I, x[st]);
+      load_rows(hrow, next, row.token >= 0 && next * kChunk + g * kGroup < p.I, x[st]);
       rows[st] = row;
       __builtin_amdgcn_sched_barrier(0);
       if (++next == KC) {                               // past the last block its chunks come again, not used
         next = 0;
         if (blk < last) {
           ++blk;
-          row = row_ahead;
-          expert = expert_ahead;
           seek();
         }
       }
@@ -404,10 +419,9 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParam
       ++u;
       if (++c == KC || u == u1) {                       // the block's (or the wave's) last chunk
         c = 0;
-        const int token = mine.slot / p.topk;           // of this lane's column, where slot >= 0
-        const int n = __popcll(__ballot(mine.slot >= 0)) / 4;
+        const int n = __popcll(__ballot(mine.token >= 0)) / 4;
         for (int r = 0; r < n; ++r) {                   // valid rows come first
-          const int t = __builtin_amdgcn_readlane(token, r);
+          const int t = __builtin_amdgcn_readlane(mine.token, r);
           const float wt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine.weight), r));
           f32x4_t v;
 #pragma unroll
@@ -423,12 +437,12 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParam
     });
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) red[wave][m][lane] = tot[m];
+  for (int m = 0; m < MT; ++m) sm.red[wave][m][lane] = tot[m];
   __syncthreads();
   if (wave >= MT) return;
-  f32x4_t y = red[0][wave][lane];
+  f32x4_t y = sm.red[0][wave][lane];
 #pragma unroll
-  for (int v = 1; v < kFewWaves; ++v) y += red[v][wave][lane];
+  for (int v = 1; v < kFewWaves; ++v) y += sm.red[v][wave][lane];
   const int t = 16 * wave + col;
   if (t >= p.T) return;
   uint2 o;

@@ -165,12 +165,18 @@ hipError_t launch_route(const void* logits, int dtype, int64_t row_stride, const
 // ---- a whole layer for a few tokens (few.hip)
 constexpr int kFewMaxTokens = 64;
 constexpr int kFewMaxSlots = 1024;        // T * topk
+constexpr int kFewMaxExperts = 1024;      // held here
 
-// one row of a block of an expert's rows: its slot (-1: none) and the token's
+// one row of a block of an expert's rows: its token (-1: none) and the token's
 // weight for the expert
 struct FewRow {
-  int32_t slot;
+  int32_t token;
   float weight;
+};
+
+// a block of at most 16 rows: its expert and the first of its rows of h
+struct FewBlock {
+  int32_t expert, h_row;
 };
 
 struct FewParams {
@@ -180,10 +186,10 @@ struct FewParams {
   const float* topk_weights;
   int32_t T, topk, first, E;              // experts [first, first + E) are held here
   int32_t H, I, KC1, KC2;                 // hidden and intermediate width, their 128-wide chunks
-  uint16_t* h;                            // [T * topk][I], rows of local slots
+  uint16_t* h;                            // [T * topk][I], blocks' rows one after another
   // left by the gate/up kernel for the down kernel: at most T * topk blocks
   int32_t* blocks;                        // their number
-  int32_t* experts;                       // [blocks]
+  FewBlock* plan;                         // [blocks]
   FewRow* rows;                           // [blocks][16]
   uint16_t* out;                          // [T][H]
 };
