@@ -39,6 +39,14 @@ constexpr int kFewThreads = kFewWaves * kWave;
 static_assert(kFewMaxSlots == 2 * kFewThreads && kFewMaxTokens <= 64, "two slots a thread, a bit a token");
 // workgroups of the gate/up kernel: two on each of 256 CUs
 constexpr int kFewGroups = 512;
+// The down kernel takes two column tiles a workgroup (a deeper ring, one
+// workgroup per CU, half the work a block costs besides its weights) where
+// that leaves most CUs a workgroup and each wave several units.  Measured on
+// MI355X, whole call, one / two tiles: 16 tokens on an INT4 EP8 share 93.8 /
+// 88.8 us, 37 x 16 on an MXFP4 share 278 / 264 us; but one token on a TP8
+// slice 19.4 / 22.9 us.
+constexpr int kFewWideDown = 192;
+constexpr int kFewWideUnits = 512;
 
 // ---- the two weight kinds: K chunk c of one packed 16-row tile
 
@@ -69,13 +77,25 @@ struct Mxfp4Weights {
 };
 
 // 32 bf16 of K chunk c for this lane (block g of the chunk) as four operand
-// words; zeros where `on` is false
-__device__ __forceinline__ void load_rows(gptr_t row, int c, bool on, bf16x8_t (&B)[4]) {
+// words.  Always four loads: a load that a lane or a branch may skip would
+// make the compiler count fewer loads in flight and wait too early.  Lanes
+// past the block's rows read its first row, which only reaches columns that
+// nothing reads; lanes past K (a ragged last chunk) read the row's start, and
+// clear_tail makes zeros of that before it is used.
+__device__ __forceinline__ void load_rows(gptr_t row, int c, int g, int K, bf16x8_t (&B)[4]) {
+  const int k = c * kChunk + g * kGroup;
+  const gptr_t p = row + (k < K ? k * 2 : 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) B[j] = __builtin_bit_cast(bf16x8_t, gload_u32x4(p + 16 * j));
+}
+
+__device__ __forceinline__ void clear_tail(int c, int g, int K, bf16x8_t (&B)[4]) {
+  if ((c + 1) * kChunk <= K) return;                    // the same for the whole wave
+  const bool in = c * kChunk + g * kGroup < K;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (on) v = gload_u32x4(row + (int64_t)c * (kChunk * 2) + 16 * j);
-    B[j] = __builtin_bit_cast(bf16x8_t, v);
+    const u32x4_t v = __builtin_bit_cast(u32x4_t, B[j]);
+    B[j] = __builtin_bit_cast(bf16x8_t, in ? v : u32x4_t{0u, 0u, 0u, 0u});
   }
 }
 
@@ -160,26 +180,15 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Calls step(0), step(1), ..., step(D - 1) over and over, the index a
-// compile-time constant (a ring of registers has no other), until one
-// returns true.
-template <int D, typename Step>
-__device__ __forceinline__ void ring_loop(Step&& step) {
-  for (;;) {
-    if (step(std::integral_constant<int, 0>{})) return;
-    if constexpr (D > 1)
-      if (step(std::integral_constant<int, 1>{})) return;
-    if constexpr (D > 2)
-      if (step(std::integral_constant<int, 2>{})) return;
-    if constexpr (D > 3)
-      if (step(std::integral_constant<int, 3>{})) return;
-    if constexpr (D > 4)
-      if (step(std::integral_constant<int, 4>{})) return;
-    if constexpr (D > 5)
-      if (step(std::integral_constant<int, 5>{})) return;
-    if constexpr (D > 6)
-      if (step(std::integral_constant<int, 6>{})) return;
-    static_assert(D <= 7, "ring depth");
+// step(0), step(1), ..., step(D - 1), the index a compile-time constant (a
+// ring of registers takes no other).  A loop over whole turns of the ring
+// with its only exit at the end: with an exit after every step the compiler
+// waited for all loads once a turn.
+template <int D, int I = 0, typename Step>
+__device__ __forceinline__ void ring_turn(Step&& step) {
+  if constexpr (I < D) {
+    step(std::integral_constant<int, I>{});
+    ring_turn<D, I + 1>(step);
   }
 }
 
@@ -203,26 +212,24 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
   const int KC = p.KC1;
   const int c0 = (int)((int64_t)wave * KC / kFewWaves);
   const int share = (int)((int64_t)(wave + 1) * KC / kFewWaves) - c0;
-  const int nc = max(share, 1);                         // a wave without a chunk multiplies one by zeros
+  const int nc = max(share, 1);                         // a wave without a chunk loads one and adds nothing
   const gptr_t xbase = uniform_ptr(p.x);
   const Weights weights;
 
   // the chunk to load next
   gptr_t wbase[2], sbase[2], xrow;
-  bool on;
   int next = 0, next_item = blockIdx.x;
   auto seek = [&](int item) {
     const int b = item / pairs, pair = item - b * pairs;
     const int expert = __builtin_amdgcn_readfirstlane(sm.block[b].expert);
-    on = (lane & 15) < (int)sm.count[b];
-    xrow = xbase + (int64_t)(on ? sm.token[b][lane & 15] : 0) * p.H * 2 + g * 64;
+    const int r = (lane & 15) < (int)sm.count[b] ? lane & 15 : 0;
+    xrow = xbase + (int64_t)sm.token[b][r] * p.H * 2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int64_t tile = (int64_t)expert * (p.I / 8) + 2 * pair + r;
       wbase[r] = uniform_ptr(p.w1 + tile * KC * (kWave * 16));
       sbase[r] = uniform_ptr(p.s1 + tile * Weights::scale_tile_bytes(KC));
     }
-    on = on && share > 0;
   };
   u32x4_t w[D][2];
   uint32_t sw[D][2];
@@ -236,7 +243,7 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
       w[st][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16) + lane * 16);
       sw[st][r] = Weights::load_scale(sbase[r], c, lane);
     }
-    load_rows(xrow, c, on && c * kChunk + g * kGroup < p.H, x[st]);
+    load_rows(xrow, c, g, p.H, x[st]);
     __builtin_amdgcn_sched_barrier(0);
     if (++next == nc) {                                 // past the last item its chunks come again, not used
       next = 0;
@@ -294,15 +301,11 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
     *reinterpret_cast<uint2*>(p.h + (int64_t)(blk.h_row + r) * p.I + pair * kRowTile + 4 * g) = o;
   };
   seek(blockIdx.x);
-  {
-    int st = 0;
-    ring_loop<D>([&](auto st_) {
-      issue(st_);
-      return ++st == D;
-    });
-  }
-  ring_loop<D>([&](auto st_) {
-    constexpr int st = decltype(st_)::value;
+  ring_turn<D>(issue);
+  for (int left = items * nc; left > 0; left -= D) ring_turn<D>([&](auto st_) {
+    constexpr int st = decltype(st_)::value;            // steps past the last chunk finish nothing
+    clear_tail(c0 + c, g, p.H, x[st]);
+    if (share > 0)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       bf16x8_t A[4];
@@ -313,49 +316,53 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
     issue(st_);
     if (++c == nc) {
       c = 0;
-      finish();
-      if (++n == items) return true;
+      if (n < items) finish();
+      ++n;
     }
-    return false;
   });
 }
 
 // ------------------------------------------------------------ down
 
-// Workgroup n: 16 output columns of every token.  The (block, K chunk) units
-// of all blocks are split evenly over the waves, which keep D of theirs in
-// flight; a wave adds each of its blocks' rows, times the row's weight, to
+// Workgroup n: 16 NT output columns of every token.  The (block, K chunk)
+// units of all blocks are split evenly over the waves, which keep D of theirs
+// in flight; a wave adds each of its blocks' rows, times the row's weight, to
 // its totals (token t in column t % 16 of total t / 16), and the waves'
 // totals meet in LDS in wave order.
 constexpr int kStage = 16;                              // blocks staged at a time
 
-template <int MT>
+template <int MT, int NT>
 struct DownSmem {
   FewRow rows[kFewWaves][kStage * 16];                  // of each wave's next blocks
   FewBlock block[kFewWaves][kStage];
-  f32x4_t red[kFewWaves][MT][kWave];
+  f32x4_t red[kFewWaves][NT * MT][kWave];
 };
 
-template <typename Weights, int MT, int D>
-__global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParams p) {
-  __shared__ DownSmem<MT> sm;
-  const int nt = blockIdx.x;
+template <typename Weights, int MT, int NT, int D, int kPerCU>
+__global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_down_kernel(const FewParams p) {
+  __shared__ DownSmem<MT, NT> sm;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int KC = p.KC2;
   const int64_t units = (int64_t)*p.blocks * KC;
   const int u0 = (int)(wave * units / kFewWaves), u1 = (int)((wave + 1) * units / kFewWaves);
   const int g = lane >> 4, col = lane & 15;
+  const int tiles = p.H / kRowTile;
+  int nt[NT];                                           // a tile past H is the last one again, not stored
+#pragma unroll
+  for (int i = 0; i < NT; ++i) nt[i] = min(NT * (int)blockIdx.x + i, tiles - 1);
   const gptr_t hbase = uniform_ptr(p.h);
   const Weights weights;
-  f32x4_t tot[MT];
+  f32x4_t tot[NT][MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) tot[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) tot[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (u0 < u1) {
     const int last = (u1 - 1) / KC;
     int blk = u0 / KC, next = u0 - blk * KC;            // the unit to load next
     int staged = blk;                                   // blocks [staged, staged + kStage) are in LDS
-    gptr_t wbase, sbase, hrow;
+    gptr_t wbase[NT], sbase[NT], hrow;
     FewRow row;
     // the wave's own part of LDS: its accesses stay in order, no barrier
     auto stage = [&]() {
@@ -372,22 +379,28 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParam
       }
       row = sm.rows[wave][(blk - staged) * 16 + col];
       const FewBlock block = sm.block[wave][blk - staged];
-      const int64_t tile = (int64_t)__builtin_amdgcn_readfirstlane(block.expert) * (p.H / kRowTile) + nt;
-      wbase = uniform_ptr(p.w2 + tile * KC * (kWave * 16));
-      sbase = uniform_ptr(p.s2 + tile * Weights::scale_tile_bytes(KC));
-      hrow = hbase + (int64_t)(block.h_row + col) * p.I * 2 + g * 64;
+      const int64_t tile0 = (int64_t)__builtin_amdgcn_readfirstlane(block.expert) * tiles;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        wbase[i] = uniform_ptr(p.w2 + (tile0 + nt[i]) * KC * (kWave * 16));
+        sbase[i] = uniform_ptr(p.s2 + (tile0 + nt[i]) * Weights::scale_tile_bytes(KC));
+      }
+      hrow = hbase + (int64_t)(block.h_row + (row.token >= 0 ? col : 0)) * p.I * 2;
     };
     stage();
-    u32x4_t w[D];
-    uint32_t sw[D];
+    u32x4_t w[D][NT];
+    uint32_t sw[D][NT];
     FewRow rows[D];
     bf16x8_t x[D][4];
     auto issue = [&](auto st_) {
       constexpr int st = decltype(st_)::value;
       __builtin_amdgcn_sched_barrier(0);
-      w[st] = gload_u32x4(wbase + (int64_t)next * (kWave * 16) + lane * 16);
-      sw[st] = Weights::load_scale(sbase, next, lane);
-      load_rows(hrow, next, row.token >= 0 && next * kChunk + g * kGroup < p.I, x[st]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        w[st][i] = gload_u32x4(wbase[i] + (int64_t)next * (kWave * 16) + lane * 16);
+        sw[st][i] = Weights::load_scale(sbase[i], next, lane);
+      }
+      load_rows(hrow, next, g, p.I, x[st]);
       rows[st] = row;
       __builtin_amdgcn_sched_barrier(0);
       if (++next == KC) {                               // past the last block its chunks come again, not used
@@ -399,56 +412,63 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewParam
       }
     };
     seek();
-    {
-      int st = 0;
-      ring_loop<D>([&](auto st_) {
-        issue(st_);
-        return ++st == D;
-      });
-    }
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    int u = u0, c = u0 % KC;
-    ring_loop<D>([&](auto st_) {
-      constexpr int st = decltype(st_)::value;
-      bf16x8_t A[4];
-      weights.operands(w[st], sw[st], c, A);
+    ring_turn<D>(issue);
+    f32x4_t acc[NT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], x[st][j], acc, 0, 0, 0);
+    for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    int u = u0, c = u0 % KC;
+    while (u < u1) ring_turn<D>([&](auto st_) {
+      constexpr int st = decltype(st_)::value;          // units past the last add nothing
+      clear_tail(c, g, p.I, x[st]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        bf16x8_t A[4];
+        weights.operands(w[st][i], sw[st][i], c, A);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], x[st][j], acc[i], 0, 0, 0);
+      }
       const FewRow mine = rows[st];
       issue(st_);
-      ++u;
+      if (++u > u1) return;
       if (++c == KC || u == u1) {                       // the block's (or the wave's) last chunk
         c = 0;
         const int n = __popcll(__ballot(mine.token >= 0)) / 4;
         for (int r = 0; r < n; ++r) {                   // valid rows come first
           const int t = __builtin_amdgcn_readlane(mine.token, r);
           const float wt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine.weight), r));
-          f32x4_t v;
+          f32x4_t v[NT];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = __shfl(acc[q], 16 * g + r);
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[i][q] = wt * __shfl(acc[i][q], 16 * g + r);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tot[m][q] += m == t / 16 && col == t % 16 ? wt * v[q] : 0.f;
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) tot[i][m][q] += 16 * m + col == t ? v[i][q] : 0.f;
         }
-        acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-      return u == u1;
     });
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) sm.red[wave][m][lane] = tot[m];
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sm.red[wave][i * MT + m][lane] = tot[i][m];
   __syncthreads();
-  if (wave >= MT) return;
+  if (wave >= NT * MT) return;                          // one wave for each (tile, 16 tokens)
   f32x4_t y = sm.red[0][wave][lane];
 #pragma unroll
   for (int v = 1; v < kFewWaves; ++v) y += sm.red[v][wave][lane];
-  const int t = 16 * wave + col;
-  if (t >= p.T) return;
+  const int t = 16 * (wave % MT) + col;
+  const int tile = NT * (int)blockIdx.x + wave / MT;
+  if (t >= p.T || tile >= tiles) return;
   uint2 o;
   o.x = pack_bf16x2(y[0], y[1]);
   o.y = pack_bf16x2(y[2], y[3]);
-  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + nt * kRowTile + 4 * g) = o;
+  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + tile * kRowTile + 4 * g) = o;
 }
 
 template <typename Weights>
@@ -461,12 +481,21 @@ hipError_t launch_kind(const FewParams& p, hipStream_t stream) {
     hipLaunchKernelGGL((few_gate_up_kernel<Weights, 3, 2>), up, block, 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (p.T <= 16)
-    hipLaunchKernelGGL((few_down_kernel<Weights, 1, 3>), down, block, 0, stream, p);
-  else if (p.T <= 32)
-    hipLaunchKernelGGL((few_down_kernel<Weights, 2, 3>), down, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((few_down_kernel<Weights, 4, 3>), down, block, 0, stream, p);
+  if (p.H / kRowTile >= 2 * kFewWideDown && (int64_t)p.T * p.topk * p.KC2 >= kFewWideUnits) {
+    const dim3 half((p.H / kRowTile + 1) / 2);
+    if (p.T <= 16)
+      hipLaunchKernelGGL((few_down_kernel<Weights, 1, 2, 6, 1>), half, block, 0, stream, p);
+    else if (p.T <= 32)
+      hipLaunchKernelGGL((few_down_kernel<Weights, 2, 2, 6, 1>), half, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((few_down_kernel<Weights, 4, 2, 5, 1>), half, block, 0, stream, p);
+  } else if (p.T <= 16) {
+    hipLaunchKernelGGL((few_down_kernel<Weights, 1, 1, 3, 2>), down, block, 0, stream, p);
+  } else if (p.T <= 32) {
+    hipLaunchKernelGGL((few_down_kernel<Weights, 2, 1, 3, 2>), down, block, 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((few_down_kernel<Weights, 4, 1, 3, 2>), down, block, 0, stream, p);
+  }
   return hipGetLastError();
 }
 
