@@ -197,7 +197,10 @@ __device__ __forceinline__ void ring_turn(Step&& step) {
 // sums meet in LDS in wave order, and the waves take turns finishing.  A wave
 // sees its chunks of all its items as one sequence and keeps D of them in
 // flight across the items' ends.
-template <typename Weights, int D, int kPerCU>
+// PARTS = 2 (few items): an item is half a pair, rows 8 h .. 8 h + 7 of the
+// gate and the up tile as the two halves of one operand, so twice as many
+// workgroups share the dequantisation.
+template <typename Weights, int PARTS, int D, int kPerCU>
 __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(const FewParams p) {
   __shared__ GateUpSmem sm;
   const int lane = threadIdx.x & (kWave - 1);
@@ -205,7 +208,8 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
   const int g = lane >> 4;
   const int blocks = find_blocks(p, sm);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.blocks = blocks;
-  const int pairs = p.I / kRowTile;
+  constexpr int R = 2 / PARTS;                          // operands a chunk
+  const int pairs = p.I / kRowTile * PARTS;             // items of a block
   const int total = blocks * pairs, grid = gridDim.x;
   if ((int)blockIdx.x >= total) return;
   const int items = (total - 1 - (int)blockIdx.x) / grid + 1;
@@ -217,31 +221,37 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
   const Weights weights;
 
   // the chunk to load next
-  gptr_t wbase[2], sbase[2], xrow;
-  int next = 0, next_item = blockIdx.x;
+  gptr_t wbase[R], sbase[R], xrow;
+  int half = 0, next = 0, next_item = blockIdx.x;
   auto seek = [&](int item) {
     const int b = item / pairs, pair = item - b * pairs;
     const int expert = __builtin_amdgcn_readfirstlane(sm.block[b].expert);
     const int r = (lane & 15) < (int)sm.count[b] ? lane & 15 : 0;
     xrow = xbase + (int64_t)sm.token[b][r] * p.H * 2;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t tile = (int64_t)expert * (p.I / 8) + 2 * pair + r;
+    for (int r = 0; r < R; ++r) {
+      const int64_t tile = (int64_t)expert * (p.I / 8) + 2 * (pair / PARTS) + r;
       wbase[r] = uniform_ptr(p.w1 + tile * KC * (kWave * 16));
       sbase[r] = uniform_ptr(p.s1 + tile * Weights::scale_tile_bytes(KC));
     }
+    half = pair % PARTS * 8;
   };
-  u32x4_t w[D][2];
-  uint32_t sw[D][2];
+  // this lane's row of the operand: its own of each tile, or row half + l % 8
+  // of the gate (l % 16 < 8) or the up tile, which follows it
+  const bool up = PARTS == 2 && (lane & 8);
+  const int64_t w_up = up ? (int64_t)KC * (kWave * 16) : 0, s_up = up ? Weights::scale_tile_bytes(KC) : 0;
+  u32x4_t w[D][R];
+  uint32_t sw[D][R];
   bf16x8_t x[D][4];
   auto issue = [&](auto st_) {
     constexpr int st = decltype(st_)::value;
     const int c = c0 + next;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      w[st][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16) + lane * 16);
-      sw[st][r] = Weights::load_scale(sbase[r], c, lane);
+    for (int r = 0; r < R; ++r) {
+      const int from = PARTS == 2 ? (lane & 0x37) + half : lane;
+      w[st][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16) + (w_up + from * 16));
+      sw[st][r] = Weights::load_scale(sbase[r] + s_up, c, from);
     }
     load_rows(xrow, c, g, p.H, x[st]);
     __builtin_amdgcn_sched_barrier(0);
@@ -252,14 +262,16 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
     }
   };
 
-  f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  f32x4_t acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   int c = 0, n = 0;
   // the item's last chunk is done: two buffers and one barrier an item (the
   // buffer written here was last read before the previous item's barrier)
   auto finish = [&]() {
     f32x4_t (&red)[kFewWaves][2][kWave] = sm.red[n & 1];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < R; ++r) {
       red[wave][r][lane] = acc[r];
       acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
@@ -286,19 +298,22 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
       p.rows[b * 16 + r] = row;
       if (lane == 0) p.plan[b] = blk;
     }
-    if (!valid) return;
+    // columns 4 g .. 4 g + 3 of gate and up; of half a pair: the gate's in
+    // lanes g = 0, 1 and the up's in g = 2, 3
+    if (!valid || (PARTS == 2 && g >= 2)) return;
     f32x4_t gu[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      gu[r] = red[0][r][lane];
+      const int from = lane + (PARTS == 2 ? 32 * r : 0), q = PARTS == 2 ? 0 : r;
+      gu[r] = red[0][q][from];
 #pragma unroll
-      for (int v = 1; v < kFewWaves; ++v) gu[r] += red[v][r][lane];
+      for (int v = 1; v < kFewWaves; ++v) gu[r] += red[v][q][from];
     }
     // one rounding, to the bf16 the down product's operand holds
     uint2 o;
     o.x = pack_bf16x2(silu_mul(gu[0][0], gu[1][0]), silu_mul(gu[0][1], gu[1][1]));
     o.y = pack_bf16x2(silu_mul(gu[0][2], gu[1][2]), silu_mul(gu[0][3], gu[1][3]));
-    *reinterpret_cast<uint2*>(p.h + (int64_t)(blk.h_row + r) * p.I + pair * kRowTile + 4 * g) = o;
+    *reinterpret_cast<uint2*>(p.h + (int64_t)(blk.h_row + r) * p.I + pair * (kRowTile / PARTS) + 4 * g) = o;
   };
   seek(blockIdx.x);
   ring_turn<D>(issue);
@@ -307,7 +322,7 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
     clear_tail(c0 + c, g, p.H, x[st]);
     if (share > 0)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < R; ++r) {
       bf16x8_t A[4];
       weights.operands(w[st][r], sw[st][r], c0 + c, A);
 #pragma unroll
@@ -475,10 +490,13 @@ template <typename Weights>
 hipError_t launch_kind(const FewParams& p, hipStream_t stream) {
   const int64_t items = (int64_t)p.I / kRowTile * p.T * p.topk;
   const dim3 up((unsigned)std::min<int64_t>(items, kFewGroups)), down(p.H / kRowTile), block(kFewThreads);
-  if (items <= kFewGroups / 2)
-    hipLaunchKernelGGL((few_gate_up_kernel<Weights, 7, 1>), up, block, 0, stream, p);
+  // halves of pairs where twice the items still fit one workgroup per CU:
+  // one token on a TP8 slice (128 items) 19.5 -> 18.3 us a call; 256 items
+  // 23.6 -> 29.2 us, so not there
+  if (items <= kFewGroups / 4)
+    hipLaunchKernelGGL((few_gate_up_kernel<Weights, 2, 7, 1>), dim3((unsigned)(2 * items)), block, 0, stream, p);
   else
-    hipLaunchKernelGGL((few_gate_up_kernel<Weights, 3, 2>), up, block, 0, stream, p);
+    hipLaunchKernelGGL((few_gate_up_kernel<Weights, 1, 3, 2>), up, block, 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.H / kRowTile >= 2 * kFewWideDown && (int64_t)p.T * p.topk * p.KC2 >= kFewWideUnits) {
