@@ -572,7 +572,7 @@ w4a16_status w4a16_mxfp4_dequant(const w4a16_weight_desc* desc, const void* pack
  * Masked: rows = E * max_m; a count masked_m[g] outside [0, max_m] is taken
  * as the nearer end; expected_m (host, > 0) only steers the tile choice.
  * Sizes: rows * K / 2 below 4 GiB (ERR_SHAPE).
- * Pointers: packed_w, packed_s, a_codes, out 16-byte aligned.
+ * Pointers: packed_w, packed_s, a_codes, out 16-byte aligned, a_scales 4.
  * Errors: ERR_ARG, ERR_LAYOUT (not an MXFP4 weight), ERR_SHAPE, ERR_HIP. */
 w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
                                             const uint8_t* a_codes, const uint8_t* a_scales, int64_t m_rows,

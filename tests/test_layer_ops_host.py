@@ -147,7 +147,7 @@ def test_grouped_mxfp4_refusals(L):
     assert c(m=0, a=None, s=None, idx=None, out=None) == 0
     assert c(m=-128) == -1 and c(m=64) == -2                             # segments start at multiples of 128
     assert c(a=None) == -1 and c(s=None) == -1 and c(idx=None) == -1 and c(out=None) == -1
-    assert c(a=P + 8) == -1 and c(out=P + 8) == -1
+    assert c(a=P + 8) == -1 and c(out=P + 8) == -1 and c(s=P + 2) == -1
     assert c(d=W.weight_desc(4, 64, 256)) == -3
     assert c(m=1 << 25) == -2                                            # 4 GiB of codes
     m = lambda d=d, a=P, mm=P, max_m=32, exp=8, out=P: L.w4a16_mxfp4_grouped_masked(

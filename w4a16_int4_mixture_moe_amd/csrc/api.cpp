@@ -1058,10 +1058,11 @@ namespace {
 
 // ---- checks the grouped MXFP4 calls share
 w4a16_status check_mx_grouped(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
-                              const uint8_t* a_codes, const uint16_t* out) {
+                              const uint8_t* a_codes, const uint8_t* a_scales, const uint16_t* out) {
   w4a16_status st = check_mx_desc(desc);
   if (st != W4A16_OK) return st;
   if (!packed_w || !packed_s) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (reinterpret_cast<uintptr_t>(a_scales) % 4) return fail(W4A16_ERR_ARG, "activation scales must be 4-byte aligned");
   if (!aligned16(packed_w) || !aligned16(packed_s) || !aligned16(a_codes) || !aligned16(out))
     return fail(W4A16_ERR_ARG, "packed weights, activation codes and output must be 16-byte aligned");
   return W4A16_OK;
@@ -1348,7 +1349,7 @@ w4a16_status w4a16_mxfp4_dequant(const w4a16_weight_desc* desc, const void* pack
 w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
                                             const uint8_t* a_codes, const uint8_t* a_scales, int64_t m_rows,
                                             const int32_t* m_indices, uint16_t* out, w4a16_stream_t stream) {
-  w4a16_status st = check_mx_grouped(desc, packed_w, packed_s, a_codes, out);
+  w4a16_status st = check_mx_grouped(desc, packed_w, packed_s, a_codes, a_scales, out);
   if (st != W4A16_OK) return st;
   if (m_rows < 0) return fail(W4A16_ERR_ARG, "m_rows < 0");
   if (m_rows > 0 && (!a_codes || !a_scales || !m_indices || !out)) return fail(W4A16_ERR_ARG, "NULL pointer argument");
@@ -1371,7 +1372,7 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
                                         const uint8_t* a_codes, const uint8_t* a_scales, int32_t max_m,
                                         const int32_t* masked_m, int32_t expected_m, uint16_t* out,
                                         w4a16_stream_t stream) {
-  w4a16_status st = check_mx_grouped(desc, packed_w, packed_s, a_codes, out);
+  w4a16_status st = check_mx_grouped(desc, packed_w, packed_s, a_codes, a_scales, out);
   if (st != W4A16_OK) return st;
   if (max_m <= 0) return fail(W4A16_ERR_ARG, "max_m must be positive");
   if (expected_m <= 0) return fail(W4A16_ERR_ARG, "expected_m must be positive");

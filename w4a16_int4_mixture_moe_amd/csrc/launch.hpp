@@ -151,6 +151,7 @@ hipError_t launch_mx_dequant(const uint32_t* pw, const uint8_t* ps, int32_t E, i
 // The grouped layouts (route kRouteContiguous or kRouteMasked), bf16 store;
 // m_tiles: 16-row token tiles per block (1, 2, 4 or 8)
 hipError_t launch_mx_grouped(int route, int m_tiles, const GemmParams& p, hipStream_t stream);
+hipError_t launch_mx_tile(int route, const GemmParams& p, hipStream_t stream);   // its 128-row tile (mx_tile.hip)
 // Indexed routing only; epilogue kEpiStore, kEpiWeighted or kEpiSiluMx.
 bool mx_gemm_config_supported(int epilogue, int m_tiles, int nr, int waves, int stages);
 hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stages, const GemmParams& p,

@@ -748,17 +748,18 @@ hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stag
 
 // ------------------------------------------------------------ grouped layouts
 
+// blocks of up to 64 rows; 128-row blocks run the tile of mx_tile.hip
 template <int ROUTE>
 static MxKernel pick_mx_grouped(int m_tiles) {
   if (m_tiles == 1) return mx_gemm_kernel<1, 4, 4, 4, kEpiStore, ROUTE>;
   if (m_tiles == 2) return mx_gemm_kernel<2, 4, 4, 4, kEpiStore, ROUTE>;
-  if (m_tiles == 4) return mx_gemm_kernel<4, 4, 4, 2, kEpiStore, ROUTE>;
-  return m_tiles == 8 ? mx_gemm_kernel<8, 4, 4, 2, kEpiStore, ROUTE> : nullptr;
+  return m_tiles == 4 ? mx_gemm_kernel<4, 4, 4, 2, kEpiStore, ROUTE> : nullptr;
 }
 
 hipError_t launch_mx_grouped(int route, int m_tiles, const GemmParams& p, hipStream_t stream) {
-  const MxKernel k = route == kRouteContiguous ? pick_mx_grouped<kRouteContiguous>(m_tiles)
-                                               : pick_mx_grouped<kRouteMasked>(m_tiles);
+  if (m_tiles == 8) return launch_mx_tile(route, p, stream);
+  if (route != kRouteMasked) return hipErrorInvalidValue;
+  const MxKernel k = pick_mx_grouped<kRouteMasked>(m_tiles);
   if (k == nullptr) return hipErrorInvalidValue;
   GemmParams q = p;
   q.n_tiles = (p.NT + 15) / 16;                        // 16 weight tiles per workgroup (4 waves x 4)
