@@ -23,6 +23,7 @@
 // instruction behind a wait for this wave's LDS reads: __syncthreads, or a
 // fence, would wait for every load (an LDS-DMA counts as a write to LDS).
 // Nothing is requested past the last chunk, so no DMA outlives the workgroup.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -37,6 +38,7 @@ constexpr int kMT = 8, kNR = 4, kNW = 4;            // token tiles, weight tiles
 constexpr int kTiles = kNR * kNW;                   // weight tiles per workgroup
 constexpr int kStages = 3;
 constexpr int kThreads = kNW * kWave;
+constexpr int kRun = 4, kRunMinBlocks = 64;
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
@@ -44,15 +46,21 @@ struct Stage {
   u32x4_t w[kTiles][kWave];                         // weight fragments
   u32x4_t x[kMT][kWave];                            // activation fragments
   uint8_t ws[kTiles][kWave];                        // weight scales, a byte per lane
-  uint32_t xs[16 * kMT];                            // activation scales, four blocks per row
 };
 
 struct TileSmemMx {
   Stage stage[kStages];
-  int row[16 * kMT];
-  int out[16 * kMT];
-  float w[16 * kMT];
+  union {                                           // activation scales
+    u32x4_t four[2][16 * kMT];                      // a row's 16 bytes of four chunks, two groups of chunks
+    uint32_t one[kStages][kNW][kWave];              // a row's 4 bytes of a chunk: 32 rows a wave (and 32 copies)
+  } xs;
+  union {
+    int row[16 * kMT];                              // activation row per block row, -1 = padding
+    int out[16 * kMT];                              // output row: the same in both grouped layouts
+  };
 };
+// two workgroups fit the 160 KB of a CU in its units of 1280 bytes
+static_assert((sizeof(TileSmemMx) + 1279) / 1280 * 1280 * 2 <= 160 * 1024, "two workgroups per CU");
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
@@ -76,13 +84,17 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// LDS-DMA instructions a wave issues per chunk: 4 weight fragments, 2
-// activation fragments, 4 tiles' scales, 64 rows' scales
-constexpr int kLoads = kTiles / kNW + kMT / kNW + 2;
-
-template <int NA>
+// FOUR: K is a multiple of 512, and a row's scales come 16 bytes (four
+// chunks) at a time: every row is a cache line of its own to the address
+// unit, and fetched chunk by chunk they kept it busier (82 % of the time) than
+// everything else together.
+template <int NA, bool FOUR>
 __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& sm, int expert, int nt,
                                               f32x4_t (&acc)[kNR][kMT]) {
+  // LDS-DMA instructions a wave issues per chunk: 4 weight fragments, 1 or 2
+  // activation fragments, 4 tiles' scales (and, not FOUR, 32 rows' scales)
+  constexpr int XF = (NA + kNW - 1) / kNW;
+  constexpr int kLoads = kNR + XF + 1 + (FOUR ? 0 : 1);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int KC = p.KC;
@@ -102,16 +114,17 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
                        ((int64_t)expert * p.w_tiles + min(nt * kTiles + 4 * wave + (lane >> 4), p.NT - 1)) * KC * kWave +
                        4 * (lane & 15);
   const gptr_t xbase = uniform_ptr(p.a);
-  uint32_t xoff[kMT / kNW];
+  uint32_t xoff[XF];
 #pragma unroll
-  for (int i = 0; i < kMT / kNW; ++i)
+  for (int i = 0; i < XF; ++i)
     xoff[i] = row_of(16 * (wave + kNW * i) + (lane & 15)) * kb + 16u * (uint32_t)(lane >> 4);
   const gptr_t xsbase = uniform_ptr(p.a_scale);
-  // 64 rows' scales a wave, so each half is fetched twice (the same bytes to
-  // the same place): masking half the lanes off would end the basic block, and
-  // the compiler then sinks every MFMA of the loop behind its last barrier
-  const int xsrow = 64 * (wave & 1);
-  const uint32_t xsoff = row_of(xsrow + lane) * ks;
+  // no lane or wave is masked off in the loop: a branch there would end its
+  // basic block, and the compiler then sinks the MFMAs behind the last
+  // barrier.  So waves 2 and 3 fetch the 64 rows' groups of waves 0 and 1
+  // again, and the upper half of a wave copies of its first row's dword.
+  const int xs0 = FOUR ? 64 * (wave & 1) : 32 * wave;
+  const uint32_t xsoff = row_of(FOUR ? xs0 + lane : xs0 + (lane < 32 ? lane : 0)) * ks;
 
   auto issue = [&](int c, int slot) {
     Stage& s = sm.stage[slot];
@@ -119,11 +132,14 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
     for (int i = 0; i < kNR; ++i)
       dma16(wsrc[i] + (int64_t)c * (kWave * 16) + lane * 16, (lds_ptr_t)&s.w[wave + kNW * i][0]);
 #pragma unroll
-    for (int i = 0; i < kMT / kNW; ++i) dma16(xbase + (int64_t)c * 64 + xoff[i], (lds_ptr_t)&s.x[wave + kNW * i][0]);
+    for (int i = 0; i < XF; ++i) dma16(xbase + (int64_t)c * 64 + xoff[i], (lds_ptr_t)&s.x[wave + kNW * i][0]);
     dma4(wssrc + (int64_t)c * kWave, (lds_ptr_t)&s.ws[4 * wave][0]);
-    dma4(xsbase + (int64_t)c * 4 + xsoff, (lds_ptr_t)&s.xs[xsrow]);
+    if constexpr (!FOUR) dma4(xsbase + (int64_t)c * 4 + xsoff, (lds_ptr_t)&sm.xs.one[slot][wave][0]);
   };
-  auto compute = [&](int slot) {
+  auto issue_four = [&](int group) {
+    dma16(xsbase + (int64_t)min(group, KC / 4 - 1) * 16 + xsoff, (lds_ptr_t)&sm.xs.four[group & 1][xs0]);
+  };
+  auto compute = [&](int c, int slot) {
     const Stage& s = sm.stage[slot];
     u32x4_t A[kNR];
     uint32_t as[kNR];
@@ -132,7 +148,11 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
       A[r] = s.w[kNR * wave + r][lane];
       as[r] = s.ws[kNR * wave + r][lane];
     }
-    const uint8_t* xs = reinterpret_cast<const uint8_t*>(&s.xs[0]) + 4 * (lane & 15) + (lane >> 4);
+    // the scale byte of (row 16 t + l % 16, block l / 16)
+    const uint8_t* xs = FOUR ? reinterpret_cast<const uint8_t*>(&sm.xs.four[(c >> 2) & 1][lane & 15]) + 4 * (c & 3)
+                             : reinterpret_cast<const uint8_t*>(&sm.xs.one[slot][0][lane & 15]);
+    xs += lane >> 4;
+    auto xs_at = [&](int t) { return FOUR ? 256 * t : 256 * (t / 2) + 64 * (t % 2); };
     u32x4_t B = s.x[0][lane];
     uint32_t bs = xs[0];
 #pragma unroll
@@ -141,7 +161,7 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
       uint32_t bn = bs;
       if (t + 1 < NA) {
         Bn = s.x[t + 1][lane];
-        bn = xs[64 * (t + 1)];
+        bn = xs[xs_at(t + 1)];
       }
       const i32x8_t b = {(int)B[0], (int)B[1], (int)B[2], (int)B[3], 0, 0, 0, 0};
 #pragma unroll
@@ -156,45 +176,81 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
   };
 
   static_assert(kStages == 3, "the waits below keep one later chunk in flight");
+  auto after = [](int slot) { return slot == kStages - 1 ? 0 : slot + 1; };
+  if constexpr (FOUR) issue_four(0);
   issue(0, 0);
   if (KC > 1) issue(1, 1);
-  // chunk c: landed; its buffer's predecessor free; ask for chunk c + 2; multiply
-  auto step = [&](int c, int slot, int ahead) {
-    wait_loads<kLoads>();
+  int c = 0, slot = 0;
+  // Chunk c has landed and its predecessor's buffer is free: fill that with
+  // chunk c + 2, multiply.  newer: this wave's loads issued after chunk c's.
+  auto step = [&](auto newer, auto group) {
+    wait_loads<decltype(newer)::value>();
     lds_barrier();
-    issue(c + 2, ahead);
+    if constexpr (decltype(group)::value) issue_four(c / 4 + 1);
+    issue(c + 2, after(after(slot)));
     __builtin_amdgcn_sched_barrier(0);
-    compute(slot);
+    compute(c, slot);
+    ++c;
+    slot = after(slot);
   };
-  int c = 0;
-  for (; c + 4 < KC; c += 3) {
-    step(c, 0, 2);
-    step(c + 1, 1, 0);
-    step(c + 2, 2, 1);
-  }
-  // at most four chunks are left, c is a multiple of 3; the last two ask for nothing
-  for (int slot = 0; c < KC; ++c, slot = slot == 2 ? 0 : slot + 1) {
-    if (c + 1 < KC)
-      wait_loads<kLoads>();
-    else
-      wait_loads<0>();
+  auto last = [&](auto newer) {
+    wait_loads<decltype(newer)::value>();
     lds_barrier();
-    if (c + 2 < KC) issue(c + 2, slot == 0 ? 2 : slot - 1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(slot);
+    compute(c, slot);
+    ++c;
+    slot = after(slot);
+  };
+  using N0 = std::integral_constant<int, 0>;
+  using N1 = std::integral_constant<int, kLoads>;
+  using N2 = std::integral_constant<int, kLoads + 1>;   // and the next four chunks' scales, one step old
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if constexpr (FOUR) {                             // KC is a multiple of 4
+    for (; c + 4 < KC;) {
+      step(N1{}, Yes{});
+      step(N2{}, No{});
+      step(N1{}, No{});
+      step(N1{}, No{});
+    }
+    step(N1{}, Yes{});                              // the last group's scales again, so that the count holds
+    step(N2{}, No{});
+    last(N1{});
+    last(N0{});
+  } else {
+    for (; c + 2 < KC;) step(N1{}, No{});
+    if (c + 1 < KC) last(N1{});
+    last(N0{});
   }
+}
+
+// Workgroup w -> block and N tile.  p.xcd_group = G > 0: runs of G blocks x
+// all N tiles share an XCD (workgroups go to the eight XCDs in turn), the
+// blocks of a run next to each other for each N tile, so that an expert's
+// consecutive blocks read a weight tile from HBM once and its rows stay in
+// one L2.  0: block after block.
+__device__ __forceinline__ void item_of(const GemmParams& p, int w, int& mb, int& nt) {
+  if (p.xcd_group == 0) {
+    mb = w / p.n_tiles;
+    nt = w - mb * p.n_tiles;
+    return;
+  }
+  const int per = p.xcd_group * p.n_tiles, k = w >> 3;
+  const int run = k / per, r = k - run * per;
+  nt = r / p.xcd_group;
+  mb = (run * 8 + (w & 7)) * p.xcd_group + (r - nt * p.xcd_group);
 }
 
 template <int ROUTE>
 __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const GemmParams p) {
   __shared__ __attribute__((aligned(16))) TileSmemMx sm;
   int mb, nt;
-  if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
+  item_of(p, blockIdx.x, mb, nt);
+  if (mb >= p.grid_blocks) return;
   const int expert = setup_rows<kMT, kNW, ROUTE, kEpiStore>(p, mb, sm);
   if (expert < 0) return;
   __syncthreads();
   const uint32_t tmask = active_tiles<kMT>(sm);
-  // token tiles run: the active prefix rounded up to an even count (an extra
+  // token tiles run: the active prefix, above one rounded up to an even count (an extra
   // tile of padding rows reads a valid row and is never stored)
   auto go = [&](auto na) {
     constexpr int NA = decltype(na)::value;
@@ -203,11 +259,15 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const GemmParams p
     for (int r = 0; r < kNR; ++r)
 #pragma unroll
       for (int t = 0; t < kMT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    tile_mainloop<NA>(p, sm, expert, nt, acc);
+    if (p.KC % 4 == 0)
+      tile_mainloop<NA, true>(p, sm, expert, nt, acc);
+    else
+      tile_mainloop<NA, false>(p, sm, expert, nt, acc);
     epilogue<kMT, kNR, kNW, kEpiStore>(p, sm, nt, (1u << NA) - 1u, acc);
   };
   const int na = 32 - __clz(tmask);
-  if (na <= 2) go(std::integral_constant<int, 2>{});
+  if (na <= 1) go(std::integral_constant<int, 1>{});
+  else if (na <= 2) go(std::integral_constant<int, 2>{});
   else if (na <= 4) go(std::integral_constant<int, 4>{});
   else if (na <= 6) go(std::integral_constant<int, 6>{});
   else go(std::integral_constant<int, 8>{});
@@ -218,8 +278,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const GemmParams p
 hipError_t launch_mx_tile(int route, const GemmParams& p, hipStream_t stream) {
   GemmParams q = p;
   q.n_tiles = (p.NT + kTiles - 1) / kTiles;
-  q.xcd_group = 0;
-  const int64_t grid = grid_of(q, q.n_tiles);
+  q.xcd_group = p.grid_blocks >= kRunMinBlocks ? kRun : 0;
+  const int64_t run = 8 * (int64_t)std::max(q.xcd_group, 1);
+  const int64_t grid = (q.xcd_group ? (p.grid_blocks + run - 1) / run * run : p.grid_blocks) * q.n_tiles;
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
   if (route == kRouteContiguous)
