@@ -409,7 +409,9 @@ def _grouped_check(got, rows, experts, a, w, what):
 
 
 CONTIGUOUS = [((1,), 1, 16, 128), ((128, 0, 5), 4, 208, 256), ((129, 300, 0, 17, 64), 5, 1040, 640),
-              ((40, 256, 384), 3, 512, 384), ((1000,), 1, 768, 1152)]
+              ((40, 256, 384), 3, 512, 384), ((1000,), 1, 768, 1152),
+              # 256-row blocks: odd and even numbers of 128-row blocks, halves that end early
+              ((700, 130, 257, 128), 4, 272, 512), ((1500,), 1, 96, 1024), ((256, 0, 385, 640, 1, 900), 6, 528, 512)]
 
 
 @pytest.mark.parametrize("counts,E,N,K", CONTIGUOUS)
@@ -456,6 +458,25 @@ def test_grouped_masked(counts, max_m, expected, E, N, K):
     out = torch.full((E * max_m + 1, N), 2.0, dtype=torch.bfloat16, device=dev())
     M.grouped_mxfp4_masked(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array(counts, np.int32)), expected, out=out)
     _grouped_check(bits(out), [i for i, _ in live], [g for _, g in live], a, w, f"masked {counts} N={N} K={K}")
+
+
+def test_grouped_contiguous_long_runs_and_split_segments():
+    """More than 512 blocks of one expert in a row, then two segments of one
+    expert next to each other, the first ending inside a block."""
+    packed, w = _mx_weight(2, 32, 512, 12)
+    idx = [0] * (128 * 515 + 5) + [-1] * 123 + [1] * 130 + [-1] * 126 + [1] * 200 + [-1] * 56 + [1] * 3 + [-1] * 125
+    c, s, a = _mx_rows(len(idx), 512, 4)
+    out = torch.full((len(idx), 32), 2.0, dtype=torch.bfloat16, device=dev())
+    M.grouped_mxfp4_contiguous(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array(idx, np.int32)), out=out)
+    live = [i for i, e in enumerate(idx) if e >= 0]
+    touched = np.array(idx) >= 0
+    got = bits(out)
+    assert (got[~touched] == 0x4000).all()
+    for e in (0, 1):
+        r = np.nonzero(np.array(idx) == e)[0]
+        ref, tol = LO.product(a[r], w[e])
+        LO.assert_within(got[r], ref, tol, f"expert {e}")
+    assert len(live) == int(touched.sum())
 
 
 def test_grouped_masked_clamps_counts():

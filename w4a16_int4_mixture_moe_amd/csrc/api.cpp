@@ -1358,12 +1358,11 @@ w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const
   st = check_mx_rows(m_rows, desc->K);
   if (st != W4A16_OK) return st;
   if (m_rows == 0) return W4A16_OK;
-  const int32_t bm = 128;
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, reinterpret_cast<const uint16_t*>(a_codes), out, 4, 4);
   p.a_scale = a_scales;
   p.m_indices = m_indices;
-  p.grid_blocks = (int32_t)(m_rows / bm);
-  hipError_t e = w4a16::launch_mx_grouped(w4a16::kRouteContiguous, bm / 16, p, static_cast<hipStream_t>(stream));
+  p.grid_blocks = (int32_t)(m_rows / 128);
+  hipError_t e = w4a16::launch_mx_tile(w4a16::kRouteContiguous, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "mxfp4_grouped_contiguous launch");
   return W4A16_OK;
 }
@@ -1380,15 +1379,13 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
   if ((int64_t)desc->E * max_m >= INT32_MAX / 2) return fail(W4A16_ERR_SHAPE, "E * max_m too large");
   st = check_mx_rows((int64_t)desc->E * max_m, desc->K);
   if (st != W4A16_OK) return st;
-  const int32_t want = std::min(max_m, expected_m + (expected_m + 3) / 4);
-  const int32_t bm = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, reinterpret_cast<const uint16_t*>(a_codes), out, 4, 4);
   p.a_scale = a_scales;
   p.masked_m = masked_m;
   p.max_m = max_m;
-  p.blocks_per_group = (max_m + bm - 1) / bm;
+  p.blocks_per_group = (max_m + 127) / 128;
   p.grid_blocks = desc->E * p.blocks_per_group;
-  hipError_t e = w4a16::launch_mx_grouped(w4a16::kRouteMasked, bm / 16, p, static_cast<hipStream_t>(stream));
+  hipError_t e = w4a16::launch_mx_tile(w4a16::kRouteMasked, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "mxfp4_grouped_masked launch");
   return W4A16_OK;
 }

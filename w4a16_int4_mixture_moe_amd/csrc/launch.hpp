@@ -148,10 +148,9 @@ hipError_t launch_mx_quant_pack(const void* w, bool fp32, int32_t E, int32_t N, 
                                 uint32_t* pw, uint8_t* ps, hipStream_t stream);
 hipError_t launch_mx_dequant(const uint32_t* pw, const uint8_t* ps, int32_t E, int32_t N, int32_t K, int32_t gate_up,
                              uint16_t* out, hipStream_t stream);
-// The grouped layouts (route kRouteContiguous or kRouteMasked), bf16 store;
-// m_tiles: 16-row token tiles per block (1, 2, 4 or 8)
-hipError_t launch_mx_grouped(int route, int m_tiles, const GemmParams& p, hipStream_t stream);
-hipError_t launch_mx_tile(int route, const GemmParams& p, hipStream_t stream);   // its 128-row tile (mx_tile.hip)
+// The grouped layouts (route kRouteContiguous or kRouteMasked; grid_blocks and
+// blocks_per_group count 128-row blocks), bf16 store (mx_tile.hip)
+hipError_t launch_mx_tile(int route, const GemmParams& p, hipStream_t stream);
 // Indexed routing only; epilogue kEpiStore, kEpiWeighted or kEpiSiluMx.
 bool mx_gemm_config_supported(int epilogue, int m_tiles, int nr, int waves, int stages);
 hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stages, const GemmParams& p,

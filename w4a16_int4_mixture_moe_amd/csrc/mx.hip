@@ -556,13 +556,13 @@ __device__ __forceinline__ void mx_silu_epilogue(const GemmParams& p, const Smem
   }
 }
 
-template <int MT, int NR, int NW, int D, int EPI, int ROUTE = kRouteIndexed>
+template <int MT, int NR, int NW, int D, int EPI>
 __global__ __launch_bounds__(NW * kWave) void mx_gemm_kernel(const GemmParams p) {
   constexpr bool STAGED = MT >= 4;
   __shared__ std::conditional_t<STAGED, MxStagedSmem<MT>, MxSmem<MT>> sm;
   int mb, nt;
   if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
-  const int expert = setup_rows<MT, NW, ROUTE, EPI>(p, mb, sm);
+  const int expert = setup_rows<MT, NW, kRouteIndexed, EPI>(p, mb, sm);
   if (expert < 0) return;
   __syncthreads();
   const uint32_t tmask = active_tiles<MT>(sm);
@@ -743,31 +743,6 @@ hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stag
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(waves * kWave), 0, stream, q);
-  return hipGetLastError();
-}
-
-// ------------------------------------------------------------ grouped layouts
-
-// blocks of up to 64 rows; 128-row blocks run the tile of mx_tile.hip
-template <int ROUTE>
-static MxKernel pick_mx_grouped(int m_tiles) {
-  if (m_tiles == 1) return mx_gemm_kernel<1, 4, 4, 4, kEpiStore, ROUTE>;
-  if (m_tiles == 2) return mx_gemm_kernel<2, 4, 4, 4, kEpiStore, ROUTE>;
-  return m_tiles == 4 ? mx_gemm_kernel<4, 4, 4, 2, kEpiStore, ROUTE> : nullptr;
-}
-
-hipError_t launch_mx_grouped(int route, int m_tiles, const GemmParams& p, hipStream_t stream) {
-  if (m_tiles == 8) return launch_mx_tile(route, p, stream);
-  if (route != kRouteMasked) return hipErrorInvalidValue;
-  const MxKernel k = pick_mx_grouped<kRouteMasked>(m_tiles);
-  if (k == nullptr) return hipErrorInvalidValue;
-  GemmParams q = p;
-  q.n_tiles = (p.NT + 15) / 16;                        // 16 weight tiles per workgroup (4 waves x 4)
-  q.xcd_group = 0;
-  const int64_t grid = grid_of(q, q.n_tiles);
-  if (grid <= 0) return hipSuccess;
-  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(4 * kWave), 0, stream, q);
   return hipGetLastError();
 }
 

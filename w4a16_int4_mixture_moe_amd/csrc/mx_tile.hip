@@ -6,15 +6,26 @@
 // goes HBM -> LDS by LDS-DMA, three chunks deep, and from there to the
 // matrix unit, so no register holds data in flight and two workgroups (two
 // waves per SIMD) share a CU: 128 accumulator registers a wave, 76.5 KB of
-// LDS a workgroup.  (With the activations through registers and one chunk
-// ahead, as the general tile does it, a chunk took as long as its loads.)
+// LDS a workgroup.  Measured on MI355X (N 4096, K 7168, graph replays):
+// 16384 rows of 48 experts, 44 of them with rows, 360 us, 2.7 PFLOP/s on
+// valid rows; all rows one expert's 276 us, 3.5 PFLOP/s; masked decode, 576
+// rows of 48 experts, 137 us, 5.3 TB/s of weights and rows.  What bounds it:
+// with one expert the LDS-DMA stream (without the MFMAs 252 us before the
+// order of the fetches below, without the DMA 185 us), with many experts the
+// HBM (4.6 TB/s beyond the L2s), in decode the HBM.  Tried and slower: the
+// operands through registers, two chunks ahead (472 against 378 us); 256 rows
+// by 256 weight rows on eight waves, one workgroup per CU, three chunks ahead
+// (436 against 363 us); every request of a chunk in one go (376 against 375 us).
 //
-// LDS holds whole operand fragments: fragment f is the 64 lanes' 16 bytes in
-// lane order, which is how one LDS-DMA instruction writes and one
-// conflict-free ds_read_b128 reads it.  The packed weights are fragments
-// already; of the activations, lane l fetches the 16 bytes of block l / 16 of
-// its row l % 16.  Scales: a dword (four blocks) per row, a byte per lane of
-// each weight tile; both are read as the byte the lane's operand wants.
+// LDS holds whole operand fragments of 1 KB, one LDS-DMA instruction each.
+// The packed weights are fragments in lane order already.  Of the
+// activations, lane l fetches 16 of the 64 bytes of row l / 4 of the tile, so
+// that neighbouring lanes share a row (with row l % 16, the operand's own
+// order, every lane was a request of its own: the rows alone took a third of
+// the time); block b of row r lands in place b ^ (r / 4) of the row's four,
+// which makes the operand read, row l % 16 and block l / 16, free of bank
+// conflicts.  Scales: four blocks' bytes per row, a byte per lane of each
+// weight tile; both are read as the byte the lane's operand wants.
 //
 // One barrier a chunk.  A wave waits until its own part of chunk c has landed
 // (its loads complete in order: at most the next chunk's may be in flight),
@@ -23,7 +34,6 @@
 // instruction behind a wait for this wave's LDS reads: __syncthreads, or a
 // fence, would wait for every load (an LDS-DMA counts as a write to LDS).
 // Nothing is requested past the last chunk, so no DMA outlives the workgroup.
-#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -38,7 +48,7 @@ constexpr int kMT = 8, kNR = 4, kNW = 4;            // token tiles, weight tiles
 constexpr int kTiles = kNR * kNW;                   // weight tiles per workgroup
 constexpr int kStages = 3;
 constexpr int kThreads = kNW * kWave;
-constexpr int kRun = 4, kRunMinBlocks = 64;
+constexpr int kAhead = 2;                           // token tiles whose LDS reads run ahead of their MFMAs
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
@@ -73,6 +83,13 @@ __device__ __forceinline__ void wait_loads() {
   static_assert(n >= 0 && n < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14));
 }
+
+// Activation fragments in LDS: the row of its tile and the block that lane l
+// fetches, and where the operand's lane l (row l % 16, block l / 16) finds its
+// 16 bytes.
+__device__ __forceinline__ int fetch_row(int lane) { return lane >> 2; }
+__device__ __forceinline__ uint32_t fetch_block(int lane) { return (uint32_t)((lane & 3) ^ (lane >> 4)); }
+__device__ __forceinline__ int operand_at(int lane) { return 4 * (lane & 15) + ((lane >> 4) ^ ((lane >> 2) & 3)); }
 
 // This wave's LDS reads have ended and every wave is here; loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
@@ -117,7 +134,7 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
   uint32_t xoff[XF];
 #pragma unroll
   for (int i = 0; i < XF; ++i)
-    xoff[i] = row_of(16 * (wave + kNW * i) + (lane & 15)) * kb + 16u * (uint32_t)(lane >> 4);
+    xoff[i] = row_of(16 * (wave + kNW * i) + fetch_row(lane)) * kb + 16u * fetch_block(lane);
   const gptr_t xsbase = uniform_ptr(p.a_scale);
   // no lane or wave is masked off in the loop: a branch there would end its
   // basic block, and the compiler then sinks the MFMAs behind the last
@@ -126,20 +143,31 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
   const int xs0 = FOUR ? 64 * (wave & 1) : 32 * wave;
   const uint32_t xsoff = row_of(FOUR ? xs0 + lane : xs0 + (lane < 32 ? lane : 0)) * ks;
 
-  auto issue = [&](int c, int slot) {
+  const int at = operand_at(lane);
+  // instruction i (of kLoads) of chunk c
+  auto issue = [&](int i, int c, int slot) {
     Stage& s = sm.stage[slot];
-#pragma unroll
-    for (int i = 0; i < kNR; ++i)
+    if (i < kNR)
       dma16(wsrc[i] + (int64_t)c * (kWave * 16) + lane * 16, (lds_ptr_t)&s.w[wave + kNW * i][0]);
+    else if (i < kNR + XF)
+      dma16(xbase + (int64_t)c * 64 + xoff[i - kNR], (lds_ptr_t)&s.x[wave + kNW * (i - kNR)][0]);
+    else if (i == kNR + XF)
+      dma4(wssrc + (int64_t)c * kWave, (lds_ptr_t)&s.ws[4 * wave][0]);
+    else
+      dma4(xsbase + (int64_t)c * 4 + xsoff, (lds_ptr_t)&sm.xs.one[slot][wave][0]);
+  };
+  auto issue_all = [&](int c, int slot) {
 #pragma unroll
-    for (int i = 0; i < XF; ++i) dma16(xbase + (int64_t)c * 64 + xoff[i], (lds_ptr_t)&s.x[wave + kNW * i][0]);
-    dma4(wssrc + (int64_t)c * kWave, (lds_ptr_t)&s.ws[4 * wave][0]);
-    if constexpr (!FOUR) dma4(xsbase + (int64_t)c * 4 + xsoff, (lds_ptr_t)&sm.xs.one[slot][wave][0]);
+    for (int i = 0; i < kLoads; ++i) issue(i, c, slot);
   };
   auto issue_four = [&](int group) {
     dma16(xsbase + (int64_t)min(group, KC / 4 - 1) * 16 + xsoff, (lds_ptr_t)&sm.xs.four[group & 1][xs0]);
   };
-  auto compute = [&](int c, int slot) {
+  // chunk c; the requests of a later one (more: chunk `ask`, buffer `to`) go
+  // out one after each tile's MFMAs, since an LDS-DMA takes the address unit
+  // some 40 cycles
+  auto compute = [&](int c, int slot, auto more, int ask, int to) {
+    constexpr bool MORE = decltype(more)::value;
     const Stage& s = sm.stage[slot];
     u32x4_t A[kNR];
     uint32_t as[kNR];
@@ -153,33 +181,44 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
                              : reinterpret_cast<const uint8_t*>(&sm.xs.one[slot][0][lane & 15]);
     xs += lane >> 4;
     auto xs_at = [&](int t) { return FOUR ? 256 * t : 256 * (t / 2) + 64 * (t % 2); };
-    u32x4_t B = s.x[0][lane];
-    uint32_t bs = xs[0];
+    // kAhead tiles of reads in flight: a read takes about as long as the MFMAs
+    // of two or three tiles
+    u32x4_t B[kAhead + 1];
+    uint32_t bs[kAhead + 1];
+#pragma unroll
+    for (int t = 0; t < kAhead && t < NA; ++t) {
+      B[t] = s.x[t][at];
+      bs[t] = xs[xs_at(t)];
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < NA; ++t) {
-      u32x4_t Bn = B;
-      uint32_t bn = bs;
-      if (t + 1 < NA) {
-        Bn = s.x[t + 1][lane];
-        bn = xs[xs_at(t + 1)];
+      if (t + kAhead < NA) {
+        B[(t + kAhead) % (kAhead + 1)] = s.x[t + kAhead][at];
+        bs[(t + kAhead) % (kAhead + 1)] = xs[xs_at(t + kAhead)];
       }
-      const i32x8_t b = {(int)B[0], (int)B[1], (int)B[2], (int)B[3], 0, 0, 0, 0};
+      const u32x4_t v = B[t % (kAhead + 1)];
+      const i32x8_t b = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < kNR; ++r) {
         const i32x8_t a = {(int)A[r][0], (int)A[r][1], (int)A[r][2], (int)A[r][3], 0, 0, 0, 0};
-        acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[r][t], 4, 4, 0, (int)as[r], 0, (int)bs);
+        acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[r][t], 4, 4, 0, (int)as[r], 0,
+                                                                     (int)bs[t % (kAhead + 1)]);
       }
-      B = Bn;
-      bs = bn;
-      __builtin_amdgcn_sched_barrier(0);            // one tile read ahead, no more: the registers are full
+      __builtin_amdgcn_sched_barrier(0);            // no more reads ahead: the registers are full
+      if (MORE && t < kLoads) issue(t, ask, to);
+      __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int i = NA; i < kLoads; ++i)
+      if (MORE) issue(i, ask, to);
   };
 
   static_assert(kStages == 3, "the waits below keep one later chunk in flight");
   auto after = [](int slot) { return slot == kStages - 1 ? 0 : slot + 1; };
   if constexpr (FOUR) issue_four(0);
-  issue(0, 0);
-  if (KC > 1) issue(1, 1);
+  issue_all(0, 0);
+  if (KC > 1) issue_all(1, 1);
   int c = 0, slot = 0;
   // Chunk c has landed and its predecessor's buffer is free: fill that with
   // chunk c + 2, multiply.  newer: this wave's loads issued after chunk c's.
@@ -187,16 +226,15 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
     wait_loads<decltype(newer)::value>();
     lds_barrier();
     if constexpr (decltype(group)::value) issue_four(c / 4 + 1);
-    issue(c + 2, after(after(slot)));
     __builtin_amdgcn_sched_barrier(0);
-    compute(c, slot);
+    compute(c, slot, std::true_type{}, c + 2, after(after(slot)));
     ++c;
     slot = after(slot);
   };
   auto last = [&](auto newer) {
     wait_loads<decltype(newer)::value>();
     lds_barrier();
-    compute(c, slot);
+    compute(c, slot, std::false_type{}, 0, 0);
     ++c;
     slot = after(slot);
   };
@@ -206,7 +244,7 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
   using Yes = std::true_type;
   using No = std::false_type;
   if constexpr (FOUR) {                             // KC is a multiple of 4
-    for (; c + 4 < KC;) {
+    while (c + 4 < KC) {
       step(N1{}, Yes{});
       step(N2{}, No{});
       step(N1{}, No{});
@@ -217,35 +255,16 @@ __device__ __forceinline__ void tile_mainloop(const GemmParams& p, TileSmemMx& s
     last(N1{});
     last(N0{});
   } else {
-    for (; c + 2 < KC;) step(N1{}, No{});
+    while (c + 2 < KC) step(N1{}, No{});
     if (c + 1 < KC) last(N1{});
     last(N0{});
   }
 }
 
-// Workgroup w -> block and N tile.  p.xcd_group = G > 0: runs of G blocks x
-// all N tiles share an XCD (workgroups go to the eight XCDs in turn), the
-// blocks of a run next to each other for each N tile, so that an expert's
-// consecutive blocks read a weight tile from HBM once and its rows stay in
-// one L2.  0: block after block.
-__device__ __forceinline__ void item_of(const GemmParams& p, int w, int& mb, int& nt) {
-  if (p.xcd_group == 0) {
-    mb = w / p.n_tiles;
-    nt = w - mb * p.n_tiles;
-    return;
-  }
-  const int per = p.xcd_group * p.n_tiles, k = w >> 3;
-  const int run = k / per, r = k - run * per;
-  nt = r / p.xcd_group;
-  mb = (run * 8 + (w & 7)) * p.xcd_group + (r - nt * p.xcd_group);
-}
-
 template <int ROUTE>
 __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const GemmParams p) {
   __shared__ __attribute__((aligned(16))) TileSmemMx sm;
-  int mb, nt;
-  item_of(p, blockIdx.x, mb, nt);
-  if (mb >= p.grid_blocks) return;
+  const int mb = blockIdx.x / p.n_tiles, nt = blockIdx.x - mb * p.n_tiles;
   const int expert = setup_rows<kMT, kNW, ROUTE, kEpiStore>(p, mb, sm);
   if (expert < 0) return;
   __syncthreads();
@@ -278,9 +297,11 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const GemmParams p
 hipError_t launch_mx_tile(int route, const GemmParams& p, hipStream_t stream) {
   GemmParams q = p;
   q.n_tiles = (p.NT + kTiles - 1) / kTiles;
-  q.xcd_group = p.grid_blocks >= kRunMinBlocks ? kRun : 0;
-  const int64_t run = 8 * (int64_t)std::max(q.xcd_group, 1);
-  const int64_t grid = (q.xcd_group ? (p.grid_blocks + run - 1) / run * run : p.grid_blocks) * q.n_tiles;
+  // Block after block: a block's N tiles go to the eight XCDs in turn, so each
+  // XCD reads every block's rows and its own share of the N tiles.  (Runs of 2
+  // to 8 blocks with all their N tiles on one XCD, which reads the rows once,
+  // measured no faster: 16384 rows of 48 experts 358 - 404 us against 360.)
+  const int64_t grid = (int64_t)p.grid_blocks * q.n_tiles;
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
   if (route == kRouteContiguous)
