@@ -570,7 +570,8 @@ w4a16_status w4a16_mxfp4_dequant(const w4a16_weight_desc* desc, const void* pack
  * Contiguous: rows = m_rows, a multiple of 128; a row's m_indices entry
  * outside [0, E) marks padding, and a segment's valid rows come first.
  * Masked: rows = E * max_m; a count masked_m[g] outside [0, max_m] is taken
- * as the nearer end; expected_m (host, > 0) only steers the tile choice.
+ * as the nearer end; expected_m (host, > 0) is taken as in
+ * w4a16_grouped_masked, but the one tile built does not depend on it.
  * Sizes: rows * K / 2 below 4 GiB (ERR_SHAPE).
  * Pointers: packed_w, packed_s, a_codes, out 16-byte aligned, a_scales 4.
  * Errors: ERR_ARG, ERR_LAYOUT (not an MXFP4 weight), ERR_SHAPE, ERR_HIP. */
@@ -641,7 +642,7 @@ w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32
  * not initialised; its contents are the call's own until it has finished.
  * out must not overlap any input.
  * Sizes: T <= W4A16_FEW_MAX_TOKENS, T * topk <= W4A16_FEW_MAX_SLOTS,
- * E <= W4A16_FEW_MAX_EXPERTS (ERR_SHAPE; larger batches take w4a16_moe_align and the GEMM calls).
+ * E <= W4A16_FEW_MAX_EXPERTS, H and I <= 2^24 (ERR_SHAPE; larger batches take w4a16_moe_align and the GEMM calls).
  * Pointers 16-byte aligned (topk_ids, topk_weights: 4).
  * Errors: ERR_ARG, ERR_LAYOUT (packing), ERR_SHAPE, ERR_WORKSPACE, ERR_HIP. */
 w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* gate_up_w, const void* gate_up_s,

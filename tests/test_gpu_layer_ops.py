@@ -244,6 +244,24 @@ def test_few_tokens_agrees_with_the_routed_path(layers):
     assert ((y - z).abs() <= 7 * 4 * 2.0 ** -8 * rms + 2.0 ** -7 * y.abs()).all()
 
 
+def test_routed_path_skips_slots_without_an_expert(layers):
+    """The router's -1 ids through moe_align and the combine."""
+    lay = layers["int4_wide"]
+    x, _, _ = _tokens(20, 2, 3, lay.H, 31)
+    dx = to_dev_bf16(x)
+    l = torch.randn(20, 3, device=dev())
+    l[::4] = float("-inf")
+    l[1, 1:] = float("nan")                                # one expert left for two slots
+    di, dw = M.moe_route(l, 2)
+    assert (di[::4] == -1).all() and di[1].tolist() == [0, -1] and dw[1].tolist() == [1.0, 0.0]
+    y = M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw).float()
+    r = M.moe_align(di, 3, 0, 3, 16)
+    z = M.moe_w4a16_gemm(M.moe_gate_up_silu(dx, lay.p1, r), lay.p2, r, dw, a_layout="sorted").float()
+    assert not y[::4].any() and not z[::4].any()
+    rms = y.pow(2).mean().sqrt()                           # bounds as in the test above
+    assert ((y - z).abs() <= 7 * 4 * 2.0 ** -8 * rms + 2.0 ** -7 * y.abs()).all()
+
+
 # ------------------------------------------------------------------ chain, graph, streams
 
 def test_route_then_layer_captured_and_replayed(layers):

@@ -113,7 +113,7 @@ def test_few_tokens_refusals(L, mx):
                                       wsb, None)
     assert call(T=0, x=None, ids=None, w=None, out=None, ws=None, wsb=0) == 0
     assert call(wsb=need - 1) == -8 and call(ws=None) == -8 and call(ws=P + 8) == -8
-    assert call(T=-1) == -1 and call(k=0) == -1 and call(first=-1) == -1 and call(first=2 ** 31 - 2) == -1
+    assert call(T=-1) == -1 and call(k=0) == -1 and call(first=-1) == -1 and call(first=2 ** 30 + 1) == -1
     assert call(T=65, k=1) == -2 and call(T=64, k=17) == -2 and call(T=1, k=1025) == -2
     assert call(x=None) == -1 and call(ids=None) == -1 and call(w=None) == -1 and call(out=None) == -1
     assert call(w1=None) == -1 and call(x=P + 8) == -1 and call(ids=P + 2) == -1

@@ -345,6 +345,8 @@ __all__ = [
     "moe_gate_up_silu",
     "grouped_contiguous",
     "grouped_masked",
+    "quant_pack_mxfp4", "dequant_mxfp4", "grouped_mxfp4_contiguous", "grouped_mxfp4_masked",
+    "moe_route", "moe_few_tokens", "few_tokens_workspace_bytes",
 ]
 
 
@@ -527,7 +529,7 @@ def quant_pack_mxfp4(w: torch.Tensor, gate_up: bool = False) -> PackedW4:
     pw = torch.empty(d.w_bytes, dtype=torch.uint8, device=w.device)
     ps = torch.empty(d.s_bytes, dtype=torch.uint8, device=w.device)
     _launch(w.device, load().w4a16_mxfp4_quant_pack, w.data_ptr(), _WEIGHT_DTYPES[w.dtype], ctypes.byref(d),
-                pw.data_ptr(), ps.data_ptr())
+            pw.data_ptr(), ps.data_ptr())
     return PackedW4(d, pw, ps)
 
 
@@ -545,7 +547,7 @@ def dequant_mxfp4(packed: PackedW4, out: Optional[torch.Tensor] = None) -> torch
             raise ValueError(f"out must be {list(shape)}")
     _same_device(packed.w, w=packed.w, s=packed.s, out=out)
     _launch(out.device, load().w4a16_mxfp4_dequant, ctypes.byref(packed.desc), packed.w.data_ptr(),
-                packed.s.data_ptr(), out.data_ptr())
+            packed.s.data_ptr(), out.data_ptr())
     return out
 
 
@@ -589,8 +591,8 @@ def grouped_mxfp4_contiguous(a: MXRows, packed: PackedW4, m_indices: torch.Tenso
     left as they are (zero in an out made here)."""
     out = _grouped_mx_args(a, packed, m_indices, "m_indices", m_indices.shape[0], out)
     _launch(out.device, load().w4a16_mxfp4_grouped_contiguous, ctypes.byref(packed.desc), packed.w.data_ptr(),
-                packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), a.rows, m_indices.data_ptr(),
-                out.data_ptr())
+            packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), a.rows, m_indices.data_ptr(),
+            out.data_ptr())
     return out
 
 
@@ -605,8 +607,8 @@ def grouped_mxfp4_masked(a: MXRows, packed: PackedW4, masked_m: torch.Tensor, ex
     if masked_m.shape[0] != packed.E:
         raise ValueError(f"masked_m has {masked_m.shape[0]} entries, the weight {packed.E} experts")
     _launch(out.device, load().w4a16_mxfp4_grouped_masked, ctypes.byref(packed.desc), packed.w.data_ptr(),
-                packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), a.rows // packed.E,
-                masked_m.data_ptr(), int(expected_m), out.data_ptr())
+            packed.s.data_ptr(), a.codes.data_ptr(), a.scales.data_ptr(), a.rows // packed.E,
+            masked_m.data_ptr(), int(expected_m), out.data_ptr())
     return out
 
 
@@ -642,9 +644,9 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
     dev = logits.device
     ids = torch.empty(T, max(int(topk), 0), dtype=torch.int32, device=dev)
     weights = torch.empty(T, max(int(topk), 0), dtype=torch.float32, device=dev)
-    _launch(dev, load().w4a16_moe_route, logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E, logits.stride(0) if T
-                > 1 else E, _ptr(bias), int(topk), _SCORINGS[scoring], int(bool(renormalize)), float(scale),
-                ids.data_ptr(), weights.data_ptr())
+    stride = logits.stride(0) if T > 1 else E
+    _launch(dev, load().w4a16_moe_route, logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E, stride, _ptr(bias),
+            int(topk), _SCORINGS[scoring], int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -685,7 +687,7 @@ def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids:
     _same_device(x, gate_up=gate_up.w, gate_up_scales=gate_up.s, down=down.w, down_scales=down.s, topk_ids=topk_ids,
                  topk_weights=topk_weights, out=out, workspace=workspace)
     _launch(dev, load().w4a16_moe_few_tokens, ctypes.byref(gate_up.desc), gate_up.w.data_ptr(),
-                gate_up.s.data_ptr(), ctypes.byref(down.desc), down.w.data_ptr(), down.s.data_ptr(), x.data_ptr(),
-                T, k, topk_ids.data_ptr(), topk_weights.data_ptr(), int(first_expert), out.data_ptr(),
-                _ptr(workspace), 0 if workspace is None else workspace.numel())
+            gate_up.s.data_ptr(), ctypes.byref(down.desc), down.w.data_ptr(), down.s.data_ptr(), x.data_ptr(),
+            T, k, topk_ids.data_ptr(), topk_weights.data_ptr(), int(first_expert), out.data_ptr(),
+            _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out

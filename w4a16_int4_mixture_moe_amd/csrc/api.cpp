@@ -1081,6 +1081,8 @@ struct FewWorkspace {
   size_t total() const { return h + rows + plan + 256; }
 };
 
+constexpr int32_t kFewMaxWidth = 1 << 24;   // blocks x tiles and blocks x chunks stay below 2^31
+
 FewWorkspace few_workspace(int32_t I, int32_t slots) {
   FewWorkspace w;
   w.h = al256((size_t)slots * I * 2);
@@ -1451,7 +1453,10 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
                 gate_up->K, down->E, down->N, down->K);
   if (T < 0 || topk <= 0 || first_expert < 0)
     return fail(W4A16_ERR_ARG, "bad sizes T=%d topk=%d first_expert=%d", T, topk, first_expert);
-  if ((int64_t)first_expert + gate_up->E > INT32_MAX) return fail(W4A16_ERR_ARG, "first_expert = %d too large", first_expert);
+  // id - first_expert must not wrap round for any 32-bit id
+  if (first_expert > (1 << 30)) return fail(W4A16_ERR_ARG, "first_expert = %d too large", first_expert);
+  if (gate_up->K > kFewMaxWidth || down->K > kFewMaxWidth)
+    return fail(W4A16_ERR_SHAPE, "widths H = %d, I = %d: at most %d", gate_up->K, down->K, kFewMaxWidth);
   if (gate_up->E > W4A16_FEW_MAX_EXPERTS)
     return fail(W4A16_ERR_SHAPE, "%d local experts, at most %d", gate_up->E, W4A16_FEW_MAX_EXPERTS);
   if (T > W4A16_FEW_MAX_TOKENS || (int64_t)T * topk > W4A16_FEW_MAX_SLOTS)

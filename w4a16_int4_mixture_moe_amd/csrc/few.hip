@@ -10,6 +10,17 @@
 // in operand order; there is no align kernel, no combine kernel and no
 // partial sum in memory.
 //
+//
+// Measured on MI355X (whole calls, graph replays; bytes are the touched
+// experts' weights and scales): 16 tokens on an INT4 EP8 share (48 of 384
+// experts, H 7168, I 2048) 75 - 92 us, 3.8 - 4.5 TB/s; 37 tokens x 16 on an
+// MXFP4 share of 112 of 896 experts 221 - 250 us, 5.1 - 5.8 TB/s; one token on
+// a TP8 slice (I 256) 18 us, of which the weights' bytes are 5.  HBM bounds
+// the MXFP4 call; the INT4 one spends about half its vector issue on the
+// dequantisation (17 instructions for 8 weights) and loses some 15 % to the
+// last round of its items; the single token is two launches and their chains
+// of dependent loads.
+//
 // Both weight layouts give lane l = 16 g + i the 32 consecutive K of row i
 // that scale block 4 c + g covers, eight codes a word, so one dequantised
 // word is a v_mfma_f32_16x16x32_bf16 operand and only the dequantisation
@@ -37,14 +48,16 @@ namespace {
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kFewWaves * kWave;
 static_assert(kFewMaxSlots == 2 * kFewThreads && kFewMaxTokens <= 64, "two slots a thread, a bit a token");
-// workgroups of the gate/up kernel: two on each of 256 CUs
+// workgroups of the gate/up kernel, two on each of 256 CUs: with a workgroup
+// for every (slot, tile pair) instead, those with nothing to do held the CUs
+// for as long as the others took (139 -> 101 us on the INT4 share above)
 constexpr int kFewGroups = 512;
 // The down kernel takes two column tiles a workgroup (a deeper ring, one
 // workgroup per CU, half the work a block costs besides its weights) where
 // that leaves most CUs a workgroup and each wave several units.  Measured on
 // MI355X, whole call, one / two tiles: 16 tokens on an INT4 EP8 share 93.8 /
 // 88.8 us, 37 x 16 on an MXFP4 share 278 / 264 us; but one token on a TP8
-// slice 19.4 / 22.9 us.
+// slice 19.4 / 22.9 us (each wave then has two units).
 constexpr int kFewWideDown = 192;
 constexpr int kFewWideUnits = 512;
 

@@ -117,7 +117,9 @@ hipError_t launch_mx_quant(const uint16_t* x, int64_t rows, int32_t K, uint8_t* 
 // whole 256-byte (fp32: 512-byte) row pieces and the four lanes of an MX
 // block are neighbours, which share their maximum with two DPP steps.  Each
 // lane's 8 codes are one word of the packed fragment.  HBM-bound: 2 or 4
-// bytes in and 17/32 byte out an element, one pass.
+// bytes in and 17/32 byte out an element, one pass.  Measured on MI355X with
+// the dequantisation below, 48 x 4096 x 7168 bf16: 1266 us for both, 5.6 TB/s
+// of the 7.1 GB they move (a 2 GiB copy: 4.9 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void mx_quant_pack_kernel(const T* __restrict__ w, int64_t tiles, int32_t N,
                                                              int32_t K, int32_t gate_up,
