@@ -8,7 +8,7 @@
 // waves per SIMD) share a CU: 128 accumulator registers a wave, 76.5 KB of
 // LDS a workgroup.  Measured on MI355X (N 4096, K 7168, graph replays):
 // 16384 rows of 48 experts, 44 of them with rows, 360 us, 2.7 PFLOP/s on
-// valid rows; all rows one expert's 276 us, 3.5 PFLOP/s; masked decode, 576
+// valid rows; all rows one expert's 278 us, 3.5 PFLOP/s; masked decode, 576
 // rows of 48 experts, 137 us, 5.3 TB/s of weights and rows.  What bounds it:
 // with one expert the LDS-DMA stream (without the MFMAs 252 us before the
 // order of the fetches below, without the DMA 185 us), with many experts the
@@ -22,10 +22,13 @@
 // activations, lane l fetches 16 of the 64 bytes of row l / 4 of the tile, so
 // that neighbouring lanes share a row (with row l % 16, the operand's own
 // order, every lane was a request of its own: the rows alone took a third of
-// the time); block b of row r lands in place b ^ (r / 4) of the row's four,
-// which makes the operand read, row l % 16 and block l / 16, free of bank
-// conflicts.  Scales: four blocks' bytes per row, a byte per lane of each
-// weight tile; both are read as the byte the lane's operand wants.
+// the time); block b of row r lands in place b of the row's four, or 3 - b
+// where bit 2 of r is set, so that the lanes a b128 read serves together
+// (not sixteen in a row) fall on different banks.  Scales: four blocks' bytes
+// per row, a byte per lane of each weight tile; both are read as the byte the
+// lane's operand wants.  Bank conflicts (SQ_LDS_BANK_CONFLICT, the prefill
+// case above) take 4 % of the CUs' cycles, about two for each read of the row
+// scales, which lie 16 bytes apart; with places b ^ (r / 4) they took 12 %.
 //
 // One barrier a chunk.  A wave waits until its own part of chunk c has landed
 // (its loads complete in order: at most the next chunk's may be in flight),
@@ -88,8 +91,9 @@ __device__ __forceinline__ void wait_loads() {
 // fetches, and where the operand's lane l (row l % 16, block l / 16) finds its
 // 16 bytes.
 __device__ __forceinline__ int fetch_row(int lane) { return lane >> 2; }
-__device__ __forceinline__ uint32_t fetch_block(int lane) { return (uint32_t)((lane & 3) ^ (lane >> 4)); }
-__device__ __forceinline__ int operand_at(int lane) { return 4 * (lane & 15) + ((lane >> 4) ^ ((lane >> 2) & 3)); }
+__device__ __forceinline__ int place_swap(int row) { return row & 4 ? 3 : 0; }
+__device__ __forceinline__ uint32_t fetch_block(int lane) { return (uint32_t)((lane & 3) ^ place_swap(lane >> 2)); }
+__device__ __forceinline__ int operand_at(int lane) { return 4 * (lane & 15) + ((lane >> 4) ^ place_swap(lane)); }
 
 // This wave's LDS reads have ended and every wave is here; loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
