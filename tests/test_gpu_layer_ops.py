@@ -108,8 +108,9 @@ def test_route_strided_rows_other_stream_and_refusals():
         M.moe_route(wide.double(), 4)
     with pytest.raises(ValueError):
         M.moe_route(wide, 4, scoring="sigmoid", bias=torch.zeros(4, device=dev()))
-    with pytest.raises(M.W4A16Error):
-        M.moe_route(wide, 33)
+    for k in (33, 0, -1, 513, 2**32 + 4):
+        with pytest.raises(M.W4A16Error):
+            M.moe_route(wide, k)
 
 
 # ------------------------------------------------------------------ few-token layer
@@ -227,6 +228,14 @@ def test_few_tokens_empty_and_refusals(layers):
             dx, lay.p1, lay.p1, di, dw)
     with pytest.raises(M.W4A16Error):
         M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, workspace=torch.empty(64, dtype=torch.uint8, device=dev()))
+    ws = torch.empty(4 * M.few_tokens_workspace_bytes(lay.p1, 4, 2), dtype=torch.uint8, device=dev())
+    with pytest.raises(ValueError):                       # bytes between a strided view's are not the call's
+        M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, workspace=ws[::2])
+    with pytest.raises(TypeError):
+        M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, workspace=ws.view(torch.int32))
+    for first in (-1, 2**32):
+        with pytest.raises(ValueError):
+            M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, first_expert=first)
 
 
 def test_few_tokens_agrees_with_the_routed_path(layers):
@@ -504,6 +513,21 @@ def test_grouped_masked_clamps_counts():
     M.grouped_mxfp4_masked(M.MXRows(to_dev(c), to_dev(s)), packed, to_dev(np.array([-4, 99, 2], np.int32)), 8, out=out)
     rows = list(range(20, 40)) + [40, 41]
     _grouped_check(bits(out), rows, [1] * 20 + [2] * 2, a, w, "clamped")
+
+
+def test_grouped_mxfp4_scales_on_four_bytes():
+    """K a multiple of 512 with scales that lie on 4 bytes but not on 16: the same bits."""
+    packed, _ = _mx_weight(2, 64, 1024, 2)
+    c, s, _ = _mx_rows(256, 1024, 6)
+    codes, idx = to_dev(c), to_dev(np.repeat(np.array([0, 1], np.int32), 128))
+    buf = torch.empty(s.size + 4, dtype=torch.uint8, device=dev())
+    moved = buf[4:].view(256, 32).copy_(to_dev(s))
+    assert moved.data_ptr() % 16 == 4
+    ref = M.grouped_mxfp4_contiguous(M.MXRows(codes, to_dev(s)), packed, idx)
+    assert torch.equal(M.grouped_mxfp4_contiguous(M.MXRows(codes, moved), packed, idx), ref)
+    counts = torch.tensor([128, 77], dtype=torch.int32, device=dev())
+    ref = M.grouped_mxfp4_masked(M.MXRows(codes, to_dev(s)), packed, counts, 100)
+    assert torch.equal(M.grouped_mxfp4_masked(M.MXRows(codes, moved), packed, counts, 100), ref)
 
 
 def test_grouped_mxfp4_refusals_and_empty():

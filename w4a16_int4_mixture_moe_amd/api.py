@@ -642,11 +642,12 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
             raise ValueError(f"bias has {bias.shape[0]} entries, logits {E} experts")
         _same_device(logits, bias=bias)
     dev = logits.device
-    ids = torch.empty(T, max(int(topk), 0), dtype=torch.int32, device=dev)
-    weights = torch.empty(T, max(int(topk), 0), dtype=torch.float32, device=dev)
+    topk = max(0, min(int(topk), E + 1))                  # outside [1, E] the call refuses it
+    ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
     stride = logits.stride(0) if T > 1 else E
     _launch(dev, load().w4a16_moe_route, logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E, stride, _ptr(bias),
-            int(topk), _SCORINGS[scoring], int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr())
+            topk, _SCORINGS[scoring], int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -684,6 +685,10 @@ def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids:
         nws = few_tokens_workspace_bytes(gate_up, T, k)
         if nws:
             workspace = torch.empty(nws, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", (torch.uint8,))
+    if not 0 <= first_expert < 2**31:
+        raise ValueError(f"first_expert = {first_expert} is not a 32-bit index")
     _same_device(x, gate_up=gate_up.w, gate_up_scales=gate_up.s, down=down.w, down_scales=down.s, topk_ids=topk_ids,
                  topk_weights=topk_weights, out=out, workspace=workspace)
     _launch(dev, load().w4a16_moe_few_tokens, ctypes.byref(gate_up.desc), gate_up.w.data_ptr(),

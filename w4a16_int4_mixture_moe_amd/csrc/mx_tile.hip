@@ -105,8 +105,8 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// FOUR: K is a multiple of 512, and a row's scales come 16 bytes (four
-// chunks) at a time: every row is a cache line of its own to the address
+// FOUR: K is a multiple of 512 and the scales lie on 16 bytes, so a row's
+// come 16 bytes (four chunks) at a time: every row is a cache line of its own to the address
 // unit, and fetched chunk by chunk they kept it busier (82 % of the time) than
 // everything else together.
 template <int NA, bool FOUR>
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const GemmParams p
     for (int r = 0; r < kNR; ++r)
 #pragma unroll
       for (int t = 0; t < kMT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (p.KC % 4 == 0)
+    if (p.KC % 4 == 0 && (reinterpret_cast<uintptr_t>(p.a_scale) & 15) == 0)
       tile_mainloop<NA, true>(p, sm, expert, nt, acc);
     else
       tile_mainloop<NA, false>(p, sm, expert, nt, acc);
