@@ -28,6 +28,8 @@
 // enough to swap two experts that nearly tie.  The list's bound is lowered by
 // that error, and where two of its keys are closer than it the group ranks
 // the list again by s_e + b_e in 64 bits.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -43,6 +45,20 @@ template <typename T>
 __device__ __forceinline__ float logit_value(T v) {
   const float x = (float)v;
   return x > kMaxFinite ? kMaxFinite : x;
+}
+
+// a buffer of bytes, bounds checked by the load (zero past its end)
+constexpr int kRawBuffer = 0x00027000;
+
+template <typename T>
+__device__ __forceinline__ float buffer_value(__amdgpu_buffer_rsrc_t buffer, uint32_t at) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(buffer, at, 0, 0);
+    return __builtin_bit_cast(float, v);
+  } else {
+    const uint16_t v = __builtin_amdgcn_raw_buffer_load_b16(buffer, at, 0, 0);
+    return (float)__builtin_bit_cast(T, v);
+  }
 }
 
 template <int kCtrl>
@@ -139,10 +155,18 @@ struct RouteArgs {
   float* weights;
 };
 
-struct Candidate {
-  float key;
-  int32_t expert;
-};
+// A listed expert as one number, larger = earlier in order of choice: the
+// key's bits in rising order (-0 as +0), then the expert, lower first.
+__device__ __forceinline__ uint64_t listed_as(float key, int expert) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, key + 0.f);
+  const uint32_t up = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return (uint64_t)up << 32 | (uint32_t)~expert;
+}
+__device__ __forceinline__ int listed_expert(uint64_t c) { return (int)~(uint32_t)c; }
+__device__ __forceinline__ float listed_key(uint64_t c) {
+  const uint32_t up = (uint32_t)(c >> 32);
+  return __builtin_bit_cast(float, up ^ ((uint32_t)((int32_t)~up >> 31) | 0x80000000u));
+}
 
 // in order of choice: larger key first, the lower expert of equals
 template <typename K>
@@ -152,8 +176,9 @@ template <int L>
 struct RouteSmem {
   static constexpr int G = kRouteThreads / L;      // tokens per workgroup
   static constexpr int CAP = 2 * (L < 32 ? 16 : L);  // listed experts a token, at most
-  Candidate list[G][CAP + 4];                       // read four at a time
+  uint64_t list[G][CAP + 4];                        // read four at a time, zeros behind the last
   float logit[G][CAP];                              // with a bias
+  float sorted[G][CAP];                             // with a bias: the keys in order
   double exact[G][CAP];
   int count[G];
 };
@@ -169,26 +194,40 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
   const int follow = (int)min((int64_t)g, p.T - 1 - t0);
   const bool real = follow == g;
   const int64_t t = t0 + follow;
-  // the workgroup's rows: a uniform base and 32-bit offsets (the launcher bounds the stride)
+  // the workgroup's rows: a uniform base and 32-bit offsets (the launcher
+  // bounds the stride).  Read as a buffer that ends with the last row's E
+  // values: offsets are constants added by the load, and what a lane reads
+  // past its row is in the buffer, or zero, and masked below.
   const T* rows = static_cast<const T*>(p.logits) + t0 * p.row_stride;
   const uint32_t row0 = (uint32_t)follow * (uint32_t)p.row_stride;
+  const uint32_t held = (uint32_t)min((int64_t)Smem::G, p.T - t0) - 1u;   // rows of the workgroup, less one
+  const uint32_t extent = (held * (uint32_t)p.row_stride + (uint32_t)p.E) * (uint32_t)sizeof(T);
   const bool biased = kSigmoid && p.bias != nullptr;
 
   // keys; -inf: masked or past E
   float x[V], key[V];
+  const auto row_buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(rows), 0, extent, kRawBuffer);
+  const uint32_t lane0 = (row0 + l) * (uint32_t)sizeof(T);
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = logit_value(rows[min(row0 + i * L + l, row0 + p.E - 1)]);
+  for (int i = 0; i < V; ++i) x[i] = buffer_value<T>(row_buffer, lane0 + i * L * (uint32_t)sizeof(T));
   double sum = 0.0;
   float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = i * L + l < p.E && x[i] > -INFINITY ? x[i] : -INFINITY;   // a NaN compares false
   if (biased) {
+    // an infinite logit needs no clamp here (its score is 1); a NaN bias
+    // makes a NaN key, which loses every comparison below
+    const auto bias_buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.bias), 0, 4u * (uint32_t)p.E, kRawBuffer);
     float b[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = p.bias[min((uint32_t)(i * L + l), (uint32_t)p.E - 1u)];
+    for (int i = 0; i < V; ++i) b[i] = buffer_value<float>(bias_buffer, (uint32_t)l * 4u + i * L * 4u);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float c = sigmoid_key(x[i]) + b[i];
+      key[i] = i * L + l < p.E && x[i] > -INFINITY ? (c > kMaxFinite ? kMaxFinite : c) : -INFINITY;
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      key[i] = key[i] > -INFINITY && b[i] > -INFINITY ? fminf(sigmoid_key(key[i]) + b[i], kMaxFinite) : -INFINITY;
+      key[i] = i * L + l < p.E && x[i] > -INFINITY ? fminf(x[i], kMaxFinite) : -INFINITY;   // a NaN compares false
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) m = fmaxf(m, key[i]);
@@ -220,7 +259,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
   for (int i = 0; i < V; ++i)
     if (key[i] >= bound) {
       if (at < Smem::CAP) {
-        sm.list[g][at] = Candidate{key[i], i * L + l};
+        sm.list[g][at] = listed_as(key[i], i * L + l);
         if (biased) sm.logit[g][at] = x[i];
       }
       ++at;
@@ -228,35 +267,47 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
   __builtin_amdgcn_wave_barrier();
   const int listed = sm.count[g];
   const int n = min(listed, Smem::CAP);
+  if (l < 4) sm.list[g][n + l] = 0;                 // comes before nothing
+  __builtin_amdgcn_wave_barrier();
 
   int expert[OWN], rank[OWN];
   float logit[OWN];
   bool close = false;
   {
-    float own[OWN];
+    uint64_t own[OWN];
 #pragma unroll
     for (int q = 0; q < OWN; ++q) {
-      const Candidate c = sm.list[g][l + q * L];
-      expert[q] = l + q * L < n ? c.expert : -1;
-      own[q] = logit[q] = c.key;
-      if (biased) logit[q] = sm.logit[g][l + q * L];
+      own[q] = sm.list[g][l + q * L];
+      expert[q] = l + q * L < n ? listed_expert(own[q]) : -1;
+      logit[q] = biased ? sm.logit[g][l + q * L] : listed_key(own[q]);
       rank[q] = 0;
     }
-    for (int j = 0; j < n; j += 4) {
-      Candidate c[4];
+    auto count = [&](auto owned) {
+      constexpr int Q = decltype(owned)::value;
+      for (int j = 0; j < n; j += 4) {
+        uint64_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = sm.list[g][j + i];
+        for (int i = 0; i < 4; ++i) c[i] = sm.list[g][j + i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool there = j + i < n;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int q = 0; q < OWN; ++q) {
-          rank[q] += there && before(c[i].key, c[i].expert, own[q], expert[q]) ? 1 : 0;
-          if (biased)
-            close = close || (there && expert[q] >= 0 && c[i].expert != expert[q] &&
-                              fabsf(c[i].key - own[q]) <= key_error(own[q]));
-        }
+          for (int q = 0; q < Q; ++q) rank[q] += c[i] > own[q] ? 1 : 0;
       }
+    };
+    if (__ballot(n > L)) count(std::integral_constant<int, OWN>{});   // any group of the wave
+    else count(std::integral_constant<int, 1>{});
+    if (biased) {
+      // neighbours in order: where any two are close, two neighbours are
+#pragma unroll
+      for (int q = 0; q < OWN; ++q)
+        if (expert[q] >= 0) sm.sorted[g][rank[q]] = listed_key(own[q]);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int q = 0; q < OWN; ++q)
+        if (expert[q] >= 0 && rank[q] + 1 < n) {
+          const float k = listed_key(own[q]), next = sm.sorted[g][rank[q] + 1];
+          close = close || k - next <= fmaxf(key_error(k), key_error(next));
+        }
     }
   }
   if (biased && __ballot(close)) {                  // any group of the wave
@@ -273,7 +324,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
     __builtin_amdgcn_wave_barrier();
     for (int j = 0; j < n; ++j) {
       const double c = sm.exact[g][j];
-      const int e = sm.list[g][j].expert;
+      const int e = listed_expert(sm.list[g][j]);
 #pragma unroll
       for (int q = 0; q < OWN; ++q) rank[q] += before(c, e, own[q], expert[q]) ? 1 : 0;
     }
