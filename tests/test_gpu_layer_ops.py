@@ -88,6 +88,38 @@ def test_route_orders_near_ties_in_64_bits():
     _check_route(l.to(dev()), 8, "sigmoid", huge, True, 1.0, "large bias")
 
 
+@pytest.mark.parametrize("T", [5, 6151])
+@pytest.mark.parametrize("E,k,stride,lanes", [(384, 8, 16, 1), (1024, 9, 16, 3), (1024, 32, 64, 31), (896, 10, 64, 9)])
+def test_route_crowded_residues(T, E, k, stride, lanes):
+    """The largest logits at experts of a few residues: far more than k experts lie above any bound by residue."""
+    g = torch.Generator().manual_seed(T + E + k)
+    l = 0.1 * torch.randn(T, E, generator=g)
+    l[:, torch.arange(E) % stride < lanes] += 3.0
+    l[1::3] = l[1::3].round(decimals=1)                   # and many equal ones
+    b = (0.05 * torch.randn(E, generator=g)).to(dev())
+    for dtype in (torch.float32, torch.bfloat16):
+        d = l.to(dtype).to(dev())
+        _check_route(d, k, "softmax", None, True, 1.0, "softmax")
+        _check_route(d, k, "sigmoid", b, True, 1.5, "sigmoid + bias")
+
+
+@pytest.mark.parametrize("E,k", [(384, 8), (9, 9), (100, 10), (1000, 3)])
+def test_route_many_tokens(E, k):
+    g = torch.Generator().manual_seed(E + k)
+    l = torch.randn(6147, E, generator=g)
+    l[torch.rand(6147, E, generator=g) < 0.05] = float("-inf")
+    l[3] = float("nan")
+    l[4] = float("-inf")
+    l[4, E - 1] = float("inf")
+    l[6146] = 0.0
+    b = (0.1 * torch.randn(E, generator=g)).to(dev())
+    _check_route(l.to(dev()), k, "softmax", None, False, 1.0, "softmax")
+    _check_route(l.to(dev()), k, "sigmoid", b, True, 1.0, "sigmoid + bias")
+    wide = torch.full((6147, E + 7), float("inf"), device=dev())   # what lies between the rows is never chosen
+    wide[:, 4:4 + E] = l.to(dev())
+    _check_route(wide[:, 4:4 + E], k, "sigmoid", None, True, 1.0, "strided")
+
+
 def test_route_strided_rows_other_stream_and_refusals():
     wide = torch.randn(50, 512, device=dev())
     _check_route(wide[::2, 64:64 + 96], 5, "softmax", what="strided")

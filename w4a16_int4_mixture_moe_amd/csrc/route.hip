@@ -21,8 +21,8 @@
 //      L = 16; 18 at k = 16, L = 64);
 //   3. each listed expert counts the listed ones that come before it (larger
 //      key, or equal and lower index): its rank, whatever the list's order.
-// A list that overflows (many equal keys) falls back to k passes over the
-// row.
+// A list that overflows is made once more above its own k-th key; if it
+// overflows again (many equal keys) k passes over the row take its place.
 //
 // Order with a bias.  s_e + b_e in 32 bits carries an error of a few 2^-24,
 // enough to swap two experts that nearly tie.  The list's bound is lowered by
@@ -179,6 +179,7 @@ struct RouteSmem {
   uint64_t list[G][CAP + 4];                        // read four at a time, zeros behind the last
   float logit[G][CAP];                              // with a bias
   float sorted[G][CAP];                             // with a bias: the keys in order
+  float kth[G];                                     // of an overflowing list
   double exact[G][CAP];
   int count[G];
 };
@@ -250,31 +251,31 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
   }
   if (biased) bound -= key_error(bound);
   bound = fmaxf(bound, -kMaxFinite);                // fewer lanes than k hold an expert: every live one (NaN: as well)
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) mine += key[i] >= bound ? 1 : 0;
-  int at = group_prefix<L>(mine);
-  if (l == L - 1) sm.count[g] = at + mine;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (key[i] >= bound) {
-      if (at < Smem::CAP) {
-        sm.list[g][at] = listed_as(key[i], i * L + l);
-        if (biased) sm.logit[g][at] = x[i];
-      }
-      ++at;
-    }
-  __builtin_amdgcn_wave_barrier();
-  const int listed = sm.count[g];
-  const int n = min(listed, Smem::CAP);
-  if (l < 4) sm.list[g][n + l] = 0;                 // comes before nothing
-  __builtin_amdgcn_wave_barrier();
-
-  int expert[OWN], rank[OWN];
+  int expert[OWN], rank[OWN], listed, n;
+  uint64_t own[OWN];
   float logit[OWN];
-  bool close = false;
-  {
-    uint64_t own[OWN];
+  // the list, and the ranks in it.  Where it overflows, the k-th of the listed
+  // is a higher bound: once more with that.
+  for (bool again = false;; again = true) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine += key[i] >= bound ? 1 : 0;
+    int at = group_prefix<L>(mine);
+    if (l == L - 1) sm.count[g] = at + mine;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] >= bound) {
+        if (at < Smem::CAP) {
+          sm.list[g][at] = listed_as(key[i], i * L + l);
+          if (biased) sm.logit[g][at] = x[i];
+        }
+        ++at;
+      }
+    __builtin_amdgcn_wave_barrier();
+    listed = sm.count[g];
+    n = min(listed, Smem::CAP);
+    if (l < 4) sm.list[g][n + l] = 0;               // comes before nothing
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int q = 0; q < OWN; ++q) {
       own[q] = sm.list[g][l + q * L];
@@ -296,28 +297,40 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
     };
     if (__ballot(n > L)) count(std::integral_constant<int, OWN>{});   // any group of the wave
     else count(std::integral_constant<int, 1>{});
-    if (biased) {
-      // neighbours in order: where any two are close, two neighbours are
+    if (again || !__ballot(listed > Smem::CAP)) break;
+    if (listed > Smem::CAP) {
 #pragma unroll
       for (int q = 0; q < OWN; ++q)
-        if (expert[q] >= 0) sm.sorted[g][rank[q]] = listed_key(own[q]);
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int q = 0; q < OWN; ++q)
-        if (expert[q] >= 0 && rank[q] + 1 < n) {
-          const float k = listed_key(own[q]), next = sm.sorted[g][rank[q] + 1];
-          close = close || k - next <= fmaxf(key_error(k), key_error(next));
-        }
+        if (rank[q] == p.topk - 1) sm.kth[g] = listed_key(own[q]);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (listed > Smem::CAP) {
+      const float k = sm.kth[g];
+      bound = fmaxf(bound, biased ? k - key_error(k) : k);
     }
   }
+  bool close = false;
+  if (biased) {
+    // neighbours in order: where any two are close, two neighbours are
+#pragma unroll
+    for (int q = 0; q < OWN; ++q)
+      if (expert[q] >= 0) sm.sorted[g][rank[q]] = listed_key(own[q]);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < OWN; ++q)
+      if (expert[q] >= 0 && rank[q] + 1 < n) {
+        const float k = listed_key(own[q]), next = sm.sorted[g][rank[q] + 1];
+        close = close || k - next <= fmaxf(key_error(k), key_error(next));
+      }
+  }
   if (biased && __ballot(close)) {                  // any group of the wave
-    double own[OWN];
+    double exact[OWN];
 #pragma unroll
     for (int q = 0; q < OWN; ++q) {
-      own[q] = -HUGE_VAL;
+      exact[q] = -HUGE_VAL;
       if (expert[q] >= 0) {
-        own[q] = exact_key(logit[q], p.bias[expert[q]]);
-        sm.exact[g][l + q * L] = own[q];
+        exact[q] = exact_key(logit[q], p.bias[expert[q]]);
+        sm.exact[g][l + q * L] = exact[q];
       }
       rank[q] = 0;
     }
@@ -326,7 +339,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
       const double c = sm.exact[g][j];
       const int e = listed_expert(sm.list[g][j]);
 #pragma unroll
-      for (int q = 0; q < OWN; ++q) rank[q] += before(c, e, own[q], expert[q]) ? 1 : 0;
+      for (int q = 0; q < OWN; ++q) rank[q] += before(c, e, exact[q], expert[q]) ? 1 : 0;
     }
   }
   if (__ballot(listed > Smem::CAP)) {
@@ -403,10 +416,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
 // Lanes per token: 16 lanes share every instruction of the search with three
 // other tokens, 64 lanes finish a token sooner; and a 16-lane list stays short
 // only while k is well below 16.  Measured on MI355X, graph replays, 384
-// experts, top 8, 64 / 16 lanes: fp32 sigmoid + bias 4096 tokens 9.6 / 11.1 us,
-// 8192 13.4 / 12.2 us, 16384 22.6 / 17.1 us (1.5 TB/s of logits; an empty
-// launch is about 4.5 us); bf16 softmax 4096 7.6 / 8.0 us, 8192 10.9 / 8.7 us.
-// (Taking the k winners out one by one, 64 lanes: 16384 tokens 25 us.)
+// experts, fp32 sigmoid + bias, 64 / 16 lanes: top 8, 1024 tokens 5.3 / 7.9 us,
+// 4096 7.8 / 8.4, 6144 9.8 / 9.0, 8192 11.2 / 9.1, 16384 19.6 / 13.1 us (2.0
+// TB/s of logits; an empty launch is about 4.5 us); 8192 tokens top 10 12.0 /
+// 10.7, top 12 13.0 / 12.8, top 14 14.4 / 62 us (lists that overflow twice);
+// 6144 tokens top 12 11.4 / 12.7 us; bf16 softmax 8192 tokens 9.4 / 6.9 us.
+// (Taking the k winners out one by one, 64 lanes: 16384 tokens 25 us.  A
+// 16-lane list that went straight to k passes when it overflowed: 8192 tokens
+// top 10 81 us.)  What bounds 16384 tokens now: about 880 vector instructions
+// a wave of four tokens, half of them the keys and the list.
 constexpr int kNarrowMaxTopk = 10;
 constexpr int kNarrowMinTokens = 6144;
 
