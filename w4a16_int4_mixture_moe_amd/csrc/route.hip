@@ -423,8 +423,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
 // 6144 tokens top 12 11.4 / 12.7 us; bf16 softmax 8192 tokens 9.4 / 6.9 us.
 // (Taking the k winners out one by one, 64 lanes: 16384 tokens 25 us.  A
 // 16-lane list that went straight to k passes when it overflowed: 8192 tokens
-// top 10 81 us.)  What bounds 16384 tokens now: about 880 vector instructions
-// a wave of four tokens, half of them the keys and the list.
+// top 10 81 us.)  What 16384 tokens spend: about 880 vector instructions
+// a wave of four tokens, whose issue fills half of the kernel's 10.5 us, and
+// the chains of the rounds and of the list in LDS for the rest.
 constexpr int kNarrowMaxTopk = 10;
 constexpr int kNarrowMinTokens = 6144;
 
