@@ -145,6 +145,22 @@ def test_route_strided_rows_other_stream_and_refusals():
             M.moe_route(wide, k)
 
 
+@pytest.mark.parametrize("T,E,k", [(2**26 + 5, 11, 11), (2**28 + 5, 2, 1)])
+def test_route_more_tokens_than_one_grid_holds(T, E, k):
+    """Past 2^26 (64 lanes a token) or 2^28 tokens (16 lanes) the threads of one launch do not fit 32 bits."""
+    n = 2**20
+    g = torch.Generator().manual_seed(k)
+    block = torch.randn(n, E, generator=g).half().to(dev())
+    logits = block.repeat(T // n + 1, 1)[:T]
+    ref_ids, ref_w = M.moe_route(block, k)
+    _check_route(block[:500].contiguous(), k, "softmax")
+    ids, w = M.moe_route(logits, k)
+    for got, ref in ((ids, ref_ids), (w, ref_w)):
+        whole = got[:T // n * n].view(T // n, n, k)
+        assert all(torch.equal(part, ref) for part in whole)
+        assert torch.equal(got[T // n * n:], ref[:T % n])
+
+
 # ------------------------------------------------------------------ few-token layer
 
 class Layer:

@@ -28,6 +28,7 @@
 // enough to swap two experts that nearly tie.  The list's bound is lowered by
 // that error, and where two of its keys are closer than it the group ranks
 // the list again by s_e + b_e in 64 bits.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -429,21 +430,43 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
 constexpr int kNarrowMaxTopk = 10;
 constexpr int kNarrowMinTokens = 6144;
 
+// Threads of one launch are counted in 32 bits, and a grid past them wraps
+// without an error: 2^26 tokens of 64 lanes would be no workgroup at all.
+// Longer batches go in pieces, each far below.
+constexpr int kLaunchTokens = 1 << 24;
+
 template <typename T, bool kSigmoid>
-hipError_t launch_typed(const RouteArgs& a, hipStream_t stream) {
-  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens;
-  const int lanes = narrow ? 16 : 64;
+hipError_t launch_piece(const RouteArgs& a, int lanes, hipStream_t stream) {
   const int v = (a.E + lanes - 1) / lanes;
   const int per = kRouteThreads / lanes;
   const dim3 grid((unsigned)((a.T + per - 1) / per)), block(kRouteThreads);
   // keys per lane rounded up to a built width
-#define W4A16_ROUTE_CASE(L_, V_)                                                                  if (lanes == L_ && v <= V_) {                                                                     hipLaunchKernelGGL((route_kernel<T, L_, V_, kSigmoid>), grid, block, 0, stream, a);              return hipGetLastError();                                                                     }
+#define W4A16_ROUTE_CASE(L_, V_)                                                         \
+  if (lanes == L_ && v <= V_) {                                                          \
+    hipLaunchKernelGGL((route_kernel<T, L_, V_, kSigmoid>), grid, block, 0, stream, a);  \
+    return hipGetLastError();                                                            \
+  }
   W4A16_ROUTE_CASE(16, 8) W4A16_ROUTE_CASE(16, 16) W4A16_ROUTE_CASE(16, 24) W4A16_ROUTE_CASE(16, 32)
   W4A16_ROUTE_CASE(16, 56) W4A16_ROUTE_CASE(16, 64)
   W4A16_ROUTE_CASE(64, 2) W4A16_ROUTE_CASE(64, 4) W4A16_ROUTE_CASE(64, 6) W4A16_ROUTE_CASE(64, 8)
   W4A16_ROUTE_CASE(64, 14) W4A16_ROUTE_CASE(64, 16)
 #undef W4A16_ROUTE_CASE
   return hipErrorInvalidValue;
+}
+
+template <typename T, bool kSigmoid>
+hipError_t launch_typed(const RouteArgs& a, hipStream_t stream) {
+  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens;
+  for (int64_t t = 0; t < a.T; t += kLaunchTokens) {
+    RouteArgs piece = a;
+    piece.logits = static_cast<const T*>(a.logits) + t * a.row_stride;
+    piece.T = (int32_t)std::min((int64_t)kLaunchTokens, a.T - t);
+    piece.ids = a.ids + t * a.topk;
+    piece.weights = a.weights + t * a.topk;
+    const hipError_t e = launch_piece<T, kSigmoid>(piece, narrow ? 16 : 64, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
