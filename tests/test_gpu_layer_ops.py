@@ -161,6 +161,25 @@ def test_route_more_tokens_than_one_grid_holds(T, E, k):
         assert torch.equal(got[T // n * n:], ref[:T % n])
 
 
+def test_sizes_past_32_bits_are_refused(layers):
+    """Cut to 32 bits each of these would be a small call; nothing is written, so nothing is launched."""
+    big = 2**32
+    for T, E in ((big + 4, 1), (1, big + 8), (2**31, 1)):
+        with pytest.raises(ValueError, match="32-bit"):
+            M.moe_route(torch.empty(T, E, dtype=torch.float16, device=dev()), 1)
+    lay = layers["int4"]
+    x = torch.zeros(1, lay.H, dtype=torch.bfloat16, device=dev())
+    ids = torch.empty(1, big + 1, dtype=torch.int32, device=dev())
+    with pytest.raises(ValueError, match="32-bit"):
+        M.moe_few_tokens(x, lay.p1, lay.p2, ids, ids.view(torch.float32))
+    del ids
+    packed, _ = _mx_weight(1, 16, 128, 2)
+    rows = M.MXRows(torch.zeros(8, 64, dtype=torch.uint8, device=dev()), torch.zeros(8, 4, dtype=torch.uint8, device=dev()))
+    with pytest.raises(ValueError, match="32-bit"):
+        M.grouped_mxfp4_masked(rows, packed, torch.zeros(1, dtype=torch.int32, device=dev()), big + 8)
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ few-token layer
 
 class Layer:

@@ -167,6 +167,20 @@ def test_binding_refuses_host_tensors():
         W.moe_route(x.numpy(), 2)
 
 
+@pytest.mark.parametrize("make", [W.weight_desc, W.mxfp4_weight_desc])
+def test_binding_refuses_sizes_past_32_bits(L, make):
+    """Cut to 32 bits these would be the small weight [1, 64, 128]."""
+    big = 2**32
+    for E, N, K in ((big + 1, 64, 128), (1, big + 64, 128), (1, 64, big + 128), (1 - big, 64, 128)):
+        with pytest.raises(ValueError, match="32-bit"):
+            make(E, N, K)
+    g = make(1, 128, 128, gate_up=True)
+    p = W.PackedW4(g, None, None)
+    assert W.few_tokens_workspace_bytes(p, 4, 2) > 0
+    for T, k in ((big + 4, 2), (4, big + 2), (4 - big, 2), (-1, 2), (4, -1)):
+        assert W.few_tokens_workspace_bytes(p, T, k) == 0
+
+
 def test_header_constants_match_the_binding(tmp_path):
     import os
     import re

@@ -49,6 +49,13 @@ def _launch(dev: torch.device, fn, *args) -> None:
             check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
 
 
+def _need_32bit(**sizes: int) -> None:
+    """A size past 32 bits would lose its high bits on the way into the library."""
+    for name, n in sizes.items():
+        if not -2**31 <= n < 2**31:
+            raise ValueError(f"{name} = {n} is not a 32-bit size")
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -93,6 +100,7 @@ class PackedW4:
 
 
 def weight_desc(E: int, N: int, K: int, gate_up: bool = False) -> WeightDesc:
+    _need_32bit(E=E, N=N, K=K)
     d = WeightDesc()
     init = load().w4a16_weight_desc_init_gate_up if gate_up else load().w4a16_weight_desc_init
     check(init(E, N, K, ctypes.byref(d)))
@@ -369,6 +377,7 @@ class MXRows:
 
 
 def mxfp4_weight_desc(E: int, N: int, K: int, gate_up: bool = False) -> WeightDesc:
+    _need_32bit(E=E, N=N, K=K)
     d = WeightDesc()
     init = load().w4a16_mxfp4_weight_desc_init_gate_up if gate_up else load().w4a16_mxfp4_weight_desc_init
     check(init(E, N, K, ctypes.byref(d)))
@@ -603,6 +612,7 @@ def grouped_mxfp4_masked(a: MXRows, packed: PackedW4, masked_m: torch.Tensor, ex
     group's count are left as they are (zero in an out made here)."""
     if packed.E == 0 or a.rows % packed.E or a.rows == 0:
         raise ValueError(f"{a.rows} rows are not a whole number of rows for each of {packed.E} groups")
+    _need_32bit(max_m=a.rows // packed.E, expected_m=int(expected_m))
     out = _grouped_mx_args(a, packed, masked_m, "masked_m", a.rows, out)
     if masked_m.shape[0] != packed.E:
         raise ValueError(f"masked_m has {masked_m.shape[0]} entries, the weight {packed.E} experts")
@@ -632,6 +642,7 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
     if logits.dim() != 2:
         raise ValueError(f"logits must have 2 dims, got {tuple(logits.shape)}")
     T, E = logits.shape
+    _need_32bit(T=T, E=E)
     if E > 1 and logits.stride(1) != 1:
         raise ValueError("the experts of a row must be contiguous")
     if scoring not in _SCORINGS:
@@ -653,6 +664,8 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
 
 def few_tokens_workspace_bytes(gate_up: PackedW4, T: int, topk: int) -> int:
     """Workspace bytes of moe_few_tokens (0 where the call refuses T, topk)."""
+    if max(T, topk) >= 2**31 or min(T, topk) < 0:
+        return 0
     return int(load().w4a16_moe_few_tokens_workspace_bytes(ctypes.byref(gate_up.desc), T, topk))
 
 
@@ -674,6 +687,7 @@ def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids:
         raise ValueError(f"topk_ids {tuple(topk_ids.shape)} / topk_weights {tuple(topk_weights.shape)} "
                          f"do not match {T} tokens")
     k = topk_ids.shape[1]
+    _need_32bit(T=T, topk=k)
     dev = x.device
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
