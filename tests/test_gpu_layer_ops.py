@@ -145,6 +145,32 @@ def test_route_strided_rows_other_stream_and_refusals():
             M.moe_route(wide, k)
 
 
+@pytest.mark.parametrize("T", [3, 6147])
+def test_route_scores_below_the_normal_range(T):
+    """Scores that fp32 holds in a few bits or not at all, brought back into range by the sum or the scale."""
+    lows = torch.linspace(-78.0, -130.0, 53)
+    l = torch.full((T, 64), float("-inf"))
+    l[0, :53] = lows
+    l[1, :53] = lows.flip(0)
+    l[2, 7:11] = -100.0
+    l[3:, 3], l[3:, 60] = -95.0, -103.0
+    d = l.to(dev())
+    v = l.double().numpy()
+    bias = torch.zeros(64, device=dev())
+    for scoring, renorm, b, scale in (("sigmoid", True, None, 1.0), ("sigmoid", True, bias, 2.5),
+                                      ("sigmoid", False, None, 2.0**70), ("softmax", True, None, 2.0**100),
+                                      ("softmax", False, None, 2.0**100)):
+        ids, w = M.moe_route(d, 4, scoring=scoring, bias=b, renormalize=renorm, scale=scale)
+        ref_ids, ref_w, _ = LO.route(v, 4, scoring, None if b is None else np.zeros(64), renorm, scale)
+        np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids)
+        got = w.double().cpu().numpy()
+        # a score within 5 units of 2^-24 (difference, exp, sum and division round once each, exp twice), the
+        # chosen scores' sum as far, one rounding of the weight, which may be a subnormal; a difference from the
+        # maximum is exact here (all are whole numbers)
+        tol = 11 * 2.0 ** -24 * np.abs(ref_w) + 2.0 ** -150
+        assert (np.abs(got - ref_w) <= tol).all(), (scoring, renorm, float((np.abs(got - ref_w) / tol).max()))
+
+
 @pytest.mark.parametrize("T,E,k", [(2**26 + 5, 11, 11), (2**28 + 5, 2, 1)])
 def test_route_more_tokens_than_one_grid_holds(T, E, k):
     """Past 2^26 (64 lanes a token) or 2^28 tokens (16 lanes) the threads of one launch do not fit 32 bits."""

@@ -127,10 +127,22 @@ __device__ __forceinline__ int group_prefix(int v) {
   return s - v;
 }
 
-// 1 / (1 + exp(-x)), without overflow at either end, within a few 2^-24
-__device__ __forceinline__ float sigmoid32(float x) {
+// Weights before their division and scale: exp(x) of x <= 0, and
+// 1 / (1 + exp(-x)) without overflow at either end.  Evaluated in 32 bits,
+// within a few 2^-24, down to exp(-80); below that in 64, since an fp32 result
+// would soon be a subnormal of fewer bits (2 % off at exp(-100)), which a
+// division by a small sum or a large scale brings back into range.
+constexpr float kExp32 = -80.f;
+
+__device__ __forceinline__ double exp_weight(float x) {
+  if (x < kExp32) return exp((double)x);
+  return (double)expf(x);
+}
+
+__device__ __forceinline__ double sigmoid_weight(float x) {
+  if (x < kExp32) return exp((double)x);                // 1 + exp(x) is 1 in 64 bits
   const float z = expf(-fabsf(x));
-  return (x >= 0.f ? 1.f : z) / (1.f + z);
+  return (double)((x >= 0.f ? 1.f : z) / (1.f + z));
 }
 
 // the same within 2^-22 absolutely (exp and reciprocal instructions; the
@@ -389,13 +401,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
   }
 
   // weights of the chosen, each by the lane that ranked it; sums in 64 bits
-  float w[OWN];
-  double chosen = 0.0;
+  double w[OWN], chosen = 0.0;
 #pragma unroll
   for (int q = 0; q < OWN; ++q) {
-    w[q] = 0.f;
-    if (expert[q] >= 0 && rank[q] < p.topk) w[q] = kSigmoid ? sigmoid32(logit[q]) : expf(logit[q] - top);
-    chosen += (double)w[q];
+    w[q] = 0.0;
+    if (expert[q] >= 0 && rank[q] < p.topk) w[q] = kSigmoid ? sigmoid_weight(logit[q]) : exp_weight(logit[q] - top);
+    chosen += w[q];
   }
   if (p.renorm) sum = group_sum<L>(chosen) + (kSigmoid ? 1e-20 : 0.0);
   if (!real) return;
@@ -404,7 +415,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
   for (int q = 0; q < OWN; ++q) {
     if (expert[q] >= 0 && rank[q] < p.topk) {
       p.ids[t * p.topk + rank[q]] = expert[q];
-      p.weights[t * p.topk + rank[q]] = (float)((divide ? (double)w[q] / sum : (double)w[q]) * (double)p.scale);
+      p.weights[t * p.topk + rank[q]] = (float)((divide ? w[q] / sum : w[q]) * (double)p.scale);
     }
   }
   // slots for which no expert was left (an overflowing list never leaves any)
