@@ -572,7 +572,8 @@ w4a16_status w4a16_mxfp4_dequant(const w4a16_weight_desc* desc, const void* pack
  * Masked: rows = E * max_m; a count masked_m[g] outside [0, max_m] is taken
  * as the nearer end; expected_m (host, > 0) is taken as in
  * w4a16_grouped_masked, but the one tile built does not depend on it.
- * Sizes: rows * K / 2 below 4 GiB (ERR_SHAPE).
+ * Sizes: rows * K / 2 below 4 GiB, and 128-row blocks (m_rows / 128, or
+ * E * ceil(max_m / 128)) times ceil(N / 256) below 2^24 (ERR_SHAPE).
  * Pointers: packed_w, packed_s, a_codes, out 16-byte aligned, a_scales 4.
  * Errors: ERR_ARG, ERR_LAYOUT (not an MXFP4 weight), ERR_SHAPE, ERR_HIP. */
 w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,

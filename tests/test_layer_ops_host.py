@@ -157,6 +157,15 @@ def test_grouped_mxfp4_refusals(L):
     assert m(max_m=1 << 23) == -2 and m(max_m=1 << 29) == -2
 
 
+def test_grouped_mxfp4_refuses_grids_past_32_bits(L):
+    """2^24 tiles are 2^32 threads, a launch that would wrap to no workgroup at all."""
+    for E, N in ((1 << 24, 16), (1 << 22, 1024), ((1 << 23) + 1, 272)):
+        d = W.mxfp4_weight_desc(E, N, 128)
+        assert L.w4a16_mxfp4_grouped_masked(ctypes.byref(d), P, P, P, P, 1, P, 1, P, None) == -2
+    d = W.mxfp4_weight_desc(1, 1 << 18, 128)                             # 2^10 tiles a block
+    assert L.w4a16_mxfp4_grouped_contiguous(ctypes.byref(d), P, P, P, P, 128 << 14, P, P, None) == -2
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(2, 8)
     with pytest.raises(ValueError, match="GPU"):

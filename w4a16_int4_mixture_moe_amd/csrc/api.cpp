@@ -1068,10 +1068,14 @@ w4a16_status check_mx_grouped(const w4a16_weight_desc* desc, const void* packed_
   return W4A16_OK;
 }
 
-w4a16_status check_mx_rows(int64_t rows, int32_t K) {
+// blocks: of 128 rows, each with a 256-thread workgroup for 256 weight rows;
+// a launch whose threads pass 32 bits would wrap to a smaller one
+w4a16_status check_mx_rows(int64_t rows, int32_t N, int32_t K, int64_t blocks) {
   if (rows >= INT32_MAX / 2) return fail(W4A16_ERR_SHAPE, "%lld rows are too many", (long long)rows);
   if (rows * (int64_t)(K / 2) >= ((int64_t)1 << 32))
     return fail(W4A16_ERR_SHAPE, "activation codes exceed 4 GiB (32-bit row offsets)");
+  if (blocks * (((int64_t)N + 255) / 256) >= (1 << 24))
+    return fail(W4A16_ERR_SHAPE, "%lld blocks of rows x N = %d: 2^24 tiles or more", (long long)blocks, N);
   return W4A16_OK;
 }
 
@@ -1357,7 +1361,7 @@ w4a16_status w4a16_mxfp4_grouped_contiguous(const w4a16_weight_desc* desc, const
   if (m_rows > 0 && (!a_codes || !a_scales || !m_indices || !out)) return fail(W4A16_ERR_ARG, "NULL pointer argument");
   if (m_rows % 128)
     return fail(W4A16_ERR_SHAPE, "m_rows=%lld is not a multiple of 128 (segments are 128-row aligned)", (long long)m_rows);
-  st = check_mx_rows(m_rows, desc->K);
+  st = check_mx_rows(m_rows, desc->N, desc->K, m_rows / 128);
   if (st != W4A16_OK) return st;
   if (m_rows == 0) return W4A16_OK;
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, reinterpret_cast<const uint16_t*>(a_codes), out, 4, 4);
@@ -1379,7 +1383,7 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
   if (expected_m <= 0) return fail(W4A16_ERR_ARG, "expected_m must be positive");
   if (!a_codes || !a_scales || !masked_m || !out) return fail(W4A16_ERR_ARG, "NULL pointer argument");
   if ((int64_t)desc->E * max_m >= INT32_MAX / 2) return fail(W4A16_ERR_SHAPE, "E * max_m too large");
-  st = check_mx_rows((int64_t)desc->E * max_m, desc->K);
+  st = check_mx_rows((int64_t)desc->E * max_m, desc->N, desc->K, desc->E * (((int64_t)max_m + 127) / 128));
   if (st != W4A16_OK) return st;
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, reinterpret_cast<const uint16_t*>(a_codes), out, 4, 4);
   p.a_scale = a_scales;

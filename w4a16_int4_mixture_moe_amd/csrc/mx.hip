@@ -177,7 +177,7 @@ hipError_t launch_mx_quant_pack(const void* w, bool fp32, int32_t E, int32_t N, 
                                 uint32_t* pw, uint8_t* ps, hipStream_t stream) {
   const int64_t tiles = (int64_t)E * (N / 16) * (K / 128);
   const int64_t grid = (tiles + 3) / 4;
-  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (grid > UINT32_MAX / 256) return hipErrorInvalidConfiguration;   // threads past 32 bits wrap, without an error
   if (fp32)
     hipLaunchKernelGGL(mx_quant_pack_kernel<uint32_t>, dim3((unsigned)grid), dim3(256), 0, stream,
                        static_cast<const uint32_t*>(w), tiles, N, K, gate_up, pw, ps);
@@ -220,7 +220,7 @@ hipError_t launch_mx_dequant(const uint32_t* pw, const uint8_t* ps, int32_t E, i
                              uint16_t* out, hipStream_t stream) {
   const int64_t tiles = (int64_t)E * (N / 16) * (K / 128);
   const int64_t grid = (tiles + 3) / 4;
-  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (grid > UINT32_MAX / 256) return hipErrorInvalidConfiguration;   // threads past 32 bits wrap, without an error
   hipLaunchKernelGGL(mx_dequant_kernel, dim3((unsigned)grid), dim3(256), 0, stream, pw, ps, tiles, N, K, gate_up, out);
   return hipGetLastError();
 }

@@ -307,7 +307,7 @@ hipError_t launch_mx_tile(int route, const GemmParams& p, hipStream_t stream) {
   // measured no faster: 16384 rows of 48 experts 358 - 404 us against 360.)
   const int64_t grid = (int64_t)p.grid_blocks * q.n_tiles;
   if (grid <= 0) return hipSuccess;
-  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (grid > UINT32_MAX / kThreads) return hipErrorInvalidConfiguration;   // threads past 32 bits wrap, without an error
   if (route == kRouteContiguous)
     hipLaunchKernelGGL(mx_tile_kernel<kRouteContiguous>, dim3((unsigned)grid), dim3(kThreads), 0, stream, q);
   else
