@@ -499,6 +499,32 @@ def test_quant_pack_refusals():
                                   torch.zeros(1, 16, 4, dtype=torch.bfloat16, device=dev())))
 
 
+@pytest.mark.parametrize("kind,E,N,K", [("int4", 9, 65536, 65536), ("mxfp4", 33, 65536, 65536)])
+def test_packing_past_one_grid(kind, E, N, K):
+    """More words than the threads of one launch can be (2^32): every expert is packed as it is by itself."""
+    if torch.cuda.mem_get_info()[0] < 200 * 2**30:
+        pytest.skip("needs 200 GiB of free GPU memory")
+    g = torch.Generator(device=dev()).manual_seed(E)
+    codes = torch.randint(0, 256, (1, N, K // 2), generator=g, dtype=torch.uint8, device=dev())
+    if kind == "int4":
+        one = torch.cat((codes & 15, codes >> 4), dim=2)
+        scales = torch.randn(1, N, K // 32, generator=g, device=dev()).to(torch.bfloat16)
+        pack = M.pack_w4
+    else:
+        one, pack = codes, M.pack_mxfp4
+        scales = torch.randint(100, 140, (1, N, K // 32), generator=g, dtype=torch.uint8, device=dev())
+    ref = pack(one, scales)
+    many = one.new_empty(E, *one.shape[1:])
+    many[:] = one
+    p = pack(many, scales.expand(E, -1, -1).contiguous())
+    del many
+    for e in range(E):
+        assert torch.equal(p.w.view(E, -1)[e], ref.w), e
+        assert torch.equal(p.s.view(E, -1)[e], ref.s), e
+    del p, ref, one, codes, scales
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ grouped MXFP4
 
 def _mx_weight(E, N, K, seed, gate_up=False):

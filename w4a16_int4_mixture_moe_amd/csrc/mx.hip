@@ -29,6 +29,8 @@
 // does the rounding).
 #include <type_traits>
 
+#include <algorithm>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "tile_common.hpp"
@@ -230,8 +232,9 @@ hipError_t launch_mx_dequant(const uint32_t* pw, const uint8_t* ps, int32_t E, i
 // scale byte.
 __global__ __launch_bounds__(256) void mx_pack_kernel(const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                                                        int32_t E, int32_t N, int32_t K, int32_t gate_up,
-                                                       uint4* __restrict__ pw, uint8_t* __restrict__ ps) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+                                                       uint4* __restrict__ pw, uint8_t* __restrict__ ps,
+                                                       int64_t first) {
+  const int64_t i = first + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int KC = K / 128, NT = N / 16;
   const int64_t total = (int64_t)E * NT * KC * kWave;
   if (i >= total) return;
@@ -250,11 +253,16 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(const uint8_t* __restrict_
 hipError_t launch_mx_pack(const uint8_t* w, const uint8_t* s, int32_t E, int32_t N, int32_t K, int32_t gate_up,
                           uint4* pw, uint8_t* ps, hipStream_t stream) {
   const int64_t total = (int64_t)E * (N / 16) * (K / 128) * kWave;
-  if (total == 0) return hipSuccess;
-  const int64_t grid = (total + 255) / 256;
-  if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(mx_pack_kernel, dim3((unsigned)grid), dim3(256), 0, stream, w, s, E, N, K, gate_up, pw, ps);
-  return hipGetLastError();
+  // in pieces: threads of one launch past 32 bits wrap, without an error
+  constexpr int64_t kLaunch = (int64_t)1 << 30;
+  for (int64_t first = 0; first < total; first += kLaunch) {
+    const int64_t grid = (std::min(kLaunch, total - first) + 255) / 256;
+    hipLaunchKernelGGL(mx_pack_kernel, dim3((unsigned)grid), dim3(256), 0, stream, w, s, E, N, K, gate_up, pw, ps,
+                       first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ------------------------------------------------------------ GEMM

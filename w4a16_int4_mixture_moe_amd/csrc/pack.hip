@@ -7,6 +7,8 @@
 // kernel variant: word j of lane l = 16 g + i of (tile, chunk c) holds row
 // 16 tile + i, K = 128 c + 32 g + 8 j .. + 7, so one 16-byte load per lane
 // brings one full scale group of one row.
+#include <algorithm>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -15,8 +17,8 @@ namespace w4a16 {
 __global__ __launch_bounds__(256) void pack_w_kernel(const uint8_t* __restrict__ codes, int32_t N,
                                                      int32_t K, int32_t NT, int32_t KC,
                                                      int32_t gate_up, int64_t total_words,
-                                                     uint32_t* __restrict__ packed_w) {
-  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+                                                     uint32_t* __restrict__ packed_w, int64_t first) {
+  const int64_t idx = first + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= total_words) return;
   const int j = (int)(idx & 3);
   const int l = (int)((idx >> 2) & 63);
@@ -41,10 +43,10 @@ __global__ __launch_bounds__(256) void pack_w_kernel(const uint8_t* __restrict__
 __global__ __launch_bounds__(256) void pack_s_kernel(const uint16_t* __restrict__ scales,
                                                      int32_t N, int32_t K, int32_t NT,
                                                      int32_t KC, int32_t gate_up, int64_t total,
-                                                     uint32_t* __restrict__ packed_s) {
+                                                     uint32_t* __restrict__ packed_s, int64_t first) {
   // output word index = ((e * NT + tile) * KC2 + m) * 64 + lane; the word
   // holds the lane's scale for chunk 2m (low half) and 2m + 1 (high half)
-  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t idx = first + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= total) return;
   const int KC2 = (KC + 1) / 2;
   const int l = (int)(idx & 63);
@@ -61,19 +63,31 @@ __global__ __launch_bounds__(256) void pack_s_kernel(const uint16_t* __restrict_
   packed_s[idx] = lo | (hi << 16);
 }
 
+// Words of one launch: its threads are counted in 32 bits, and more would wrap
+// without an error (2^32 words are 2^35 codes).
+constexpr int64_t kLaunchWords = (int64_t)1 << 30;
+
 hipError_t launch_pack(const uint8_t* codes, const uint16_t* scales, int32_t E, int32_t N,
                        int32_t K, int32_t KC, int32_t gate_up, uint32_t* packed_w,
                        uint32_t* packed_s, hipStream_t stream) {
   const int32_t NT = N / kRowTile;
   const int64_t words = (int64_t)E * NT * KC * 256;
   const int64_t sents = (int64_t)E * NT * ((KC + 1) / 2) * 64;
-  hipLaunchKernelGGL(pack_w_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream,
-                     codes, N, K, NT, KC, gate_up, words, packed_w);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(pack_s_kernel, dim3((unsigned)((sents + 255) / 256)), dim3(256), 0, stream,
-                     scales, N, K, NT, KC, gate_up, sents, packed_s);
-  return hipGetLastError();
+  for (int64_t first = 0; first < words; first += kLaunchWords) {
+    const int64_t n = std::min(kLaunchWords, words - first);
+    hipLaunchKernelGGL(pack_w_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                       codes, N, K, NT, KC, gate_up, words, packed_w, first);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  for (int64_t first = 0; first < sents; first += kLaunchWords) {
+    const int64_t n = std::min(kLaunchWords, sents - first);
+    hipLaunchKernelGGL(pack_s_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                       scales, N, K, NT, KC, gate_up, sents, packed_s, first);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace w4a16
