@@ -629,6 +629,7 @@ w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32
 #define W4A16_FEW_MAX_TOKENS 64
 #define W4A16_FEW_MAX_SLOTS 1024   /* T * topk */
 #define W4A16_FEW_MAX_EXPERTS 1024
+#define W4A16_FEW_MAX_FIRST_EXPERT (1 << 30)
 
 /* x bf16 [T, H] -> out bf16 [T, H],
  *   out[t] = sum over j with first_expert <= topk_ids[t][j] < first_expert + E
@@ -643,7 +644,9 @@ w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32
  * not initialised; its contents are the call's own until it has finished.
  * out must not overlap any input.
  * Sizes: T <= W4A16_FEW_MAX_TOKENS, T * topk <= W4A16_FEW_MAX_SLOTS,
- * E <= W4A16_FEW_MAX_EXPERTS, H and I <= 2^24 (ERR_SHAPE; larger batches take w4a16_moe_align and the GEMM calls).
+ * E <= W4A16_FEW_MAX_EXPERTS, H and I <= 2^24 (ERR_SHAPE; larger batches take
+ * w4a16_moe_align and the GEMM calls); 0 <= first_expert <=
+ * W4A16_FEW_MAX_FIRST_EXPERT (ERR_ARG).
  * Pointers 16-byte aligned (topk_ids, topk_weights: 4).
  * Errors: ERR_ARG, ERR_LAYOUT (packing), ERR_SHAPE, ERR_WORKSPACE, ERR_HIP. */
 w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* gate_up_w, const void* gate_up_s,

@@ -331,6 +331,19 @@ def test_few_tokens_empty_and_refusals(layers):
             M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, first_expert=first)
 
 
+def test_few_tokens_first_expert_limit(layers):
+    lay = layers["int4"]
+    x, ids, wt = _tokens(5, 3, 6, lay.H, 12)
+    top = 2**30
+    lay.check(x, ids + np.int32(top), wt, top, "last first expert")
+    for low in (np.iinfo(np.int32).min, np.iinfo(np.int32).min + 5, -1, 0, top - 1):      # below the range, however far
+        assert not lay.check(x, np.full_like(ids, low), wt, top, "below").any()
+    dx, di, dw = to_dev_bf16(x), to_dev(ids), to_dev(wt)
+    for first in (top + 1, 2**31 - 1):
+        with pytest.raises(ValueError, match="first_expert"):
+            M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, first_expert=first)
+
+
 def test_few_tokens_agrees_with_the_routed_path(layers):
     """align + fused gate/up + down on the same inputs: the same h up to its
     extra bf16 roundings of gate and up, the same sums."""

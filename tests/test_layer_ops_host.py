@@ -176,6 +176,19 @@ def test_binding_refuses_host_tensors():
         W.moe_route(x.numpy(), 2)
 
 
+def test_few_tokens_first_expert_limit(L):
+    """The header's limit, the library's and the binding's are one number."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "w4a16_moe.h")).read()
+    shift = int(re.search(r"#define W4A16_FEW_MAX_FIRST_EXPERT \(1 << (\d+)\)", src).group(1))
+    assert _lib.FEW_MAX_FIRST_EXPERT == 1 << shift
+    g, d = _pair()
+    for first, status in ((1 << shift, 0), ((1 << shift) + 1, -1), (2**31 - 1, -1)):
+        assert L.w4a16_moe_few_tokens(ctypes.byref(g), P, P, ctypes.byref(d), P, P, None, 0, 8, None, None, first, None,
+                                      None, 0, None) == status
+
+
 @pytest.mark.parametrize("make", [W.weight_desc, W.mxfp4_weight_desc])
 def test_binding_refuses_sizes_past_32_bits(L, make):
     """Cut to 32 bits these would be the small weight [1, 64, 128]."""

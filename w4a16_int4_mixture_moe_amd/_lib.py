@@ -39,6 +39,7 @@ A_TOKEN, A_SLOT, A_SORTED = 0, 1, 2   # W4A16_A_TOKEN / _SLOT / _SORTED
 ROUTE_INDEXED, ROUTE_CONTIGUOUS, ROUTE_MASKED = 0, 1, 2   # W4A16_ROUTE_*
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2                # W4A16_DTYPE_*
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1                       # W4A16_SCORE_*
+FEW_MAX_FIRST_EXPERT = 1 << 30                            # W4A16_FEW_MAX_FIRST_EXPERT
 
 
 class Config(ctypes.Structure):

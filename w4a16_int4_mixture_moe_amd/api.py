@@ -32,7 +32,7 @@ from typing import Optional
 import torch
 
 from ._lib import (A_SLOT, A_SORTED, A_TOKEN, DESC_GATE_UP, DESC_MXFP4, DTYPE_BF16, DTYPE_F16, DTYPE_F32,
-                   ROUTE_CONTIGUOUS, ROUTE_INDEXED, ROUTE_MASKED, SCORE_SIGMOID, SCORE_SOFTMAX, Config,
+                   FEW_MAX_FIRST_EXPERT, ROUTE_CONTIGUOUS, ROUTE_INDEXED, ROUTE_MASKED, SCORE_SIGMOID, SCORE_SOFTMAX, Config,
                    IndexedRouting, W4A16Error, WeightDesc, check, load)
 
 
@@ -701,8 +701,8 @@ def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids:
             workspace = torch.empty(nws, dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", (torch.uint8,))
-    if not 0 <= first_expert < 2**31:
-        raise ValueError(f"first_expert = {first_expert} is not a 32-bit index")
+    if not 0 <= first_expert <= FEW_MAX_FIRST_EXPERT:
+        raise ValueError(f"first_expert = {first_expert} is outside [0, {FEW_MAX_FIRST_EXPERT}]")
     _same_device(x, gate_up=gate_up.w, gate_up_scales=gate_up.s, down=down.w, down_scales=down.s, topk_ids=topk_ids,
                  topk_weights=topk_weights, out=out, workspace=workspace)
     _launch(dev, load().w4a16_moe_few_tokens, ctypes.byref(gate_up.desc), gate_up.w.data_ptr(),

@@ -1457,8 +1457,9 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
                 gate_up->K, down->E, down->N, down->K);
   if (T < 0 || topk <= 0 || first_expert < 0)
     return fail(W4A16_ERR_ARG, "bad sizes T=%d topk=%d first_expert=%d", T, topk, first_expert);
-  // id - first_expert must not wrap round for any 32-bit id
-  if (first_expert > (1 << 30)) return fail(W4A16_ERR_ARG, "first_expert = %d too large", first_expert);
+  // id - first_expert, modulo 2^32, lies in [0, E) for no id below first_expert
+  if (first_expert > W4A16_FEW_MAX_FIRST_EXPERT)
+    return fail(W4A16_ERR_ARG, "first_expert = %d above %d", first_expert, W4A16_FEW_MAX_FIRST_EXPERT);
   if (gate_up->K > kFewMaxWidth || down->K > kFewMaxWidth)
     return fail(W4A16_ERR_SHAPE, "widths H = %d, I = %d: at most %d", gate_up->K, down->K, kFewMaxWidth);
   if (gate_up->E > W4A16_FEW_MAX_EXPERTS)

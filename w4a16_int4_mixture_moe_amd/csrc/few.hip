@@ -131,17 +131,17 @@ __device__ __forceinline__ int find_blocks(const FewParams& p, GateUpSmem& sm) {
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int S = p.T * p.topk;
   static_assert(kFewMaxExperts == 2 * kFewThreads, "two experts a thread");
-  int expert[2];
+  uint32_t expert[2];                                   // id - first: from E upwards, not held here
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = tid + q * kFewThreads;
-    expert[q] = i < S ? p.topk_ids[i] - p.first : -1;
+    expert[q] = i < S ? (uint32_t)p.topk_ids[i] - (uint32_t)p.first : ~0u;
     sm.tokens[i] = 0;
   }
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q)
-    if ((unsigned)expert[q] < (unsigned)p.E)            // bits, not a sum: the order of the updates is nothing
+    if (expert[q] < (uint32_t)p.E)                      // bits, not a sum: the order of the updates is nothing
       atomicOr(&sm.tokens[expert[q]], 1ull << ((tid + q * kFewThreads) / p.topk));
   __syncthreads();
   // blocks (high half) and rows (low half) of the experts before this thread's two
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_gate_up_kernel(co
 #pragma unroll 4
         for (int j = 0; j < p.topk; ++j) {
           const float wt = wts[j];
-          row.weight += ids[j] - p.first == blk.expert ? wt : 0.f;
+          row.weight += ids[j] == p.first + blk.expert ? wt : 0.f;
         }
       }
       p.rows[b * 16 + r] = row;
