@@ -331,6 +331,78 @@ def test_few_tokens_empty_and_refusals(layers):
             M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw, first_expert=first)
 
 
+def _few_constant(name):
+    """A launch rule's constant, from the kernel's source."""
+    import re
+    src = os.path.join(os.path.dirname(M.__file__), "csrc", "few.hip")
+    return int(re.search(rf"constexpr int {name} = (\d+);", open(src).read()).group(1))
+
+
+def _blocks(ids, first, E):
+    """Blocks of 16 rows of the local experts (a token counts once an expert)."""
+    return sum(-(-int((ids == first + e).any(1).sum()) // 16) for e in range(E))
+
+
+@pytest.mark.parametrize("kind,H,I", [("int4", 416, 2048), ("mxfp4", 384, 2048), ("int4", 1280, 1696)])
+def test_few_tokens_several_items_a_workgroup(kind, H, I):
+    """More than two rounds of gate/up items, of blocks with unequal row counts: items follow each other in a
+    workgroup with loads in flight, and both buffers of partial sums are used again."""
+    lay = Layer(kind, 4, H, I, H)
+    x, ids, wt = _tokens(64, 4, 6, H, I)                     # experts 1..4 of 6
+    ids[:, 3] = np.where(ids[:, 3] == 2, -1, ids[:, 3])
+    ids[40:][ids[40:] == 4] = 0
+    blocks = _blocks(ids, 1, 4)
+    counts = {int((ids == e).any(1).sum()) % 16 for e in range(1, 5)}
+    assert blocks * (I // 16) > 2 * _few_constant("kFewGroups") and len(counts) > 1
+    lay.check(x, ids, wt, 1, f"{blocks * (I // 16)} items")
+
+
+@pytest.mark.parametrize("kind,I", [("int4", 480), ("mxfp4", 512)])
+def test_few_tokens_two_column_tiles(kind, I):
+    """The down kernel of wide layers, in each of its token counts; INT4's I ends inside a chunk."""
+    H = 7168
+    lay = Layer(kind, 2, H, I, 3)
+    for T, k in ((16, 8), (13, 10), (32, 6), (17, 8), (64, 4), (33, 4)):
+        assert H // 16 >= 2 * _few_constant("kFewWideDown")
+        assert T * k * -(-I // 128) >= _few_constant("kFewWideUnits")
+        x, ids, wt = _tokens(T, k, 12, H, T)                 # experts 4, 5 of 12
+        lay.check(x, ids, wt, 4, f"wide T={T}")
+
+
+@pytest.mark.parametrize("kind,E,H,I", [("int4", 200, 96, 160), ("mxfp4", 300, 128, 256), ("int4", 600, 96, 64)])
+def test_few_tokens_many_blocks(kind, E, H, I):
+    """More blocks than the down kernel's waves stage at a time; experts past the 512th."""
+    lay = Layer(kind, E, H, I, E)
+    x, ids, wt = _tokens(64, 16, E, H, E)
+    waves, stage = _few_constant("kFewWaves"), _few_constant("kStage")
+    assert _blocks(ids, 0, E) > (waves + 1) * stage           # some wave has more than kStage blocks
+    lay.check(x, ids, wt, 0, f"{E} experts")
+
+
+@pytest.mark.parametrize("kind,H,I", [("int4", 64, 32), ("mxfp4", 128, 128)])
+def test_few_tokens_as_many_blocks_as_slots(kind, H, I):
+    """The largest call in blocks: 1024 slots, an expert each."""
+    E = _few_constant("kFewWaves") * 64 * 2                  # W4A16_FEW_MAX_EXPERTS
+    lay = Layer(kind, E, H, I, 9)
+    x, _, wt = _tokens(64, 16, 16, H, 9)
+    ids = np.random.default_rng(9).permutation(E).astype(np.int32).reshape(64, 16)
+    assert _blocks(ids, 0, E) == 1024
+    lay.check(x, ids, wt, 0, "a block a slot")
+    ids[:, 1:] = E - 1                                       # and the last expert for everyone, many times
+    lay.check(x, ids, wt, 0, "one expert listed 15 times")
+
+
+@pytest.mark.parametrize("kind", ["int4", "mxfp4"])
+def test_few_tokens_repeats_its_bits(kind):
+    """Sums meet in a fixed order: every run of a call gives the same bits."""
+    lay = Layer(kind, 4, 1280, 2048, 5)
+    x, ids, wt = _tokens(64, 4, 4, 1280, 6)
+    dx, di, dw = to_dev_bf16(x), to_dev(ids), to_dev(wt)
+    ref = M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw).clone()
+    for _ in range(20):
+        assert torch.equal(M.moe_few_tokens(dx, lay.p1, lay.p2, di, dw), ref)
+
+
 def test_few_tokens_first_expert_limit(layers):
     lay = layers["int4"]
     x, ids, wt = _tokens(5, 3, 6, lay.H, 12)
