@@ -210,3 +210,12 @@ def test_header_constants_match_the_binding(tmp_path):
     for name, val in (("DTYPE_F32", _lib.DTYPE_F32), ("DTYPE_BF16", _lib.DTYPE_BF16), ("DTYPE_F16", _lib.DTYPE_F16),
                       ("SCORE_SOFTMAX", _lib.SCORE_SOFTMAX), ("SCORE_SIGMOID", _lib.SCORE_SIGMOID)):
         assert int(re.search(rf"#define W4A16_{name} (\d+)", src).group(1)) == val
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_layer_widths_are_whole_pairs_of_tiles(L, mx):
+    """The down kernel of wide layers takes two 16-column tiles a workgroup: H, the gate/up weight's K, is a multiple of 32."""
+    make = W.mxfp4_weight_desc if mx else W.weight_desc
+    for H in (16, 48, 6160, 7184):
+        with pytest.raises(W.W4A16Error):
+            make(1, 128, H, gate_up=True)

@@ -376,9 +376,7 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_down_kernel(const
   const int u0 = (int)(wave * units / kFewWaves), u1 = (int)((wave + 1) * units / kFewWaves);
   const int g = lane >> 4, col = lane & 15;
   const int tiles = p.H / kRowTile;
-  int nt[NT];                                           // a tile past H is the last one again, not stored
-#pragma unroll
-  for (int i = 0; i < NT; ++i) nt[i] = min(NT * (int)blockIdx.x + i, tiles - 1);
+  const int nt = NT * (int)blockIdx.x;                  // the first of the workgroup's tiles
   const gptr_t hbase = uniform_ptr(p.h);
   const Weights weights;
   f32x4_t tot[NT][MT];
@@ -410,8 +408,8 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_down_kernel(const
       const int64_t tile0 = (int64_t)__builtin_amdgcn_readfirstlane(block.expert) * tiles;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        wbase[i] = uniform_ptr(p.w2 + (tile0 + nt[i]) * KC * (kWave * 16));
-        sbase[i] = uniform_ptr(p.s2 + (tile0 + nt[i]) * Weights::scale_tile_bytes(KC));
+        wbase[i] = uniform_ptr(p.w2 + (tile0 + nt + i) * KC * (kWave * 16));
+        sbase[i] = uniform_ptr(p.s2 + (tile0 + nt + i) * Weights::scale_tile_bytes(KC));
       }
       hrow = hbase + (int64_t)(block.h_row + (row.token >= 0 ? col : 0)) * p.I * 2;
     };
@@ -491,8 +489,8 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_down_kernel(const
 #pragma unroll
   for (int v = 1; v < kFewWaves; ++v) y += sm.red[v][wave][lane];
   const int t = 16 * (wave % MT) + col;
-  const int tile = NT * (int)blockIdx.x + wave / MT;
-  if (t >= p.T || tile >= tiles) return;
+  const int tile = nt + wave / MT;
+  if (t >= p.T) return;
   uint2 o;
   o.x = pack_bf16x2(y[0], y[1]);
   o.y = pack_bf16x2(y[2], y[3]);
@@ -513,7 +511,7 @@ hipError_t launch_kind(const FewParams& p, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.H / kRowTile >= 2 * kFewWideDown && (int64_t)p.T * p.topk * p.KC2 >= kFewWideUnits) {
-    const dim3 half((p.H / kRowTile + 1) / 2);
+    const dim3 half(p.H / kRowTile / 2);                // H, a K of the gate/up weight, is a multiple of 32
     if (p.T <= 16)
       hipLaunchKernelGGL((few_down_kernel<Weights, 1, 2, 6, 1>), half, block, 0, stream, p);
     else if (p.T <= 32)
