@@ -120,6 +120,54 @@ def test_route_many_tokens(E, k):
     _check_route(wide[:, 4:4 + E], k, "sigmoid", None, True, 1.0, "strided")
 
 
+def _route_constant(name):
+    """A launch rule's constant, from the kernel's source."""
+    import re
+    src = os.path.join(os.path.dirname(M.__file__), "csrc", "route.hip")
+    return int(re.search(rf"constexpr int {name} = (\d+);", open(src).read()).group(1))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("E", [100, 200, 384, 500, 700, 1000])
+@pytest.mark.parametrize("T,k", [(41, 8), (6149, 8), (6149, 12)])
+def test_route_every_built_width(T, k, E, dtype):
+    """16 lanes a token hold 8, 16, 24, 32, 56 or 64 keys each, 64 lanes 2, 4, 6, 8, 14 or 16; every logit type.
+    Against the definition in 64 bits, all rows at once."""
+    lanes = 16 if T >= _route_constant("kNarrowMinTokens") and k <= _route_constant("kNarrowMaxTopk") else 64
+    assert lanes == (16 if (T, k) == (6149, 8) else 64)
+    g = torch.Generator().manual_seed(T + E + k)
+    l = torch.randn(T, E, generator=g)
+    l[torch.rand(T, E, generator=g) < 0.03] = float("-inf")
+    l[5] = float("-inf")
+    l[6, 9:] = float("nan")                                # nine experts left
+    l[7, E - 1], l[7, 0] = float("inf"), float("inf")
+    l = l.to(dtype)
+    b = 0.1 * torch.randn(E, generator=g)
+    x = l.double().clamp(max=float(np.finfo(np.float32).max))
+    live = ~(l.isnan() | (l == float("-inf")))
+    for scoring, bias, renorm in (("softmax", None, True), ("softmax", None, False), ("sigmoid", None, False),
+                                  ("sigmoid", b, True)):
+        ids, w = M.moe_route(l.to(dev()), k, scoring=scoring, bias=None if bias is None else b.to(dev()),
+                             renormalize=renorm, scale=1.5)
+        sig = 1.0 / (1.0 + torch.exp(-x))
+        key = torch.where(live, x if bias is None else sig + b.double(), float("-inf"))
+        order = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :k]
+        ok = live.gather(1, order)
+        assert torch.equal(ids.cpu(), torch.where(ok, order, -1).int()), (scoring, renorm)
+        top = torch.where(live, x, float("-inf")).amax(1, keepdim=True)
+        score = torch.where(live, sig if scoring == "sigmoid" else torch.exp(x - top), 0.0)
+        ref = score.gather(1, order)
+        if scoring == "softmax":
+            ref = ref / (ref if renorm else score).sum(1, keepdim=True).clamp(min=1e-300)
+        elif renorm:
+            ref = ref / (ref.sum(1, keepdim=True) + 1e-20)
+        ref = torch.where(ok, ref, 0.0) * 1.5
+        # differences from the maximum up to 16 rounded once, exp and division a few units, in weight and sum
+        # (row 7's other differences are past fp32's exp, and 0 in both)
+        tol = 2 * (16 + 8) * 2.0 ** -24 * ref + 2.0 ** -126
+        assert ((w.double().cpu() - ref).abs() <= tol).all(), (scoring, renorm)
+
+
 def test_route_strided_rows_other_stream_and_refusals():
     wide = torch.randn(50, 512, device=dev())
     _check_route(wide[::2, 64:64 + 96], 5, "softmax", what="strided")
