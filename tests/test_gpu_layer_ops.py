@@ -758,6 +758,40 @@ def test_grouped_contiguous_long_runs_and_split_segments():
     assert len(live) == int(touched.sum())
 
 
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 1024])
+@pytest.mark.parametrize("N", [272, 512])
+def test_grouped_every_tile_count_and_pipeline_length(K, N):
+    """One to eight token tiles a block (built: 1, 2, 4, 6, 8), both ends of each; one to eight K chunks, row scales
+    fetched a chunk or four chunks at a time; a column tile that ends inside a workgroup's."""
+    packed, w = _mx_weight(4, N, K, N + K)
+    counts = [n for t in range(1, 9) for n in (16 * t - 15, 16 * t)]
+    idx = []
+    for i, n in enumerate(counts):
+        idx += [i % 4] * n + [-1] * (128 - n)
+    c, s, a = _mx_rows(len(idx), K, 3)
+    s[np.array(idx) < 0] = 255
+    live = [i for i, e in enumerate(idx) if e >= 0]
+    codes = to_dev(c)
+    for at in (0, 4):                                      # K = 512, 1024: scales on 16 bytes or not
+        buf = torch.empty(s.size + at, dtype=torch.uint8, device=dev())
+        rows = M.MXRows(codes, buf[at:].view(s.shape).copy_(to_dev(s)))
+        out = torch.full((len(idx), N), 2.0, dtype=torch.bfloat16, device=dev())
+        M.grouped_mxfp4_contiguous(rows, packed, to_dev(np.array(idx, np.int32)), out=out)
+        _grouped_check(bits(out), live, [idx[i] for i in live], a, w, f"contiguous tiles N={N} K={K} at {at}")
+        # the same rows as groups of 512: whole blocks, then one that ends early
+        for first in range(0, 4):
+            cnt = [(128 * (g + first)) % 512 + counts[4 * g + first] for g in range(4)]
+            out.fill_(2.0)
+            M.grouped_mxfp4_masked(rows, packed, to_dev(np.array(cnt, np.int32)), 100, out=out)
+            sel = [(g * 512 + r, g) for g in range(4) for r in range(cnt[g])]
+            good = [(r, g) for r, g in sel if idx[r] >= 0]  # the others are NaN rows here, and come out as NaN
+            got = bits(out)
+            bad = np.array([r for r, _ in sel if idx[r] < 0], np.int64)
+            assert np.isnan(O.bf16_to_f64(got[bad])).all()
+            got[bad] = 0x4000
+            _grouped_check(got, [r for r, _ in good], [g for _, g in good], a, w, f"masked tiles N={N} K={K} at {at}")
+
+
 def test_grouped_masked_clamps_counts():
     packed, w = _mx_weight(3, 64, 128, 2)
     c, s, a = _mx_rows(3 * 20, 128, 6)
