@@ -131,10 +131,11 @@ def _route_constant(name):
 @pytest.mark.parametrize("E", [100, 200, 384, 500, 700, 1000])
 @pytest.mark.parametrize("T,k", [(41, 8), (6149, 8), (6149, 12)])
 def test_route_every_built_width(T, k, E, dtype):
-    """16 lanes a token hold 8, 16, 24, 32, 56 or 64 keys each, 64 lanes 2, 4, 6, 8, 14 or 16; every logit type.
+    """16 lanes a token hold 8, 16, 24 or 32 keys each, 64 lanes 2, 4, 6, 8, 14 or 16; every logit type.
     Against the definition in 64 bits, all rows at once."""
-    lanes = 16 if T >= _route_constant("kNarrowMinTokens") and k <= _route_constant("kNarrowMaxTopk") else 64
-    assert lanes == (16 if (T, k) == (6149, 8) else 64)
+    narrow = (T >= _route_constant("kNarrowMinTokens") and k <= _route_constant("kNarrowMaxTopk") and
+              E <= _route_constant("kNarrowMaxExperts"))
+    assert narrow == ((T, k) == (6149, 8) and E <= 500)
     g = torch.Generator().manual_seed(T + E + k)
     l = torch.randn(T, E, generator=g)
     l[torch.rand(T, E, generator=g) < 0.03] = float("-inf")

@@ -426,20 +426,31 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
 }
 
 // Lanes per token: 16 lanes share every instruction of the search with three
-// other tokens, 64 lanes finish a token sooner; and a 16-lane list stays short
-// only while k is well below 16.  Measured on MI355X, graph replays, 384
-// experts, fp32 sigmoid + bias, 64 / 16 lanes: top 8, 1024 tokens 5.3 / 7.9 us,
-// 4096 7.8 / 8.4, 6144 9.8 / 9.0, 8192 11.2 / 9.1, 16384 19.6 / 13.1 us (2.0
-// TB/s of logits; an empty launch is about 4.5 us); 8192 tokens top 10 12.0 /
-// 10.7, top 12 13.0 / 12.8, top 14 14.4 / 62 us (lists that overflow twice);
-// 6144 tokens top 12 11.4 / 12.7 us; bf16 softmax 8192 tokens 9.4 / 6.9 us.
-// (Taking the k winners out one by one, 64 lanes: 16384 tokens 25 us.  A
-// 16-lane list that went straight to k passes when it overflowed: 8192 tokens
-// top 10 81 us.)  What 16384 tokens spend: about 880 vector instructions
-// a wave of four tokens, whose issue fills half of the kernel's 10.5 us, and
-// the chains of the rounds and of the list in LDS for the rest.
+// other tokens, 64 lanes finish a token sooner; a 16-lane list stays short
+// only while k is well below 16; and past 512 experts 16 lanes hold more keys,
+// logits and biases than their registers do.  Measured on MI355X, graph
+// replays (an empty launch is about 4.5 us), 64 / 16 lanes, us:
+//                                  4096 tokens   6144        8192        16384
+//   256 experts  sigmoid+bias k 8    7.0 /  7.4   9.3 /  7.9  10.2 /  7.8  16.6 /  9.5
+//   384          sigmoid+bias k 8    7.5 /  8.4   9.6 /  9.2  11.0 /  9.1  17.9 / 11.5
+//   384          sigmoid+bias k 10   8.1 / 10.1  10.1 /  9.5  12.2 / 10.1  19.7 / 12.7
+//   384     bf16 softmax      k 8    6.6 /  6.3   7.9 /  6.7   9.3 /  6.8  14.8 /  8.4
+//   384     bf16 softmax      k 10   7.1 /  8.8   8.7 /  9.1  10.4 /  9.2  16.7 / 11.3
+//   512          sigmoid+bias k 8    7.9 /  9.4   9.7 / 10.2  11.3 / 10.2  19.2 / 16.5
+//   640          sigmoid+bias k 8    9.0 / 11.8  10.8 / 19.9  13.1 / 20.3  22.2 / 40.7
+//   640     fp32 softmax      k 8    7.3 /  8.3   9.0 /  9.4  10.4 /  9.2  17.7 / 17.3
+//  1024          sigmoid+bias k 8    9.5 / 13.2  11.6 / 23.4  14.3 / 23.4  24.6 / 48.4
+//  1024     bf16 softmax      k 8    7.6 /  8.9   9.2 / 12.4  11.0 / 13.3  18.0 / 17.4
+// and 384 experts, sigmoid + bias, 8192 tokens, top 12 13.0 / 12.8, top 14
+// 14.4 / 62 (lists that overflow twice).  (Taking the k winners out one by
+// one, 64 lanes: 16384 tokens 25 us.  A 16-lane list that went straight to k
+// passes when it overflowed: 8192 tokens top 10 81 us.)  What 16384 tokens
+// spend: about 880 vector instructions a wave of four tokens, whose issue
+// fills half of the kernel's 10.5 us, and the chains of the rounds and of the
+// list in LDS for the rest.
 constexpr int kNarrowMaxTopk = 10;
 constexpr int kNarrowMinTokens = 6144;
+constexpr int kNarrowMaxExperts = 512;
 
 // Threads of one launch are counted in 32 bits, and a grid past them wraps
 // without an error: 2^26 tokens of 64 lanes would be no workgroup at all.
@@ -458,7 +469,6 @@ hipError_t launch_piece(const RouteArgs& a, int lanes, hipStream_t stream) {
     return hipGetLastError();                                                            \
   }
   W4A16_ROUTE_CASE(16, 8) W4A16_ROUTE_CASE(16, 16) W4A16_ROUTE_CASE(16, 24) W4A16_ROUTE_CASE(16, 32)
-  W4A16_ROUTE_CASE(16, 56) W4A16_ROUTE_CASE(16, 64)
   W4A16_ROUTE_CASE(64, 2) W4A16_ROUTE_CASE(64, 4) W4A16_ROUTE_CASE(64, 6) W4A16_ROUTE_CASE(64, 8)
   W4A16_ROUTE_CASE(64, 14) W4A16_ROUTE_CASE(64, 16)
 #undef W4A16_ROUTE_CASE
@@ -467,7 +477,7 @@ hipError_t launch_piece(const RouteArgs& a, int lanes, hipStream_t stream) {
 
 template <typename T, bool kSigmoid>
 hipError_t launch_typed(const RouteArgs& a, hipStream_t stream) {
-  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens;
+  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens && a.E <= kNarrowMaxExperts;
   for (int64_t t = 0; t < a.T; t += kLaunchTokens) {
     RouteArgs piece = a;
     piece.logits = static_cast<const T*>(a.logits) + t * a.row_stride;
