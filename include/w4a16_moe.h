@@ -607,7 +607,9 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
  *     when bias (float [E]) is NULL; weight s_e = 1 / (1 + exp(-l_e)), with
  *     renormalize divided by (sum of the chosen s + 1e-20).
  * Every weight is multiplied by scale (finite).  An expert whose logit or
- * bias is -inf or NaN is masked; +inf counts as the largest finite value.
+ * bias is -inf or NaN is masked.  A logit of +inf counts as the largest finite
+ * fp32 value; a bias of +inf comes before every finite one, the lower expert
+ * first of several.
  * Slots left without an expert get topk_ids -1 and topk_weights 0, which
  * w4a16_moe_align (validate = 0), the combine and w4a16_moe_few_tokens skip
  * like any expert held elsewhere.

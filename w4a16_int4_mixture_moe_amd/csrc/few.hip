@@ -10,16 +10,18 @@
 // in operand order; there is no align kernel, no combine kernel and no
 // partial sum in memory.
 //
-//
 // Measured on MI355X (whole calls, graph replays; bytes are the touched
-// experts' weights and scales): 16 tokens on an INT4 EP8 share (48 of 384
-// experts, H 7168, I 2048) 75 - 92 us, 3.8 - 4.5 TB/s; 37 tokens x 16 on an
-// MXFP4 share of 112 of 896 experts 221 - 250 us, 5.1 - 5.8 TB/s; one token on
-// a TP8 slice (I 256) 18 us, of which the weights' bytes are 5.  HBM bounds
-// the MXFP4 call; the INT4 one spends about half its vector issue on the
-// dequantisation (17 instructions for 8 weights) and loses some 15 % to the
-// last round of its items; the single token is two launches and their chains
-// of dependent loads.
+// experts' weights and scales; a 2 GiB copy 4.9 TB/s): 16 tokens on an INT4
+// EP8 share (48 of 384 experts, H 7168, I 2048) 107 us where the routing
+// touches 17 experts (421 MB, 3.9 TB/s), 84 us over routings that touch 12.8;
+// 37 tokens x 16 on an MXFP4 share of 112 of 896 experts, 47 touched, 221 us
+// (1111 MB, 5.0 TB/s); one token on a TP8 slice (I 256) 18 us, MXFP4 19 us
+// over many routings, of which the weights' bytes are 5.  HBM bounds the MXFP4
+// call.  The INT4 one keeps the vector units busy (issue 61 % of the time in
+// gate/up, 46 % in down; the dequantisation takes 17 instructions for 8
+// weights) and reads 1.15 times its bytes: each wave's ring asks for up to D
+// chunks past its last one.  The single token is two kernels of dependent
+// loads (10.1 + 7.0 us): ids, block search, then the first weight.
 //
 // Both weight layouts give lane l = 16 g + i the 32 consecutive K of row i
 // that scale block 4 c + g covers, eight codes a word, so one dequantised
@@ -499,6 +501,8 @@ __global__ __launch_bounds__(kFewThreads, 2 * kPerCU) void few_down_kernel(const
 
 template <typename Weights>
 hipError_t launch_kind(const FewParams& p, hipStream_t stream) {
+  // for as many blocks as there are slots: which of them are held here only
+  // the device knows, so a share counts more items than it will have
   const int64_t items = (int64_t)p.I / kRowTile * p.T * p.topk;
   const dim3 up((unsigned)std::min<int64_t>(items, kFewGroups)), down(p.H / kRowTile), block(kFewThreads);
   // halves of pairs where twice the items still fit one workgroup per CU:

@@ -7,12 +7,14 @@
 // matrix unit, so no register holds data in flight and two workgroups (two
 // waves per SIMD) share a CU: 128 accumulator registers a wave, 76.5 KB of
 // LDS a workgroup.  Measured on MI355X (N 4096, K 7168, graph replays):
-// 16384 rows of 48 experts, 44 of them with rows, 360 us, 2.7 PFLOP/s on
-// valid rows; all rows one expert's 278 us, 3.5 PFLOP/s; masked decode, 576
-// rows of 48 experts, 137 us, 5.3 TB/s of weights and rows.  What bounds it:
-// with one expert the LDS-DMA stream (without the MFMAs 252 us before the
-// order of the fetches below, without the DMA 185 us), with many experts the
-// HBM (4.6 TB/s beyond the L2s), in decode the HBM.  Tried and slower: the
+// 16384 rows of 48 experts, 44 of them with rows, 361 us, 2.7 PFLOP/s on
+// valid rows; all rows one expert's 274 us, 3.5 PFLOP/s; masked decode, 576
+// rows of 48 experts, 132 - 142 us, 5.1 - 5.5 TB/s of weights and rows.  What
+// bounds it: with one expert, whose 80 MB stay in the last-level cache, the
+// LDS-DMA stream (without the MFMAs 252 us before the order of the fetches
+// below, without the DMA 185 us; MFMA busy 47 %), with many experts that
+// stream and the requests beyond the L2s (1.78 GB, 4.9 TB/s, the weights' part
+// of them from HBM; MFMA busy 33 %), in decode the HBM.  Tried and slower: the
 // operands through registers, two chunks ahead (472 against 378 us); 256 rows
 // by 256 weight rows on eight waves, one workgroup per CU, three chunks ahead
 // (436 against 363 us); every request of a chunk in one go (376 against 375 us).

@@ -446,7 +446,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
 // one, 64 lanes: 16384 tokens 25 us.  A 16-lane list that went straight to k
 // passes when it overflowed: 8192 tokens top 10 81 us.)  What 16384 tokens
 // spend: about 880 vector instructions a wave of four tokens, whose issue
-// fills half of the kernel's 10.5 us, and the chains of the rounds and of the
+// fills half of the kernel's 10.5 - 12 us, and the chains of the rounds and of the
 // list in LDS for the rest.
 constexpr int kNarrowMaxTopk = 10;
 constexpr int kNarrowMinTokens = 6144;
