@@ -59,480 +59,11 @@
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "gemm_tile.hpp"
 #include "launch.hpp"
 #include "tile_common.hpp"
 
 namespace w4a16 {
-
-template <int MT>
-struct TileSmem {
-  uint16_t xs[2][16 * MT][kChunk + 8];  // staged activation chunk, 272-byte rows
-  int row[16 * MT];                     // activation row per block row, -1 = padding
-  int out[16 * MT];                     // output row per block row, -1 = not stored
-  float w[16 * MT];                     // top-k weight per block row (weighted epilogue)
-  int last;                             // split-K: this workgroup reduces the tile
-};
-
-#ifndef W4A16_PIPELINED_DEQUANT
-#define W4A16_PIPELINED_DEQUANT 1
-#endif
-constexpr bool kPipelinedDequant = W4A16_PIPELINED_DEQUANT != 0;
-
-// acc += this wave's weight tiles x the block's rows over K chunks [c0, c1).
-// Starts and ends with the workgroup synchronised.  The active token tiles
-// are always a prefix (valid rows come first in every layout); the loop
-// processes exactly tiles [0, NA), NA fixed at compile time, so it loads,
-// reads and multiplies only those, without per-tile branches.
-template <int MT, int NR, int NW, int D, int NA>
-__device__ __forceinline__ void mainloop(const GemmParams& p, TileSmem<MT>& sm, int expert, int nt,
-                                         int c0, int c1, f32x4_t (&acc)[NR][MT]) {
-  constexpr int NTHR = NW * kWave;
-  constexpr int ROWS_PER_PASS = NTHR / 16;          // staged rows covered by one piece index
-  static_assert(ROWS_PER_PASS == 16 || ROWS_PER_PASS == 32, "four or eight waves");
-  constexpr int PPT = (16 * MT + ROWS_PER_PASS - 1) / ROWS_PER_PASS;   // pieces per thread
-  static_assert(NA >= 1 && NA <= MT, "active tile count");
-  auto active = [&](int t) { return t < NA; };
-
-  const int tid = threadIdx.x;
-  const int lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-
-  // Activation staging.  Piece i of this thread is row (tid / 16) +
-  // i * ROWS_PER_PASS, 16 bytes at column 8 * (tid % 16); its token tile is
-  // wave-uniform (a wave covers 4 consecutive rows), so pieces of inactive
-  // tiles, or past the block (eight waves, one tile), are skipped with a
-  // scalar branch.  Padding rows read the block's first row (always valid)
-  // instead; their LDS columns only feed output columns never stored.
-  // Addressing: every stream is (wave-uniform base in SGPRs) + (per-lane
-  // 32-bit byte offset fixed for the whole loop) + (uniform chunk offset), so
-  // the per-chunk address update is scalar and loads use the saddr form.
-  const int fallback_row = sm.row[0];
-  const int xcol = (tid & 15) * 8;
-  const gptr_t xbase = uniform_ptr(p.a);
-  auto piece_row = [&](int i) { return (tid >> 4) + i * ROWS_PER_PASS; };
-  // wave-uniform: the tile of piece i, and whether the piece is loaded
-  auto piece_tile = [&](int i) { return ROWS_PER_PASS == 16 ? i : 2 * i + (wave >> 2); };
-  auto piece_on = [&](int i) { return piece_tile(i) < NA; };
-  uint32_t xoff[PPT];
-#pragma unroll
-  for (int i = 0; i < PPT; ++i) {
-    const int r = sm.row[min(piece_row(i), 16 * MT - 1)];
-    xoff[i] = (uint32_t)((r >= 0 ? r : fallback_row) * p.K + xcol) * 2u;
-  }
-
-  // this wave's weight tiles (clamped so loads stay in bounds; tiles past N
-  // compute throw-away values that are never stored)
-  const int rt_base = nt * (NW * NR) + wave * NR;
-  gptr_t wbase[NR];
-  gptr_t sbase[NR];
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int rt = min(rt_base + r, p.NT - 1);
-    const int64_t tile = (int64_t)expert * p.w_tiles + rt;
-    wbase[r] = uniform_ptr(p.packed_w + tile * p.KC * kWave);
-    sbase[r] = uniform_ptr(p.packed_s + tile * ((p.KC + 1) / 2) * kWave);
-  }
-  const uint32_t woff = (uint32_t)lane * 16u;   // one 16-byte fragment set per lane
-  const uint32_t soff = (uint32_t)lane * 4u;    // one pair of bf16 scales per lane
-
-  const int K = p.K;
-  // `tail`: chunk c may be the ragged last one; a piece past K then reads
-  // column 0 of its row (in bounds) and store_x replaces it by zeros.  No
-  // select on the loaded value, so its destination is never rewritten
-  // before it lands.
-  auto issue_x = [&](int c, u32x4_t (&xr)[PPT], bool tail) {
-    const gptr_t base = xbase + (int64_t)c * (kChunk * 2);
-    const bool kin = !tail || c * kChunk + xcol < K;
-#pragma unroll
-    for (int i = 0; i < PPT; ++i)
-      if (piece_on(i)) xr[i] = gload_u32x4(kin ? base + xoff[i] : xbase + xoff[i]);
-  };
-  auto store_x = [&](int buf, int c, const u32x4_t (&xr)[PPT], bool tail) {
-    const bool kin = !tail || c * kChunk + xcol < K;
-#pragma unroll
-    for (int i = 0; i < PPT; ++i)
-      if (piece_on(i)) {
-        const u32x4_t v = kin ? xr[i] : u32x4_t{0u, 0u, 0u, 0u};
-        *reinterpret_cast<u32x4_t*>(&sm.xs[buf][piece_row(i)][xcol]) = v;
-      }
-  };
-  // weights of chunk c and, for an even chunk (withs), the scale word of
-  // its chunk pair, which the odd chunk after it reuses: a range starts on
-  // an even chunk (split-K slices and stream-K units are whole chunk
-  // pairs), so even ring positions hold even chunks
-  auto issue_w = [&](int c, u32x4_t (&w)[NR], uint32_t (&sc)[NR], auto withs) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      w[r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16) + woff);
-      if constexpr (decltype(withs)::value) sc[r] = gload_u32(sbase[r] + (int64_t)(c >> 1) * (kWave * 4) + soff);
-    }
-  };
-  using WithS = std::integral_constant<bool, true>;
-  using NoS = std::integral_constant<bool, false>;
-
-  // Weights and scales: a ring of D register sets (the config's prefetch
-  // stages); chunk c0 + m*D + P uses set P, and the set is refilled with
-  // chunk c + D as soon as chunk c has been dequantised, so weights have
-  // about D chunk times to arrive from HBM.  Activations come from L2
-  // (every N tile of a block reads the same rows): one register set,
-  // requested at the top of a chunk and written to the other LDS buffer at
-  // its end, before the barrier.  (A second set, for two chunks of
-  // distance, measured no faster and costs registers.)
-  static_assert(D == 2 || D == 4, "the loop body below unrolls two or four chunks");
-  const DequantMasks masks = make_dequant_masks();
-  // 128-bit vector registers (not the 4-field struct): each loop-carried
-  // value stays one register tuple that the allocator can keep in place
-  u32x4_t xr[PPT];
-  u32x4_t wr[D][NR];
-  uint32_t sr[D][NR];   // scale words: even ring positions only
-  uint32_t spair[NR];   // the current pair's word, kept for its odd chunk
-
-  // c0 < c1 (both callers).  Unconditional, clamped (a set past the range
-  // re-reads the last chunk and is never used) and in ring order: the waits
-  // inside the loop are computed for the worst entry path, so a conditional
-  // or reordered load here would make every chunk wait for the newest loads.
-  issue_x(c0, xr, true);
-#pragma unroll
-  for (int i = 0; i < D; ++i) {
-    __builtin_amdgcn_sched_barrier(0);
-    if (i % 2 == 0)
-      issue_w(min(c0 + i, c1 - 1), wr[i], sr[i], WithS{});
-    else
-      issue_w(min(c0 + i, c1 - 1), wr[i], sr[i], NoS{});
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  store_x(0, c0, xr, true);
-  __syncthreads();
-
-  // one chunk at ring position P (c - c0 = P mod D).  STEADY: chunks c + 1
-  // and c + D exist and c + 1 is not the ragged last chunk, so every
-  // prefetch and store is unconditional (no register phis, no selects)
-  // Scale constants of chunk c for a weight set: s, -1032 s, s / 16, -72 s
-  // (the word holds the scales of chunks c & ~1 (low half) and c | 1 (high))
-  auto scale_consts = [&](const uint32_t (&sc)[NR], int c, float (&k)[NR][4]) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float sv = __builtin_bit_cast(float, (c & 1) ? (sc[r] & 0xFFFF0000u) : (sc[r] << 16));
-      k[r][0] = sv;
-      k[r][1] = -1032.0f * sv;
-      k[r][2] = 0.0625f * sv;
-      k[r][3] = -72.0f * sv;
-    }
-  };
-  auto dequant_set = [&](const u32x4_t (&w)[NR], int j, const float (&k)[NR][4], bf16x8_t (&A)[NR]) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) A[r] = dequant8(w[r][j], k[r][0], k[r][1], k[r][2], k[r][3], masks);
-  };
-  auto mfmas = [&](int buf, int j, const bf16x8_t (&A)[NR]) {
-    bf16x8_t B[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      if (active(t))
-        B[t] = *reinterpret_cast<const bf16x8_t*>(&sm.xs[buf][16 * t + (lane & 15)][32 * (lane >> 4) + 8 * j]);
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      if (active(t))
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[r], B[t], acc[r][t], 0, 0, 0);
-  };
-  // refill weight set P with chunk c + D once its last word is dequantised
-  // (A holds that word's operands).  The empty asm and the scheduling
-  // barrier keep the loads below that dequant: moved above it, old and new
-  // values overlap, the new ones land in other registers and the loop
-  // back-edge copies them over, which waits for the loads just issued and
-  // serialises the prefetch.  The second barrier keeps them above the
-  // chunk's activation store, whose wait (for the newest activation load)
-  // would otherwise cover them too.
-  auto refill = [&](auto P_, int c, const bf16x8_t (&A)[NR]) {
-    constexpr int P = decltype(P_)::value;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) asm volatile("" ::"v"(A[r]));
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (P % 2 == 0)
-      issue_w(c + D, wr[P], sr[P], WithS{});
-    else
-      issue_w(c + D, wr[P], sr[P], NoS{});
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  // an even chunk hands its pair's scale word to the odd chunk after it,
-  // before its refill overwrites the word (a copy of a value that arrived
-  // long ago: it waits for nothing)
-  auto keep_pair = [&](auto P_) {
-    constexpr int P = decltype(P_)::value;
-    if constexpr (P % 2 == 0) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r) spair[r] = sr[P][r];
-    }
-  };
-  // the scale word of the chunk at ring position P
-  auto word_of = [&](auto P_) -> const uint32_t(&)[NR] {
-    constexpr int P = decltype(P_)::value;
-    if constexpr (P % 2 == 0)
-      return sr[P];
-    else
-      return spair;
-  };
-
-  // Pipelined form: fragment j + 1 is dequantised
-  // before fragment j's MFMAs are issued, so the VALU work of one overlaps
-  // the matrix work of the other inside a wave; the last fragment of a chunk
-  // dequantises the first one of the next chunk (its weights are already
-  // resident).  Acur / kcur carry that across chunks.
-  constexpr bool PIPE = kPipelinedDequant;
-  bf16x8_t Acur[NR];
-  float kcur[NR][4];
-  if constexpr (PIPE) {
-    scale_consts(sr[0], c0, kcur);
-    dequant_set(wr[0], 0, kcur, Acur);
-  }
-#pragma unroll
-  for (int r = 0; r < NR; ++r) spair[r] = 0u;
-
-  // one chunk at ring position P (c - c0 = P mod D).  STEADY: chunks c + 1
-  // and c + D exist and c + 1 is not the ragged last chunk, so every
-  // prefetch and store is unconditional (no register phis, no selects)
-  auto chunk = [&](auto P_, auto STEADY_, int c) {
-    constexpr int P = decltype(P_)::value;
-    constexpr bool STEADY = decltype(STEADY_)::value;
-    const int buf = (c - c0) & 1;                   // LDS buffer holding chunk c
-    if (STEADY || c + 1 < c1) issue_x(c + 1, xr, !STEADY);
-    if constexpr (PIPE) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8_t Anext[NR];
-        if (j < 3) {
-          dequant_set(wr[P], j + 1, kcur, Anext);
-          if (j == 2) keep_pair(P_);
-          if (j == 2 && (STEADY || c + D < c1)) refill(P_, c, Anext);
-        } else if (STEADY || c + 1 < c1) {
-          using PN = std::integral_constant<int, (P + 1) % D>;
-          scale_consts(word_of(PN{}), c + 1, kcur);
-          dequant_set(wr[PN::value], 0, kcur, Anext);
-        }
-        mfmas(buf, j, Acur);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) Acur[r] = Anext[r];
-      }
-    } else {
-      float k[NR][4];
-      scale_consts(word_of(P_), c, k);
-      keep_pair(P_);
-      // one 8-wide K fragment at a time: dequantise it, read the matching
-      // activation fragments, issue its MFMAs
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8_t A[NR];
-        dequant_set(wr[P], j, k, A);
-        if (j == 3 && (STEADY || c + D < c1)) refill(P_, c, A);
-        mfmas(buf, j, A);
-      }
-    }
-    if (STEADY || c + 1 < c1) store_x(buf ^ 1, c + 1, xr, !STEADY);
-    __syncthreads();
-  };
-  using Steady = std::integral_constant<bool, true>;
-  using Tail = std::integral_constant<bool, false>;
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2 % D>;
-  using I3 = std::integral_constant<int, 3 % D>;
-  int c = c0;
-  for (; c + 2 * D - 1 < c1; c += D) {
-    chunk(I0{}, Steady{}, c);
-    chunk(I1{}, Steady{}, c + 1);
-    if constexpr (D > 2) {
-      chunk(I2{}, Steady{}, c + 2);
-      chunk(I3{}, Steady{}, c + 3);
-    }
-  }
-  // the last up to 2D - 1 chunks (c - c0 is a multiple of D here)
-  for (int m = 0; m < 2; ++m, c += D) {
-    if (c < c1) chunk(I0{}, Tail{}, c);
-    if (c + 1 < c1) chunk(I1{}, Tail{}, c + 1);
-    if constexpr (D > 2) {
-      if (c + 2 < c1) chunk(I2{}, Tail{}, c + 2);
-      if (c + 3 < c1) chunk(I3{}, Tail{}, c + 3);
-    }
-  }
-}
-
-// One tile's K range [c0, c1): zeroed accumulators, the main loop
-// specialised for the block's active token tiles (a workgroup-uniform
-// prefix), then finish(acc, mask).  One- and two-tile blocks run exactly
-// their active tiles; four- and eight-tile blocks round the count up to an
-// even one, so the extra tile (rows that are all padding: they read the
-// block's first row and are never stored) costs at most one tile of MFMAs,
-// where testing tiles inside the loop made it wait for every outstanding
-// load at each test.  Each path owns its
-// accumulators and finishes on its own: merging them into one array before
-// a shared epilogue makes the allocator rotate them between registers with
-// moves inside the loop, each of which waits for an MFMA.
-template <int MT, int NR, int NW, int D, typename Finish>
-__device__ __forceinline__ void run_tile(const GemmParams& p, TileSmem<MT>& sm, int expert, int nt,
-                                         uint32_t tmask, int c0, int c1, Finish&& finish) {
-  auto go = [&](auto na) {
-    constexpr int NA = decltype(na)::value;
-    f32x4_t acc[NR][MT];
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    mainloop<MT, NR, NW, D, NA>(p, sm, expert, nt, c0, c1, acc);
-    finish(acc, (1u << NA) - 1u);
-  };
-  if constexpr (MT == 1) {
-    go(std::integral_constant<int, 1>{});
-  } else if constexpr (MT == 2) {
-    if (tmask == 1u)
-      go(std::integral_constant<int, 1>{});
-    else
-      go(std::integral_constant<int, 2>{});
-  } else if constexpr (MT == 4) {
-    if (tmask < 4u)
-      go(std::integral_constant<int, 2>{});
-    else
-      go(std::integral_constant<int, 4>{});
-  } else {
-    static_assert(MT == 8 || MT == 16, "token tiles per block: 1, 2, 4, 8 or 16");
-    constexpr int Q = MT / 4;                        // active tiles rounded up to a multiple of Q
-    const int na = 32 - __clz(tmask);               // tmask is a prefix
-    if (na <= Q)
-      go(std::integral_constant<int, Q>{});
-    else if (na <= 2 * Q)
-      go(std::integral_constant<int, 2 * Q>{});
-    else if (na <= 3 * Q)
-      go(std::integral_constant<int, 3 * Q>{});
-    else
-      go(std::integral_constant<int, 4 * Q>{});
-  }
-}
-
-// Stream-K partial slots: slot s holds NR * MT float4 per thread, laid out
-// [(r * MT + t)][thread] so each (r, t) is one coalesced 16 * NTHR-byte store.
-template <int MT, int NR, int NW>
-__device__ __forceinline__ float4* partial_slot(const GemmParams& p, int64_t slot) {
-  constexpr int NTHR = NW * kWave;
-  return reinterpret_cast<float4*>(p.sk_partial) + slot * (int64_t)(NR * MT * NTHR);
-}
-
-// Weighted epilogue through LDS: the tile's fp32 partials (times the slot's
-// top-k weight) are first placed in the idle activation buffers, rows padded
-// by 16 bytes, then written row by row, each wave storing two 512-byte row
-// runs per instruction instead of sixteen 64-byte pieces.
-template <int MT, int NR, int NW>
-__device__ __forceinline__ void epilogue_weighted_staged(const GemmParams& p, TileSmem<MT>& sm, int nt,
-                                                         uint32_t tmask, const f32x4_t (&acc)[NR][MT]) {
-  constexpr int BN = 16 * NR * NW;
-  constexpr int LD = BN + 4;
-  static_assert(16 * MT * LD * 4 <= (int)sizeof(sm.xs), "staged tile fits the activation buffers");
-  constexpr int NTHR = NW * kWave;
-  float* tile = reinterpret_cast<float*>(&sm.xs[0][0][0]);
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  __syncthreads();                                   // every wave is done reading the buffers
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if (!((tmask >> t) & 1u)) continue;
-      const int i = 16 * t + (lane & 15);
-      const float w = sm.w[i];
-      const f32x4_t v = acc[r][t];
-      *reinterpret_cast<float4*>(tile + i * LD + (wave * NR + r) * 16 + 4 * (lane >> 4)) =
-          make_float4(w * v[0], w * v[1], w * v[2], w * v[3]);
-    }
-  __syncthreads();
-  const int n0 = nt * BN;
-  const int rows = 16 * (32 - __clz(tmask));
-  for (int idx = threadIdx.x; idx < rows * (BN / 4); idx += NTHR) {
-    const int i = idx / (BN / 4);
-    const int c = 4 * (idx - i * (BN / 4));
-    const int orow = sm.out[i];
-    if (orow == -1 || n0 + c >= p.N) continue;
-    const float4 v = *reinterpret_cast<const float4*>(tile + i * LD + c);
-    if (orow < 0) {               // the token's only local slot: its combined output
-      uint2 o;
-      o.x = pack_bf16x2(v.x, v.y);
-      o.y = pack_bf16x2(v.z, v.w);
-      *reinterpret_cast<uint2*>(p.direct_out + (int64_t)(-orow - 2) * p.direct_ld + n0 + c) = o;
-      continue;
-    }
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + (int64_t)orow * p.N + n0 + c) = v;
-  }
-}
-
-// Split-K reduce (the post gates splitting by shape, section "H200 prefill
-// and TP8"; here a plain split of K into p.split slices for grids that would
-// leave the machine underfilled).  Every slice's workgroup stores its fp32
-// accumulators, then counts its arrival on the tile's counter; the last to
-// arrive sums all slices in slice order 0, 1, ..., so the result does not
-// depend on which workgroup came last, resets the counter for the next call
-// and returns true with the sum in tot.  No workgroup waits for another.
-//
-// Coherence without whole-cache maintenance: the eight XCDs' L2 caches are
-// not coherent with each other, and an agent-scope fence writes back or
-// invalidates a whole L2 (measured: TP8 T = 16 gate/up 51 -> 349 us with a
-// fence per workgroup).  So the slices are written and read with agent-scope
-// relaxed atomic accesses, which the gfx950 code generator issues with the
-// device-coherence cache bit (write-through / re-fetch at the coherence
-// point); each workgroup waits for its stores' completion before it counts
-// its arrival, and the counter is itself an agent-scope atomic.
-template <int MT, int NR, int NW>
-__device__ __forceinline__ bool split_reduce(const GemmParams& p, TileSmem<MT>& sm, int tile, int s, uint32_t tmask,
-                                             const f32x4_t (&acc)[NR][MT], f32x4_t (&tot)[NR][MT]) {
-  constexpr int NTHR = NW * kWave;
-  constexpr int SLICE = NR * MT * NTHR * 2;          // 64-bit words per slice
-  uint64_t* base = reinterpret_cast<uint64_t*>(p.split_partial) + (int64_t)tile * p.split * SLICE;
-  uint64_t* mine = base + (int64_t)s * SLICE;
-  auto pair = [](float a, float b) {
-    return (uint64_t)__builtin_bit_cast(uint32_t, a) | ((uint64_t)__builtin_bit_cast(uint32_t, b) << 32);
-  };
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      if ((tmask >> t) & 1u) {
-        const f32x4_t v = acc[r][t];
-        uint64_t* d = mine + 2 * ((r * MT + t) * NTHR + threadIdx.x);
-        __hip_atomic_store(d, pair(v[0], v[1]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(d + 1, pair(v[2], v[3]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0);                     // this thread's slice stores have completed
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __syncthreads();                                    // ... for every thread of the workgroup
-  if (threadIdx.x == 0) {
-    const uint32_t before = __hip_atomic_fetch_add(p.split_count + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const bool last = before == (uint32_t)p.split - 1u;
-    if (last) __hip_atomic_store(p.split_count + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sm.last = last;
-  }
-  __syncthreads();
-  if (!sm.last) return false;
-  auto lo = [](uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); };
-  auto hi = [](uint64_t w) { return __builtin_bit_cast(float, (uint32_t)(w >> 32)); };
-  for (int q = 0; q < p.split; ++q) {
-    const uint64_t* src = base + (int64_t)q * SLICE;
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        if ((tmask >> t) & 1u) {
-          f32x4_t v;
-          if (q == s) {
-            v = acc[r][t];
-          } else {
-            const uint64_t* d = src + 2 * ((r * MT + t) * NTHR + threadIdx.x);
-            const uint64_t w0 = __hip_atomic_load(d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const uint64_t w1 = __hip_atomic_load(d + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            v = f32x4_t{lo(w0), hi(w0), lo(w1), hi(w1)};
-          }
-          tot[r][t] = q == 0 ? v : tot[r][t] + v;
-        }
-  }
-  return true;
-}
 
 template <int MT, int NR, int NW, int D, int ROUTE, int EPI>
 __global__ __launch_bounds__(NW * kWave) void moe_gemm_kernel(const GemmParams p) {
@@ -564,7 +95,7 @@ __global__ __launch_bounds__(NW * kWave) void moe_gemm_kernel(const GemmParams p
     else
       epilogue<MT, NR, NW, EPI>(p, sm, nt, tm, acc);
   };
-  run_tile<MT, NR, NW, D>(p, sm, expert, nt, tmask, c0, c1, [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
+  run_tile<MT, NR, NW, D>(p, sm, expert, nt, tmask, c0, c1, ZeroStart{}, [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
     if (split) {
       f32x4_t tot[NR][MT];
       if (split_reduce<MT, NR, NW>(p, sm, tile, s, tm, acc, tot)) store(tot, tm);
@@ -707,7 +238,7 @@ __global__ __launch_bounds__(NW * kWave) void moe_gemm_streamk_kernel(const Gemm
     __syncthreads();
     if (expert >= 0) {
       const uint32_t tmask = active_tiles<MT>(sm);
-      run_tile<MT, NR, NW, D>(p, sm, expert, nt, tmask, c0, c1, [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
+      run_tile<MT, NR, NW, D>(p, sm, expert, nt, tmask, c0, c1, ZeroStart{}, [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
         if (c0 == 0 && c1 == KC) {
           epilogue<MT, NR, NW, EPI>(p, sm, nt, tm, acc);
         } else {
