@@ -622,6 +622,26 @@ w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32
                              const float* bias, int32_t topk, int32_t scoring, int32_t renormalize, float scale,
                              int32_t* topk_ids, float* topk_weights, w4a16_stream_t stream);
 
+#define W4A16_ROUTE_MAX_GROUPS 64
+
+/* w4a16_moe_route limited to the best groups of experts: the E experts are
+ * n_groups runs of E / n_groups consecutive ones, the topk_groups best groups
+ * stay (the lower group first where two are equal), and the topk experts are
+ * chosen inside them, in the same order and with the same weights as
+ * w4a16_moe_route.  A group's score:
+ *   W4A16_SCORE_SOFTMAX: its largest logit;
+ *   W4A16_SCORE_SIGMOID: the sum of its two largest s_e + bias[e] (s_e without
+ *     a bias), in 64-bit arithmetic; of the one expert where only one is live.
+ * A group without a live expert comes after every other.  Without renormalize
+ * softmax still divides by the sum over all live experts, of every group.
+ * Sizes: n_groups <= W4A16_ROUTE_MAX_GROUPS dividing E, 1 <= topk_groups <=
+ * n_groups, topk <= topk_groups * (E / n_groups), others as w4a16_moe_route.
+ * Errors: as w4a16_moe_route. */
+w4a16_status w4a16_moe_route_grouped(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride,
+                                     const float* bias, int32_t n_groups, int32_t topk_groups, int32_t topk,
+                                     int32_t scoring, int32_t renormalize, float scale, int32_t* topk_ids,
+                                     float* topk_weights, w4a16_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * A whole MoE layer for a few tokens: gate/up, SiLU * up, down and the
  * weighted sum over a token's experts, in two kernels and without routing
@@ -659,6 +679,88 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
 
 /* Workspace bytes of w4a16_moe_few_tokens; 0 on bad arguments. */
 size_t w4a16_moe_few_tokens_workspace_bytes(const w4a16_weight_desc* gate_up, int32_t T, int32_t topk);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside INT4 projections.
+ *
+ * y_i = W x_i + scale[l] * B_l (A_l x_i), l = token_adapter[token of row i];
+ * rows whose entry lies outside [0, L) (-1 among them) get W x_i alone.  The
+ * adapter's inner values A_l x_i are held in fp32 and enter the second
+ * product as the sum of two bf16 numbers (2^-17 of the value); both products
+ * accumulate in fp32 and the sum is rounded once, by the call's epilogue.
+ *
+ * a: bf16 [L][E][slices * rank][K], b: bf16 [L][E][N][rank], rows of b in the
+ * logical order of the weight's columns.  slices = 2: the two halves of the
+ * weight's rows (a gate/up projection) have adapters of their own: rows
+ * [0, N/2) of b multiply the first rank rows of a, the others the second.
+ * Requests with smaller ranks are padded with zeros.  What a row without an
+ * adapter, or with another one, gives does not depend on an adapter's values,
+ * finite or not.
+ * Sizes: rank a multiple of 8 up to W4A16_ADAPTER_MAX_RANK, L up to
+ * W4A16_ADAPTER_MAX, L * E below 2^30, N % 32 == 0 with two slices; E, N and K
+ * are the weight's (ERR_SHAPE).
+ * Pointers: a, b 16-byte aligned; scale, token_adapter 4.
+ * ---------------------------------------------------------------------- */
+#define W4A16_ADAPTER_MAX 1024
+#define W4A16_ADAPTER_MAX_RANK 256
+
+typedef struct {
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;             /* [L], or NULL: 1 for every adapter */
+  const int32_t* token_adapter;   /* [T] */
+  int32_t L, E, N, K;
+  int32_t rank, slices;           /* slices: 1 or 2 */
+} w4a16_adapters;
+
+/* out = one INT4 weight (desc->E == 1: a layer's shared expert, or any dense
+ * projection) times every row of x [T, K], with adapters beside it or, with
+ * adapters NULL, without.
+ *  silu == 0: out [T, N] = bf16(y);
+ *  silu != 0: out [T, N/2] = bf16(silu(g) * u) of the fp32 sums g = y[0, N/2),
+ *             u = y[N/2, N), for a W4A16_DESC_GATE_UP weight.
+ * workspace: w4a16_linear_workspace_bytes() bytes, not initialised; its
+ * contents are the call's own until it has finished.  out must not overlap
+ * any input.  T = 0 does nothing.
+ * Sizes: T * K * 2 bytes at most 4 GiB (ERR_SHAPE).
+ * Pointers 16-byte aligned.
+ * Errors: ERR_ARG, ERR_LAYOUT (packing, or E != 1), ERR_SHAPE, ERR_WORKSPACE,
+ * ERR_HIP. */
+w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s, const uint16_t* x,
+                          int32_t T, const w4a16_adapters* adapters, int32_t silu, uint16_t* out, void* workspace,
+                          size_t workspace_bytes, w4a16_stream_t stream);
+
+/* Workspace bytes of w4a16_linear (0 without adapters, and on bad arguments). */
+size_t w4a16_linear_workspace_bytes(const w4a16_weight_desc* desc, int32_t T, const w4a16_adapters* adapters);
+
+/* w4a16_moe_gemm with the adapters of the routed experts: a slot of token t
+ * and local expert e takes adapter token_adapter[t] of that expert.  Per-slot
+ * output, or the top-k combine of the sums with topk_weights.
+ *  cfg: NULL: w4a16_indexed_config without splitting; else a config with
+ *       split_k 1 and stages 2 of four waves (nr 2; 4 on 16-row blocks and
+ *       128-row ones with K a multiple of 128), or the tiles that config gives
+ *       with eight (nr 1, and 256-row blocks).
+ *  workspace: w4a16_moe_adapter_workspace_bytes() bytes, not initialised.
+ * Everything else, and the errors, as w4a16_moe_gemm. */
+w4a16_status w4a16_moe_adapter_gemm(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                    const uint16_t* a, int64_t a_rows, int32_t a_layout,
+                                    const w4a16_indexed_routing* routing, const w4a16_adapters* adapters,
+                                    const float* topk_weights, uint16_t* out, const w4a16_config* cfg, void* workspace,
+                                    size_t workspace_bytes, w4a16_stream_t stream);
+
+/* w4a16_moe_gate_up_silu with the adapters of the routed experts.  silu(g) * u
+ * is taken of the fp32 sums (w4a16_moe_gate_up_silu rounds g and u to bf16
+ * first); cfg and workspace as w4a16_moe_adapter_gemm.
+ * Everything else, and the errors, as w4a16_moe_gate_up_silu. */
+w4a16_status w4a16_moe_adapter_gate_up_silu(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                            const uint16_t* x, int64_t x_rows, const w4a16_indexed_routing* routing,
+                                            const w4a16_adapters* adapters, uint16_t* out, const w4a16_config* cfg,
+                                            void* workspace, size_t workspace_bytes, w4a16_stream_t stream);
+
+/* Workspace bytes of the two calls above (combine: with topk_weights); 0 on
+ * bad arguments. */
+size_t w4a16_moe_adapter_workspace_bytes(const w4a16_weight_desc* desc, const w4a16_indexed_routing* routing,
+                                         const w4a16_adapters* adapters, int32_t combine, const w4a16_config* cfg);
 
 #ifdef __cplusplus
 }

@@ -40,6 +40,7 @@ ROUTE_INDEXED, ROUTE_CONTIGUOUS, ROUTE_MASKED = 0, 1, 2   # W4A16_ROUTE_*
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2                # W4A16_DTYPE_*
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1                       # W4A16_SCORE_*
 FEW_MAX_FIRST_EXPERT = 1 << 30                            # W4A16_FEW_MAX_FIRST_EXPERT
+ADAPTER_MAX, ADAPTER_MAX_RANK = 1024, 256                 # W4A16_ADAPTER_MAX, _MAX_RANK
 
 
 class Config(ctypes.Structure):
@@ -60,6 +61,14 @@ class IndexedRouting(ctypes.Structure):
         ("block_m", ctypes.c_int32), ("T", ctypes.c_int32), ("topk", ctypes.c_int32),
         ("topk_ids", ctypes.c_void_p), ("first_expert", ctypes.c_int32), ("E_loc", ctypes.c_int32),
         ("E_glob", ctypes.c_int32),
+    ]
+
+
+class AdaptersC(ctypes.Structure):
+    _fields_ = [
+        ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("token_adapter", ctypes.c_void_p),
+        ("L", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("rank", ctypes.c_int32), ("slices", ctypes.c_int32),
     ]
 
 
@@ -112,6 +121,19 @@ SIGNATURES = {
     "w4a16_moe_route": (_I32, [_P, _I32, _I32, _I32, _I64, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
     "w4a16_moe_few_tokens": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, ctypes.POINTER(WeightDesc), _P, _P, _P,
                                     _I32, _I32, _P, _P, _I32, _P, _P, _SZ, _P]),
+    "w4a16_moe_route_grouped": (_I32, [_P, _I32, _I32, _I32, _I64, _P, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P,
+                                       _P, _P]),
+    "w4a16_linear": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _I32, ctypes.POINTER(AdaptersC), _I32, _P, _P, _SZ,
+                            _P]),
+    "w4a16_linear_workspace_bytes": (_SZ, [ctypes.POINTER(WeightDesc), _I32, ctypes.POINTER(AdaptersC)]),
+    "w4a16_moe_adapter_gemm": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _I64, _I32,
+                                      ctypes.POINTER(IndexedRouting), ctypes.POINTER(AdaptersC), _P, _P,
+                                      ctypes.POINTER(Config), _P, _SZ, _P]),
+    "w4a16_moe_adapter_gate_up_silu": (_I32, [ctypes.POINTER(WeightDesc), _P, _P, _P, _I64,
+                                              ctypes.POINTER(IndexedRouting), ctypes.POINTER(AdaptersC), _P,
+                                              ctypes.POINTER(Config), _P, _SZ, _P]),
+    "w4a16_moe_adapter_workspace_bytes": (_SZ, [ctypes.POINTER(WeightDesc), ctypes.POINTER(IndexedRouting),
+                                                ctypes.POINTER(AdaptersC), _I32, ctypes.POINTER(Config)]),
     "w4a16_moe_few_tokens_workspace_bytes": (_SZ, [ctypes.POINTER(WeightDesc), _I32, _I32]),
 }
 

@@ -22,6 +22,14 @@ the computation runs in the HIP library's kernels.
     # router, and the whole layer for a few tokens (p1 / p2 INT4 or MXFP4)
     topk_ids, topk_weights = moe_route(logits[T, E_glob], k)
     y = moe_few_tokens(x, p1, p2, topk_ids, topk_weights)
+    topk_ids, topk_weights = moe_route_grouped(logits[T, E_glob], k, n_groups, topk_groups)
+    # low-rank adapters of many requests, adapter_ids int32 [T] (-1: none): beside
+    # one shared INT4 weight, and beside the routed experts'
+    ad = adapters(a[L, r, K], b[L, N, r], scale[L])
+    y = w4a16_linear(x, packed1, ad, adapter_ids)
+    ad = adapters(a[L, E, 2 * r, K], b[L, E, N, r], scale[L])
+    inter = moe_adapter_gate_up_silu(x, p1, routing, ad, adapter_ids)
+    y = moe_adapter_gemm(inter, packed2, routing, ad2, adapter_ids, topk_weights, a_layout="sorted")
 """
 from __future__ import annotations
 
@@ -31,9 +39,9 @@ from typing import Optional
 
 import torch
 
-from ._lib import (A_SLOT, A_SORTED, A_TOKEN, DESC_GATE_UP, DESC_MXFP4, DTYPE_BF16, DTYPE_F16, DTYPE_F32,
-                   FEW_MAX_FIRST_EXPERT, ROUTE_CONTIGUOUS, ROUTE_INDEXED, ROUTE_MASKED, SCORE_SIGMOID, SCORE_SOFTMAX, Config,
-                   IndexedRouting, W4A16Error, WeightDesc, check, load)
+from ._lib import (A_SLOT, A_SORTED, A_TOKEN, ADAPTER_MAX, ADAPTER_MAX_RANK, DESC_GATE_UP, DESC_MXFP4, DTYPE_BF16,
+                   DTYPE_F16, DTYPE_F32, FEW_MAX_FIRST_EXPERT, ROUTE_CONTIGUOUS, ROUTE_INDEXED, ROUTE_MASKED,
+                   SCORE_SIGMOID, SCORE_SOFTMAX, AdaptersC, Config, IndexedRouting, W4A16Error, WeightDesc, check, load)
 
 
 def _stream(dev: torch.device) -> ctypes.c_void_p:
@@ -355,6 +363,8 @@ __all__ = [
     "grouped_masked",
     "quant_pack_mxfp4", "dequant_mxfp4", "grouped_mxfp4_contiguous", "grouped_mxfp4_masked",
     "moe_route", "moe_few_tokens", "few_tokens_workspace_bytes",
+    "moe_route_grouped", "Adapters", "adapters", "w4a16_linear", "linear_workspace_bytes", "moe_adapter_gemm",
+    "moe_adapter_gate_up_silu", "adapter_workspace_bytes",
 ]
 
 
@@ -624,15 +634,7 @@ def grouped_mxfp4_masked(a: MXRows, packed: PackedW4, masked_m: torch.Tensor, ex
 
 # ------------------------------------------------------------ router, few-token layer
 
-def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
-              renormalize: bool = True, scale: float = 1.0) -> tuple[torch.Tensor, torch.Tensor]:
-    """Gate logits [T, E] (float32, bfloat16 or float16; rows may be strided)
-    -> topk_ids int32 [T, topk], topk_weights float32 [T, topk], in falling
-    order, ties to the lower expert.  scoring "softmax" orders by logit,
-    "sigmoid" by sigmoid + bias (float32 [E], selection only).  renormalize
-    divides by the chosen scores' sum; scale multiplies the weights.  Logits
-    (or biases) of -inf or NaN mask an expert; a slot without one left gets
-    id -1 and weight 0."""
+def _route_args(logits: torch.Tensor, scoring: str, bias: Optional[torch.Tensor]) -> tuple[int, int]:
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
     if not logits.is_cuda:
@@ -652,6 +654,19 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
         if bias.shape[0] != E:
             raise ValueError(f"bias has {bias.shape[0]} entries, logits {E} experts")
         _same_device(logits, bias=bias)
+    return T, E
+
+
+def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: Optional[torch.Tensor] = None,
+              renormalize: bool = True, scale: float = 1.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gate logits [T, E] (float32, bfloat16 or float16; rows may be strided)
+    -> topk_ids int32 [T, topk], topk_weights float32 [T, topk], in falling
+    order, ties to the lower expert.  scoring "softmax" orders by logit,
+    "sigmoid" by sigmoid + bias (float32 [E], selection only).  renormalize
+    divides by the chosen scores' sum; scale multiplies the weights.  Logits
+    (or biases) of -inf or NaN mask an expert; a slot without one left gets
+    id -1 and weight 0."""
+    T, E = _route_args(logits, scoring, bias)
     dev = logits.device
     topk = max(0, min(int(topk), E + 1))                  # outside [1, E] the call refuses it
     ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
@@ -659,6 +674,27 @@ def moe_route(logits: torch.Tensor, topk: int, scoring: str = "softmax", bias: O
     stride = logits.stride(0) if T > 1 else E
     _launch(dev, load().w4a16_moe_route, logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E, stride, _ptr(bias),
             topk, _SCORINGS[scoring], int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def moe_route_grouped(logits: torch.Tensor, topk: int, n_groups: int, topk_groups: int, scoring: str = "sigmoid",
+                      bias: Optional[torch.Tensor] = None, renormalize: bool = True,
+                      scale: float = 1.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """moe_route among the experts of the topk_groups best of n_groups groups
+    (at most 64, runs of E / n_groups consecutive experts).  A group scores by
+    its largest logit ("softmax") or by the sum of its two largest sigmoid +
+    bias ("sigmoid"); the lower group first of equals.  Weights as moe_route's;
+    softmax without renormalize divides by the sum over all groups."""
+    T, E = _route_args(logits, scoring, bias)
+    _need_32bit(n_groups=int(n_groups), topk_groups=int(topk_groups))
+    dev = logits.device
+    topk = max(0, min(int(topk), E + 1))                  # outside [1, E] the call refuses it
+    ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
+    stride = logits.stride(0) if T > 1 else E
+    _launch(dev, load().w4a16_moe_route_grouped, logits.data_ptr(), _LOGIT_DTYPES[logits.dtype], T, E, stride, _ptr(bias),
+            int(n_groups), int(topk_groups), topk, _SCORINGS[scoring], int(bool(renormalize)), float(scale),
+            ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -710,5 +746,217 @@ def moe_few_tokens(x: torch.Tensor, gate_up: PackedW4, down: PackedW4, topk_ids:
     _launch(dev, load().w4a16_moe_few_tokens, ctypes.byref(gate_up.desc), gate_up.w.data_ptr(),
             gate_up.s.data_ptr(), ctypes.byref(down.desc), down.w.data_ptr(), down.s.data_ptr(), x.data_ptr(),
             T, k, topk_ids.data_ptr(), topk_weights.data_ptr(), int(first_expert), out.data_ptr(),
+            _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out
+
+
+# ------------------------------------------------------------ low-rank adapters
+
+@dataclasses.dataclass
+class Adapters:
+    """L low-rank adapters of one INT4 weight [E, N, K]: scale[l] * b[l, e] @ a[l, e]
+    is what adapter l adds to expert e's weight.  a bf16 [L, E, slices * rank, K],
+    b bf16 [L, E, N, rank], scale float32 [L] or None."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor]
+
+    @property
+    def L(self):
+        return self.b.shape[0]
+
+    @property
+    def rank(self):
+        return self.b.shape[3]
+
+    @property
+    def slices(self):
+        return self.a.shape[2] // self.b.shape[3]
+
+    def as_c(self, adapter_ids: torch.Tensor) -> AdaptersC:
+        L, E, N, r = self.b.shape
+        return AdaptersC(self.a.data_ptr(), self.b.data_ptr(), _ptr(self.scale), adapter_ids.data_ptr(), L, E, N,
+                         self.a.shape[3], r, self.a.shape[2] // r)
+
+
+def adapters(a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None) -> Adapters:
+    """Adapters of one weight, a bf16 [L, slices * rank, K] and b bf16
+    [L, N, rank], or of each of E experts, a [L, E, slices * rank, K] and b
+    [L, E, N, rank]; scale float32 [L] (None: 1).  Two slices: the first
+    half of the weight's rows (the gate) takes the first rank rows of a, the
+    second half (up) the others.  rank is a multiple of 8, at most 256 (pad with
+    zeros); at most 1024 adapters."""
+    _need(a, "a", (torch.bfloat16,))
+    _need(b, "b", (torch.bfloat16,))
+    if a.dim() == 3 and b.dim() == 3:
+        a, b = a.unsqueeze(1), b.unsqueeze(1)
+    if a.dim() != 4 or b.dim() != 4 or a.shape[:2] != b.shape[:2] or 0 in a.shape or 0 in b.shape:
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} are not [L, (E,) slices * rank, K] and [L, (E,) N, rank]")
+    if a.shape[2] not in (b.shape[3], 2 * b.shape[3]):
+        raise ValueError(f"a has {a.shape[2]} rows an adapter, b rank {b.shape[3]}: one or two slices")
+    if b.shape[3] % 8 or b.shape[3] > ADAPTER_MAX_RANK or a.shape[0] > ADAPTER_MAX:
+        raise ValueError(f"{a.shape[0]} adapters of rank {b.shape[3]}: at most {ADAPTER_MAX}, a multiple of 8 up to "
+                         f"{ADAPTER_MAX_RANK} (pad with zeros)")
+    if scale is not None:
+        _need(scale, "scale", (torch.float32,), 1)
+        if scale.shape[0] != a.shape[0]:
+            raise ValueError(f"scale has {scale.shape[0]} entries, there are {a.shape[0]} adapters")
+    _need_32bit(L=a.shape[0], E=a.shape[1], N=b.shape[2], K=a.shape[3], rank=b.shape[3])
+    _same_device(a, b=b, scale=scale)
+    return Adapters(a, b, scale)
+
+
+def _adapter_ids(adapter_ids: Optional[torch.Tensor], T: int) -> torch.Tensor:
+    _need(adapter_ids, "adapter_ids", (torch.int32,), 1)
+    if adapter_ids.shape[0] != T:
+        raise ValueError(f"adapter_ids has {adapter_ids.shape[0]} entries, there are {T} tokens")
+    return adapter_ids
+
+
+def _scratch(nbytes: int, workspace: Optional[torch.Tensor], dev: torch.device) -> Optional[torch.Tensor]:
+    if workspace is not None:
+        _need(workspace, "workspace", (torch.uint8,))
+        return workspace
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def linear_workspace_bytes(packed: PackedW4, T: int, adapters: Optional[Adapters] = None) -> int:
+    """Workspace bytes of w4a16_linear on T rows (0 without adapters, and where the call refuses the sizes)."""
+    if adapters is None or not 0 < T < 2**31:
+        return 0
+    ad = adapters.as_c(adapters.b)                        # the token list's address decides nothing here
+    return int(load().w4a16_linear_workspace_bytes(ctypes.byref(packed.desc), T, ctypes.byref(ad)))
+
+
+def w4a16_linear(x: torch.Tensor, packed: PackedW4, adapters: Optional[Adapters] = None,
+                 adapter_ids: Optional[torch.Tensor] = None, silu: bool = False, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One INT4 weight [1, N, K] for every row of x bf16 [T, K] (a layer's
+    shared projection), with low-rank adapters beside it: row t adds adapter
+    adapter_ids[t] (int32 [T]; none outside [0, L)).  -> bf16 [T, N], rounded
+    once; with silu (a weight packed with gate_up=True) bf16 [T, N/2] of
+    silu(gate) * up."""
+    _need(x, "x", _BF16, 2)
+    T, K = x.shape
+    if K != packed.K:
+        raise ValueError(f"x has K={K}, weight has K={packed.K}")
+    _need_32bit(T=T)
+    if (adapters is None) != (adapter_ids is None):
+        raise ValueError("adapters and adapter_ids go together")
+    N = packed.N // 2 if silu else packed.N
+    dev = x.device
+    if out is None:
+        out = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", _BF16, 2)
+        if out.shape[0] < T or out.shape[1] != N:
+            raise ValueError(f"out must be [{T}, {N}]")
+    ad = None
+    if adapters is not None:
+        c = adapters.as_c(_adapter_ids(adapter_ids, T))
+        ad = ctypes.byref(c)
+        if workspace is None:
+            nbytes = load().w4a16_linear_workspace_bytes(ctypes.byref(packed.desc), T, ad)
+        else:
+            nbytes = 0
+        workspace = _scratch(nbytes, workspace, dev)
+        _same_device(x, a=adapters.a, adapter_ids=adapter_ids, workspace=workspace)
+    _same_device(x, weight=packed.w, weight_scales=packed.s, out=out)
+    _launch(dev, load().w4a16_linear, ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(), x.data_ptr(),
+            T, ad, int(bool(silu)), out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out
+
+
+def adapter_workspace_bytes(packed: PackedW4, routing: Routing, adapters: Adapters, combine: bool,
+                            cfg: Optional[Config] = None) -> int:
+    """Workspace bytes of moe_adapter_gemm (combine: with topk_weights) and, without combine, of
+    moe_adapter_gate_up_silu; 0 where the calls refuse the arguments."""
+    r = routing.as_c()
+    ad = adapters.as_c(adapters.b)
+    return int(load().w4a16_moe_adapter_workspace_bytes(ctypes.byref(packed.desc), ctypes.byref(r), ctypes.byref(ad),
+                                                        int(bool(combine)), None if cfg is None else ctypes.byref(cfg)))
+
+
+def _routing_device(ref: torch.Tensor, routing: Routing) -> None:
+    _same_device(ref, sorted_ids=routing.sorted_ids, expert_ids=routing.expert_ids,
+                 num_tokens_padded=routing.num_tokens_padded, topk_ids=routing.topk_ids)
+
+
+def moe_adapter_gemm(a: torch.Tensor, packed: PackedW4, routing: Routing, adapters: Adapters,
+                     adapter_ids: torch.Tensor, topk_weights: Optional[torch.Tensor] = None,
+                     a_layout: Optional[str] = None, cfg: Optional[Config] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_w4a16_gemm with the routed experts' low-rank adapters beside them: a
+    slot of token t and expert e adds adapter adapter_ids[t] (int32 [T]; none
+    outside [0, L)) of e, to the per-slot output or inside the top-k combine.
+    K is not split; the workspace needs no initial value."""
+    _need(a, "a", _BF16, 2)
+    T, k = routing.T, routing.topk
+    combine = topk_weights is not None
+    if a_layout is None:
+        a_layout = "slot" if combine else "token"
+    if a_layout not in _A_LAYOUTS:
+        raise ValueError(f"a_layout must be one of {sorted(_A_LAYOUTS)}")
+    if a.shape[1] != packed.K:
+        raise ValueError(f"a has K={a.shape[1]}, weight has K={packed.K}")
+    if combine:
+        _need(topk_weights, "topk_weights", (torch.float32,), 2)
+        if tuple(topk_weights.shape) != (T, k):
+            raise ValueError(f"topk_weights must be [{T}, {k}]")
+    dev = a.device
+    rows = T if combine else T * k
+    if out is None:
+        out = (torch.empty if combine else torch.zeros)(rows, packed.N, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", _BF16, 2)
+        if out.shape[0] < rows or out.shape[1] != packed.N:
+            raise ValueError(f"out must be [{rows}, {packed.N}]")
+    r, ad = routing.as_c(), adapters.as_c(_adapter_ids(adapter_ids, T))
+    cfg_p = None if cfg is None else ctypes.byref(cfg)
+    nbytes = 0
+    if workspace is None:
+        nbytes = load().w4a16_moe_adapter_workspace_bytes(ctypes.byref(packed.desc), ctypes.byref(r), ctypes.byref(ad),
+                                                          int(combine), cfg_p)
+    workspace = _scratch(nbytes, workspace, dev)
+    _same_device(a, weight=packed.w, weight_scales=packed.s, adapters=adapters.a, adapter_ids=adapter_ids,
+                 topk_weights=topk_weights, out=out, workspace=workspace)
+    _routing_device(a, routing)
+    _launch(dev, load().w4a16_moe_adapter_gemm, ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(),
+            a.data_ptr(), a.shape[0], _A_LAYOUTS[a_layout], ctypes.byref(r), ctypes.byref(ad), _ptr(topk_weights),
+            out.data_ptr(), cfg_p, _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out
+
+
+def moe_adapter_gate_up_silu(x: torch.Tensor, packed: PackedW4, routing: Routing, adapters: Adapters,
+                             adapter_ids: torch.Tensor, cfg: Optional[Config] = None,
+                             out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_gate_up_silu with the routed experts' low-rank adapters beside them:
+    out bf16 [capacity, I], row p = sorted position p (rows of local slots
+    written), of silu(gate) * up of the fp32 sums, rounded once."""
+    _need(x, "x", _BF16, 2)
+    if not packed.gate_up:
+        raise ValueError("moe_adapter_gate_up_silu needs a weight packed with gate_up=True")
+    if x.shape[1] != packed.K:
+        raise ValueError(f"x has K={x.shape[1]}, weight has K={packed.K}")
+    dev = x.device
+    if out is None:
+        out = torch.empty(routing.capacity, packed.N // 2, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", _BF16, 2)
+        if out.shape[0] < routing.capacity or out.shape[1] != packed.N // 2:
+            raise ValueError(f"out must be [{routing.capacity}, {packed.N // 2}]")
+    r, ad = routing.as_c(), adapters.as_c(_adapter_ids(adapter_ids, routing.T))
+    cfg_p = None if cfg is None else ctypes.byref(cfg)
+    nbytes = 0
+    if workspace is None:
+        nbytes = load().w4a16_moe_adapter_workspace_bytes(ctypes.byref(packed.desc), ctypes.byref(r), ctypes.byref(ad), 0,
+                                                          cfg_p)
+    workspace = _scratch(nbytes, workspace, dev)
+    _same_device(x, weight=packed.w, weight_scales=packed.s, adapters=adapters.a, adapter_ids=adapter_ids, out=out,
+                 workspace=workspace)
+    _routing_device(x, routing)
+    _launch(dev, load().w4a16_moe_adapter_gate_up_silu, ctypes.byref(packed.desc), packed.w.data_ptr(),
+            packed.s.data_ptr(), x.data_ptr(), x.shape[0], ctypes.byref(r), ctypes.byref(ad), out.data_ptr(), cfg_p,
             _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out

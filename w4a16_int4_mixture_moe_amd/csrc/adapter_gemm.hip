@@ -1,0 +1,125 @@
+// The indexed INT4 product with low-rank adapters: the tiles of gemm.hip and
+// prefill.hip, whose accumulators start from the adapters' products
+// (adapter.hpp) instead of zero.
+#include <type_traits>
+
+#include "adapter.hpp"
+#include "adapter_launch.hpp"
+#include "device_common.hpp"
+#include "gemm_tile.hpp"
+#include "launch.hpp"
+#include "prefill_tile.hpp"
+#include "tile_common.hpp"
+
+namespace w4a16 {
+
+namespace {
+
+template <int MT, int NR, int NW, int EPI>
+__global__ __launch_bounds__(NW * kWave) void adapter_gemm_kernel(const GemmParams p, const AdapterParams q) {
+  __shared__ __attribute__((aligned(16))) AdapterSmem<TileSmem<MT>, 16 * MT> sm;
+  int mb, nt;
+  if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
+  const int expert = setup_adapter_rows<MT, NW, kRouteIndexed, EPI>(p, q, mb, sm);
+  if (expert < 0) return;
+  __syncthreads();
+  const uint32_t tmask = active_tiles<MT>(sm);
+  const int rt_base = nt * (NW * NR) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
+  run_tile<MT, NR, NW, 2>(
+      p, static_cast<TileSmem<MT>&>(sm), expert, nt, tmask, 0, p.KC,
+      [&](f32x4_t(&acc)[NR][MT], auto na) {
+        start_from_adapters<MT, NR, decltype(na)::value>(p, q, sm, expert, rt_base, acc);
+      },
+      [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
+        if constexpr (EPI == kEpiWeighted && 16 * NR * NW <= 128)
+          epilogue_weighted_staged<MT, NR, NW>(p, sm, nt, tm, acc);
+        else
+          adapter_epilogue<MT, NR, NW, EPI>(p, sm, nt, tm, acc);
+      });
+}
+
+template <int MT, int NR, int NW, int EPI>
+__global__ __launch_bounds__(NW * kWave, 8 / NW) void adapter_prefill_kernel(const GemmParams p, const AdapterParams q) {
+  using C = PfCfg<MT, NR, NW>;
+  __shared__ __attribute__((aligned(16))) AdapterSmem<PfSmem<C::BM>, C::BM> sm;
+  int mb, nt;
+  if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
+  const int expert = setup_adapter_rows<MT, NW, kRouteIndexed, EPI>(p, q, mb, sm);
+  if (expert < 0) return;
+  __syncthreads();
+  pf_run<C, false>(
+      p, static_cast<PfSmem<C::BM>&>(sm), expert, nt, nt + 1, active_tiles<MT>(sm),
+      [&](auto& acc, auto na, int) {
+        const int rt_base = nt * (NW * NR) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
+        start_from_adapters<MT, NR, decltype(na)::value>(p, q, sm, expert, rt_base, acc);
+      },
+      [&](const auto& acc, uint32_t tm, int) { adapter_epilogue<MT, NR, NW, EPI>(p, sm, nt, tm, acc); });
+}
+
+// 16 rows of an expert on a small grid: one weight tile (a gate / up pair) a
+// workgroup, its waves splitting K and the adapters
+template <int EPI>
+__global__ __launch_bounds__(kKwWaves * kWave) void adapter_kwave_kernel(const GemmParams p, const AdapterParams q) {
+  constexpr int NT = EPI == kEpiSilu ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) AdapterSmem<SplitSmem<1, NT, kKwWaves>, 16> sm;
+  int mb, nt;
+  if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
+  const int expert = setup_adapter_rows<1, kKwWaves, kRouteIndexed, EPI>(p, q, mb, sm);
+  if (expert < 0) return;
+  clear_low(sm);
+  __syncthreads();
+  f32x4_t acc[NT][1];
+  split_product<1, NT, kKwWaves>(p, q, sm, expert, nt, acc);
+  if (threadIdx.x >= kWave) return;
+  adapter_epilogue<1, NT, 1, EPI>(p, sm, nt, 1u, acc);
+}
+
+typedef void (*AdapterKernel)(const GemmParams, const AdapterParams);
+
+template <int EPI>
+AdapterKernel pick_adapter_of(int m_tiles, int nr, int waves, int stages, int K) {
+  if (m_tiles == 1 && nr == 1 && waves == kKwWaves && stages == 2 && K % kChunk == 0) return adapter_kwave_kernel<EPI>;
+  if (stages != 2) return nullptr;
+  if (K % kChunk == 0) {
+    if (m_tiles == PfNarrow::MT && nr == PfNarrow::NR && waves == PfNarrow::NW)
+      return adapter_prefill_kernel<PfNarrow::MT, PfNarrow::NR, PfNarrow::NW, EPI>;
+    if (m_tiles == PfWide::MT && nr == PfWide::NR && waves == PfWide::NW)
+      return adapter_prefill_kernel<PfWide::MT, PfWide::NR, PfWide::NW, EPI>;
+  }
+#define W4A16_CASE(MT_, NR_) \
+  if (m_tiles == MT_ && nr == NR_ && waves == 4) return adapter_gemm_kernel<MT_, NR_, 4, EPI>;
+  W4A16_CASE(1, 2) W4A16_CASE(1, 4) W4A16_CASE(2, 2) W4A16_CASE(4, 2) W4A16_CASE(8, 2)
+#undef W4A16_CASE
+  return nullptr;
+}
+
+AdapterKernel pick_adapter(int epilogue, int m_tiles, int nr, int waves, int stages, int K) {
+  if (epilogue == kEpiStore) return pick_adapter_of<kEpiStore>(m_tiles, nr, waves, stages, K);
+  if (epilogue == kEpiWeighted) return pick_adapter_of<kEpiWeighted>(m_tiles, nr, waves, stages, K);
+  if (epilogue == kEpiSilu) return pick_adapter_of<kEpiSilu>(m_tiles, nr, waves, stages, K);
+  return nullptr;
+}
+
+}  // namespace
+
+bool adapter_gemm_supported(int epilogue, int m_tiles, int nr, int waves, int stages, int K) {
+  return pick_adapter(epilogue, m_tiles, nr, waves, stages, K) != nullptr;
+}
+
+hipError_t launch_adapter_gemm(int epilogue, int m_tiles, int nr, int waves, int stages, const GemmParams& p,
+                               const AdapterParams& q, hipStream_t stream) {
+  const AdapterKernel k = pick_adapter(epilogue, m_tiles, nr, waves, stages, p.K);
+  if (k == nullptr) return hipErrorInvalidValue;
+  GemmParams g = p;
+  g.xcd_group = xcd_group_for(1, p.n_tiles);
+  // as launch_gemm: decode tiles of a block kept together on one XCD
+  if (nr > 1 && m_tiles <= 2 && g.n_tiles >= 2 * kXcdDecodeGroup && g.n_tiles % kXcdDecodeGroup == 0)
+    g.xcd_group = kXcdDecodeGroup;
+  const int64_t grid = grid_of(g, g.n_tiles);
+  if (grid <= 0) return hipSuccess;
+  if (grid > INT32_MAX / (waves * kWave)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(waves * kWave), 0, stream, g, q);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16

@@ -1,0 +1,48 @@
+// Host-side launchers of the products with low-rank adapters and of the shared
+// projection (internal to the library; api.cpp validates arguments first).
+#pragma once
+#include "launch.hpp"
+
+namespace w4a16 {
+
+struct AdapterParams {
+  const uint16_t* a;            // bf16 [L][E][slices * rank][K]
+  const uint16_t* b;            // bf16 [L][E][N][rank]
+  const float* scale;           // [L], or NULL: 1
+  const int32_t* ids;           // [T] adapter of each token, none outside [0, L); NULL: none at all
+  int32_t L, E, rank;           // L = 0: no adapters
+  int32_t slices;               // 2: the rows of b's two halves take h's two halves (gate and up)
+  int32_t N, n0;                // rows of b of one (adapter, expert); the first output column of this launch
+  int32_t topk;                 // row (slot) s belongs to token s / topk
+  int64_t rows;                 // rows of h: T * topk slots, or T
+  float* h;                     // [ks][rows][slices * rank], of rows with an adapter
+  int32_t ks;                   // slices of K that left their sums in h
+  const int32_t* order;         // kRouteDense: the rows in order of their adapters, or NULL
+};
+
+// h = scale * A x of every row that has an adapter (adapter_shrink.hip).
+// sorted_ids == NULL: row r of x is row r of h.
+struct ShrinkParams {
+  AdapterParams ad;
+  const uint16_t* x;
+  int32_t K, KC;
+  const int32_t* sorted_ids;
+  const int32_t* expert_ids;
+  const int32_t* num_tokens_padded;
+  int32_t block_shift;          // log2 of the routing's block_m
+  int32_t sentinel, a_row_div;  // as in GemmParams
+  int64_t positions;            // bound of the sorted positions, or the rows
+  int32_t* order;               // out, with sorted_ids == NULL: see AdapterParams; or NULL
+};
+constexpr int kOrderMaxRows = 16384;     // more rows than one workgroup orders while the others work
+int shrink_slices(int64_t positions, int32_t width, int32_t KC);
+hipError_t launch_adapter_shrink(const ShrinkParams& p, hipStream_t stream);
+
+// The indexed product with adapters (adapter_gemm.hip): tiles of launch_gemm, K not split
+bool adapter_gemm_supported(int epilogue, int m_tiles, int nr, int waves, int stages, int K);
+hipError_t launch_adapter_gemm(int epilogue, int m_tiles, int nr, int waves, int stages, const GemmParams& p,
+                               const AdapterParams& q, hipStream_t stream);
+// One weight for all rows, with or without adapters (linear.hip); epilogue kEpiStore or kEpiSilu
+hipError_t launch_linear(int epilogue, const GemmParams& p, const AdapterParams& q, hipStream_t stream);
+
+}  // namespace w4a16

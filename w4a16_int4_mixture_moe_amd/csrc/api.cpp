@@ -18,6 +18,7 @@
 #include <tuple>
 #include <vector>
 
+#include "adapter_launch.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -1101,6 +1102,42 @@ static_assert(W4A16_FEW_MAX_TOKENS == w4a16::kFewMaxTokens && W4A16_FEW_MAX_SLOT
 
 }  // namespace
 
+namespace {
+
+w4a16_status route_impl(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride, const float* bias,
+                        int32_t groups, int32_t keep, int32_t topk, int32_t scoring, int32_t renormalize, float scale,
+                        int32_t* topk_ids, float* topk_weights, w4a16_stream_t stream) {
+  if (T < 0 || E <= 0) return fail(W4A16_ERR_ARG, "bad sizes T=%d E=%d", T, E);
+  if (topk <= 0 || topk > E) return fail(W4A16_ERR_ARG, "topk = %d outside [1, E = %d]", topk, E);
+  if (topk > W4A16_ROUTE_MAX_TOPK || E > W4A16_ROUTE_MAX_EXPERTS)
+    return fail(W4A16_ERR_SHAPE, "topk = %d, E = %d: at most %d of %d experts", topk, E, W4A16_ROUTE_MAX_TOPK,
+                W4A16_ROUTE_MAX_EXPERTS);
+  if (dtype != W4A16_DTYPE_F32 && dtype != W4A16_DTYPE_BF16 && dtype != W4A16_DTYPE_F16)
+    return fail(W4A16_ERR_UNSUPPORTED, "logits dtype %d is not W4A16_DTYPE_F32, _BF16 or _F16", dtype);
+  if (scoring != W4A16_SCORE_SOFTMAX && scoring != W4A16_SCORE_SIGMOID)
+    return fail(W4A16_ERR_UNSUPPORTED, "scoring %d is not W4A16_SCORE_SOFTMAX or W4A16_SCORE_SIGMOID", scoring);
+  if (bias && scoring != W4A16_SCORE_SIGMOID)
+    return fail(W4A16_ERR_UNSUPPORTED, "a selection bias is for sigmoid scores only");
+  if (!std::isfinite(scale)) return fail(W4A16_ERR_ARG, "scale must be finite");
+  if (T > 1 && row_stride < E) return fail(W4A16_ERR_ARG, "row_stride = %lld < E = %d", (long long)row_stride, E);
+  if (T > 1 && row_stride > W4A16_ROUTE_MAX_STRIDE)
+    return fail(W4A16_ERR_SHAPE, "row_stride = %lld above %d", (long long)row_stride, W4A16_ROUTE_MAX_STRIDE);
+  if (T == 0) return W4A16_OK;
+  if (!logits || !topk_ids || !topk_weights) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  const uintptr_t size = dtype == W4A16_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(bias) % 4 ||
+      reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
+    return fail(W4A16_ERR_ARG, "a pointer is not aligned to its elements");
+  // every group kept: no group decides anything
+  hipError_t e = w4a16::launch_route(logits, dtype, T > 1 ? row_stride : E, bias, T, E, keep < groups ? groups : 1, keep,
+                                     topk, scoring == W4A16_SCORE_SIGMOID, renormalize != 0, scale, topk_ids,
+                                     topk_weights, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "moe_route launch");
+  return W4A16_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 // ------------------------------------------------------------ A4W4 (MXFP4)
@@ -1401,32 +1438,25 @@ w4a16_status w4a16_mxfp4_grouped_masked(const w4a16_weight_desc* desc, const voi
 w4a16_status w4a16_moe_route(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride,
                              const float* bias, int32_t topk, int32_t scoring, int32_t renormalize, float scale,
                              int32_t* topk_ids, float* topk_weights, w4a16_stream_t stream) {
-  if (T < 0 || E <= 0) return fail(W4A16_ERR_ARG, "bad sizes T=%d E=%d", T, E);
-  if (topk <= 0 || topk > E) return fail(W4A16_ERR_ARG, "topk = %d outside [1, E = %d]", topk, E);
-  if (topk > W4A16_ROUTE_MAX_TOPK || E > W4A16_ROUTE_MAX_EXPERTS)
-    return fail(W4A16_ERR_SHAPE, "topk = %d, E = %d: at most %d of %d experts", topk, E, W4A16_ROUTE_MAX_TOPK,
-                W4A16_ROUTE_MAX_EXPERTS);
-  if (dtype != W4A16_DTYPE_F32 && dtype != W4A16_DTYPE_BF16 && dtype != W4A16_DTYPE_F16)
-    return fail(W4A16_ERR_UNSUPPORTED, "logits dtype %d is not W4A16_DTYPE_F32, _BF16 or _F16", dtype);
-  if (scoring != W4A16_SCORE_SOFTMAX && scoring != W4A16_SCORE_SIGMOID)
-    return fail(W4A16_ERR_UNSUPPORTED, "scoring %d is not W4A16_SCORE_SOFTMAX or W4A16_SCORE_SIGMOID", scoring);
-  if (bias && scoring != W4A16_SCORE_SIGMOID)
-    return fail(W4A16_ERR_UNSUPPORTED, "a selection bias is for sigmoid scores only");
-  if (!std::isfinite(scale)) return fail(W4A16_ERR_ARG, "scale must be finite");
-  if (T > 1 && row_stride < E) return fail(W4A16_ERR_ARG, "row_stride = %lld < E = %d", (long long)row_stride, E);
-  if (T > 1 && row_stride > W4A16_ROUTE_MAX_STRIDE)
-    return fail(W4A16_ERR_SHAPE, "row_stride = %lld above %d", (long long)row_stride, W4A16_ROUTE_MAX_STRIDE);
-  if (T == 0) return W4A16_OK;
-  if (!logits || !topk_ids || !topk_weights) return fail(W4A16_ERR_ARG, "NULL pointer argument");
-  const uintptr_t size = dtype == W4A16_DTYPE_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(bias) % 4 ||
-      reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
-    return fail(W4A16_ERR_ARG, "a pointer is not aligned to its elements");
-  hipError_t e = w4a16::launch_route(logits, dtype, T > 1 ? row_stride : E, bias, T, E, topk, scoring == W4A16_SCORE_SIGMOID,
-                                     renormalize != 0, scale, topk_ids, topk_weights,
-                                     static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "moe_route launch");
-  return W4A16_OK;
+  return route_impl(logits, dtype, T, E, row_stride, bias, 1, 1, topk, scoring, renormalize, scale, topk_ids,
+                    topk_weights, stream);
+}
+
+w4a16_status w4a16_moe_route_grouped(const void* logits, int32_t dtype, int32_t T, int32_t E, int64_t row_stride,
+                                     const float* bias, int32_t n_groups, int32_t topk_groups, int32_t topk,
+                                     int32_t scoring, int32_t renormalize, float scale, int32_t* topk_ids,
+                                     float* topk_weights, w4a16_stream_t stream) {
+  if (E <= 0) return fail(W4A16_ERR_ARG, "bad size E=%d", E);
+  if (n_groups <= 0 || E % n_groups) return fail(W4A16_ERR_ARG, "%d groups do not divide E = %d experts", n_groups, E);
+  if (n_groups > W4A16_ROUTE_MAX_GROUPS)
+    return fail(W4A16_ERR_SHAPE, "%d groups, at most %d", n_groups, W4A16_ROUTE_MAX_GROUPS);
+  if (topk_groups <= 0 || topk_groups > n_groups)
+    return fail(W4A16_ERR_ARG, "topk_groups = %d outside [1, n_groups = %d]", topk_groups, n_groups);
+  if (topk > topk_groups * (E / n_groups))
+    return fail(W4A16_ERR_ARG, "topk = %d above the %d experts of %d groups", topk, topk_groups * (E / n_groups),
+                topk_groups);
+  return route_impl(logits, dtype, T, E, row_stride, bias, n_groups, topk_groups, topk, scoring, renormalize, scale,
+                    topk_ids, topk_weights, stream);
 }
 
 // ------------------------------------------------------------ a layer for a few tokens
@@ -1503,6 +1533,291 @@ w4a16_status w4a16_moe_few_tokens(const w4a16_weight_desc* gate_up, const void* 
   p.out = out;
   hipError_t e = w4a16::launch_few_tokens(mx, p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "moe_few_tokens launch");
+  return W4A16_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+w4a16_status check_adapters(const w4a16_adapters* ad, const w4a16_weight_desc* d, int32_t T) {
+  if (!ad) return fail(W4A16_ERR_ARG, "adapters is NULL");
+  if (ad->L <= 0 || ad->rank <= 0 || (ad->slices != 1 && ad->slices != 2))
+    return fail(W4A16_ERR_ARG, "bad adapter sizes L=%d rank=%d slices=%d", ad->L, ad->rank, ad->slices);
+  if (ad->L > W4A16_ADAPTER_MAX || ad->rank > W4A16_ADAPTER_MAX_RANK || ad->rank % 8)
+    return fail(W4A16_ERR_SHAPE, "L = %d adapters (at most %d) of rank %d (a multiple of 8 up to %d)", ad->L,
+                W4A16_ADAPTER_MAX, ad->rank, W4A16_ADAPTER_MAX_RANK);
+  if (ad->E != d->E || ad->N != d->N || ad->K != d->K)
+    return fail(W4A16_ERR_SHAPE, "adapters of [%d, %d, %d] beside a weight [%d, %d, %d]", ad->E, ad->N, ad->K, d->E, d->N,
+                d->K);
+  if (ad->slices == 2 && d->N % 32) return fail(W4A16_ERR_SHAPE, "two slices need N %% 32 == 0 (got %d)", d->N);
+  if ((int64_t)ad->L * ad->E >= ((int64_t)1 << 30)) return fail(W4A16_ERR_SHAPE, "L * E = %d * %d too large", ad->L, ad->E);
+  if (!ad->a || !ad->b || (T > 0 && !ad->token_adapter)) return fail(W4A16_ERR_ARG, "NULL pointer in adapters");
+  if (!aligned16(ad->a) || !aligned16(ad->b)) return fail(W4A16_ERR_ARG, "adapters' a and b must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(ad->scale) % 4 || reinterpret_cast<uintptr_t>(ad->token_adapter) % 4)
+    return fail(W4A16_ERR_ARG, "scale and token_adapter must be 4-byte aligned");
+  return W4A16_OK;
+}
+
+// `rows` rows of h, of `positions` positions to look through
+w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, int32_t topk, int64_t rows, int64_t positions) {
+  w4a16::AdapterParams q;
+  std::memset(&q, 0, sizeof q);
+  q.a = ad.a;
+  q.b = ad.b;
+  q.scale = ad.scale;
+  q.ids = ad.token_adapter;
+  q.L = ad.L;
+  q.E = ad.E;
+  q.rank = ad.rank;
+  q.slices = ad.slices;
+  q.N = ad.N;
+  q.topk = topk;
+  q.rows = rows;
+  q.ks = w4a16::shrink_slices(positions, ad.slices * ad.rank, (ad.K + 127) / 128);
+  return q;
+}
+
+size_t h_bytes(const w4a16::AdapterParams& q) {
+  return al256((size_t)q.ks * (size_t)q.rows * q.slices * q.rank * sizeof(float));
+}
+
+w4a16_status check_workspace(size_t need, const void* workspace, size_t workspace_bytes) {
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(W4A16_ERR_WORKSPACE, "this call needs %zu bytes of 16-byte aligned workspace, got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  return W4A16_OK;
+}
+
+// Positions of the routing that may hold a slot.
+int64_t position_bound(const w4a16_indexed_routing& r) {
+  return indexed_block_bound(r, r.block_m) * r.block_m;
+}
+
+// The config of an indexed call with adapters: whole tiles, not split along K.
+w4a16_status adapter_call_config(const w4a16_indexed_routing& r, const w4a16_weight_desc* d, int epi,
+                                 const w4a16_config* cfg, w4a16_config* c) {
+  w4a16_status st = indexed_call_config(r, d, cfg, c);
+  if (st != W4A16_OK) return st;
+  if (!cfg) c->split_k = 1;
+  if (c->split_k != 1) return fail(W4A16_ERR_UNSUPPORTED, "a product with adapters runs one workgroup per tile (split_k = 1)");
+  st = check_config(*c, W4A16_ROUTE_INDEXED, epi, d->K);
+  if (st != W4A16_OK) return st;
+  if (!w4a16::adapter_gemm_supported(epi, c->block_m / 16, c->nr, c->waves, c->stages, d->K))
+    return fail(W4A16_ERR_UNSUPPORTED, "tile config block_m=%d nr=%d waves=%d stages=%d not built with adapters", c->block_m,
+                c->nr, c->waves, c->stages);
+  return check_tile_rows(*c, r);
+}
+
+// h of the routed slots, [ks][T * topk][slices * rank]
+hipError_t shrink_routed(const w4a16::AdapterParams& q, const uint16_t* a, int32_t a_layout, const w4a16_weight_desc* d,
+                         const w4a16_indexed_routing& r, hipStream_t stream) {
+  w4a16::ShrinkParams sp;
+  std::memset(&sp, 0, sizeof sp);
+  sp.ad = q;
+  sp.x = a;
+  sp.K = d->K;
+  sp.KC = d->chunks;
+  sp.sorted_ids = r.sorted_ids;
+  sp.expert_ids = r.expert_ids;
+  sp.num_tokens_padded = r.num_tokens_padded;
+  while ((1 << sp.block_shift) < r.block_m) ++sp.block_shift;
+  sp.sentinel = r.T * r.topk;
+  sp.a_row_div = a_layout == W4A16_A_TOKEN ? r.topk : a_layout == W4A16_A_SLOT ? 1 : 0;
+  sp.positions = position_bound(r);
+  return w4a16::launch_adapter_shrink(sp, stream);
+}
+
+struct AdapterWorkspace {
+  size_t h = 0, combine = 0;
+  int32_t cols = 0;
+  size_t total() const { return h + combine; }
+};
+
+AdapterWorkspace adapter_workspace(const w4a16_config& c, const w4a16_weight_desc* d, const w4a16_indexed_routing& r,
+                                   const w4a16::AdapterParams& q, bool combine) {
+  AdapterWorkspace w;
+  w.h = h_bytes(q);
+  w.cols = combine ? combine_cols_of(c, d->N, r.T, r.topk, r.E_glob, r.E_loc) : d->N;
+  if (combine) w.combine = al256((size_t)r.T * r.topk * w.cols * sizeof(float));
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t w4a16_linear_workspace_bytes(const w4a16_weight_desc* desc, int32_t T, const w4a16_adapters* adapters) {
+  if (check_int4_desc(desc) != W4A16_OK || !adapters || T <= 0 || check_adapters(adapters, desc, T) != W4A16_OK) return 0;
+  return h_bytes(adapter_params(*adapters, 1, T, T)) + al256((size_t)T * sizeof(int32_t));
+}
+
+w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s, const uint16_t* x,
+                          int32_t T, const w4a16_adapters* adapters, int32_t silu, uint16_t* out, void* workspace,
+                          size_t workspace_bytes, w4a16_stream_t stream) {
+  w4a16_status st = check_int4_desc(desc);
+  if (st != W4A16_OK) return st;
+  if (desc->E != 1) return fail(W4A16_ERR_LAYOUT, "one weight is needed, the packed one holds %d experts", desc->E);
+  if (silu && desc->flags != W4A16_DESC_GATE_UP)
+    return fail(W4A16_ERR_LAYOUT, "silu needs a weight packed with w4a16_weight_desc_init_gate_up");
+  if (T < 0) return fail(W4A16_ERR_ARG, "T = %d", T);
+  if (!packed_w || !packed_s || (T > 0 && (!x || !out))) return fail(W4A16_ERR_ARG, "NULL pointer argument");
+  if (!aligned16(packed_w) || !aligned16(packed_s) || !aligned16(x) || !aligned16(out))
+    return fail(W4A16_ERR_ARG, "packed weights, activations and output must be 16-byte aligned");
+  st = check_offset_range(T, desc->K, "activations");
+  if (st != W4A16_OK) return st;
+  w4a16::AdapterParams q;
+  std::memset(&q, 0, sizeof q);
+  q.rows = T;
+  size_t h = 0;
+  if (adapters) {
+    st = check_adapters(adapters, desc, T);
+    if (st != W4A16_OK) return st;
+    if (T == 0) return W4A16_OK;
+    q = adapter_params(*adapters, 1, T, T);
+    h = h_bytes(q);
+    st = check_workspace(h + al256((size_t)T * sizeof(int32_t)), workspace, workspace_bytes);
+    if (st != W4A16_OK) return st;
+  }
+  if (T == 0) return W4A16_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (adapters) {
+    q.h = static_cast<float*>(workspace);
+    w4a16::ShrinkParams sp;
+    std::memset(&sp, 0, sizeof sp);
+    sp.ad = q;
+    sp.x = x;
+    sp.K = desc->K;
+    sp.KC = desc->chunks;
+    sp.positions = T;
+    // in one block of 16 rows no order changes anything
+    if (T > 16 && T <= w4a16::kOrderMaxRows) sp.order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + h);
+    q.order = sp.order;
+    const hipError_t e = w4a16::launch_adapter_shrink(sp, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
+  }
+  const w4a16::GemmParams p = base_params(desc, packed_w, packed_s, x, out, 1, 1);
+  const hipError_t e = w4a16::launch_linear(silu ? w4a16::kEpiSilu : w4a16::kEpiStore, p, q, s);
+  if (e != hipSuccess) return hip_fail(e, "linear launch");
+  return W4A16_OK;
+}
+
+size_t w4a16_moe_adapter_workspace_bytes(const w4a16_weight_desc* desc, const w4a16_indexed_routing* routing,
+                                         const w4a16_adapters* adapters, int32_t combine, const w4a16_config* cfg) {
+  if (check_int4_desc(desc) != W4A16_OK || !routing || check_adapters(adapters, desc, routing->T) != W4A16_OK) return 0;
+  const w4a16_indexed_routing& r = *routing;
+  if (r.T < 0 || r.topk <= 0 || r.E_loc <= 0 || !valid_block_m(r.block_m) || r.capacity < 0) return 0;
+  if ((int64_t)r.T * r.topk >= INT32_MAX / 2) return 0;
+  w4a16_config c{};
+  // the config steers only the combine's columns, which do not depend on the epilogue's tile
+  if (adapter_call_config(r, desc, combine ? w4a16::kEpiWeighted : w4a16::kEpiStore, cfg, &c) != W4A16_OK) return 0;
+  const w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, position_bound(r));
+  return adapter_workspace(c, desc, r, q, combine != 0).total();
+}
+
+w4a16_status w4a16_moe_adapter_gemm(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                    const uint16_t* a, int64_t a_rows, int32_t a_layout,
+                                    const w4a16_indexed_routing* routing, const w4a16_adapters* adapters,
+                                    const float* topk_weights, uint16_t* out, const w4a16_config* cfg, void* workspace,
+                                    size_t workspace_bytes, w4a16_stream_t stream) {
+  w4a16_status st = check_indexed_call(desc, packed_w, packed_s, a, out, routing);
+  if (st != W4A16_OK) return st;
+  st = check_adapters(adapters, desc, routing->T);
+  if (st != W4A16_OK) return st;
+  const w4a16_indexed_routing& r = *routing;
+  const bool combine = topk_weights != nullptr;
+  if (combine && (desc->flags & W4A16_DESC_GATE_UP))
+    return fail(W4A16_ERR_LAYOUT, "a gate/up interleaved weight cannot take the top-k combine (it belongs to the down projection)");
+  if (a_layout != W4A16_A_TOKEN && a_layout != W4A16_A_SLOT && a_layout != W4A16_A_SORTED)
+    return fail(W4A16_ERR_ARG, "a_layout %d is not W4A16_A_TOKEN, W4A16_A_SLOT or W4A16_A_SORTED", a_layout);
+  const int64_t need_rows = a_layout == W4A16_A_TOKEN  ? (int64_t)r.T
+                            : a_layout == W4A16_A_SLOT ? (int64_t)r.T * r.topk
+                                                       : r.capacity;
+  if (a_rows < need_rows)
+    return fail(W4A16_ERR_SHAPE, "activations have %lld rows, need %lld", (long long)a_rows, (long long)need_rows);
+  st = check_offset_range(need_rows, desc->K, "activations");
+  if (st != W4A16_OK) return st;
+  const int epi = combine ? w4a16::kEpiWeighted : w4a16::kEpiStore;
+  w4a16_config c{};
+  st = adapter_call_config(r, desc, epi, cfg, &c);
+  if (st != W4A16_OK) return st;
+  if (combine && !r.topk_ids) return fail(W4A16_ERR_ARG, "combine needs routing.topk_ids");
+  if (r.T == 0) return W4A16_OK;
+  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, position_bound(r));
+  const AdapterWorkspace wl = adapter_workspace(c, desc, r, q, combine);
+  st = check_workspace(wl.total(), workspace, workspace_bytes);
+  if (st != W4A16_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  q.h = static_cast<float*>(workspace);
+  float* comb = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.h);
+  hipError_t e = shrink_routed(q, a, a_layout, desc, r, s);
+  if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
+  w4a16::GemmParams p = base_params(desc, packed_w, packed_s, a, combine ? (void*)comb : (void*)out, c.nr, c.waves);
+  p.sorted_ids = r.sorted_ids;
+  p.expert_ids = r.expert_ids;
+  p.num_tokens_padded = r.num_tokens_padded;
+  p.sentinel = r.T * r.topk;
+  p.a_row_div = a_layout == W4A16_A_TOKEN ? r.topk : a_layout == W4A16_A_SLOT ? 1 : 0;
+  p.slot_weight = topk_weights;
+  p.expert_shift = tile_shift(c, r);
+  p.grid_blocks = (int32_t)indexed_block_bound(r, c.block_m);
+  // one pass per `cols` output columns (all of N without the combine), as w4a16_moe_gemm
+  const int64_t kc2 = (p.KC + 1) / 2;
+  for (int32_t n0 = 0; n0 < desc->N; n0 += wl.cols) {
+    const int32_t nc = std::min(wl.cols, desc->N - n0);
+    w4a16::GemmParams g = p;
+    g.packed_w = p.packed_w + (int64_t)(n0 / 16) * p.KC * 64;
+    g.packed_s = p.packed_s + (int64_t)(n0 / 16) * kc2 * 64;
+    g.N = nc;
+    g.NT = nc / 16;
+    g.n_tiles = n_tiles_of(nc, c.nr, c.waves);
+    q.n0 = n0;
+    e = w4a16::launch_adapter_gemm(epi, c.block_m / 16, c.nr, c.waves, c.stages, g, q, s);
+    if (e != hipSuccess) return hip_fail(e, "adapter gemm launch");
+    if (combine) {
+      e = w4a16::launch_combine(comb, r.topk_ids, r.T, r.topk, r.first_expert, r.E_loc, nc, out + n0, desc->N, nullptr, s);
+      if (e != hipSuccess) return hip_fail(e, "combine launch");
+    }
+  }
+  return W4A16_OK;
+}
+
+w4a16_status w4a16_moe_adapter_gate_up_silu(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s,
+                                            const uint16_t* x, int64_t x_rows, const w4a16_indexed_routing* routing,
+                                            const w4a16_adapters* adapters, uint16_t* out, const w4a16_config* cfg,
+                                            void* workspace, size_t workspace_bytes, w4a16_stream_t stream) {
+  w4a16_status st = check_indexed_call(desc, packed_w, packed_s, x, out, routing);
+  if (st != W4A16_OK) return st;
+  st = check_adapters(adapters, desc, routing->T);
+  if (st != W4A16_OK) return st;
+  if (desc->flags != W4A16_DESC_GATE_UP)
+    return fail(W4A16_ERR_LAYOUT, "the fused SiLU gate/up call needs a weight packed with w4a16_weight_desc_init_gate_up");
+  const w4a16_indexed_routing& r = *routing;
+  if (x_rows < r.T) return fail(W4A16_ERR_SHAPE, "activations have %lld rows, need %d", (long long)x_rows, r.T);
+  st = check_offset_range(r.T, desc->K, "activations");
+  if (st != W4A16_OK) return st;
+  w4a16_config c{};
+  st = adapter_call_config(r, desc, w4a16::kEpiSilu, cfg, &c);
+  if (st != W4A16_OK) return st;
+  if (r.T == 0) return W4A16_OK;
+  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, position_bound(r));
+  st = check_workspace(h_bytes(q), workspace, workspace_bytes);
+  if (st != W4A16_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  q.h = static_cast<float*>(workspace);
+  hipError_t e = shrink_routed(q, x, W4A16_A_TOKEN, desc, r, s);
+  if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
+  w4a16::GemmParams p = base_params(desc, packed_w, packed_s, x, out, c.nr, c.waves);
+  p.sorted_ids = r.sorted_ids;
+  p.expert_ids = r.expert_ids;
+  p.num_tokens_padded = r.num_tokens_padded;
+  p.sentinel = r.T * r.topk;
+  p.a_row_div = r.topk;
+  p.expert_shift = tile_shift(c, r);
+  p.grid_blocks = (int32_t)indexed_block_bound(r, c.block_m);
+  if (c.nr == 1) p.n_tiles = p.NT / 2;   // one (gate, up) tile pair per workgroup
+  e = w4a16::launch_adapter_gemm(w4a16::kEpiSilu, c.block_m / 16, c.nr, c.waves, c.stages, p, q, s);
+  if (e != hipSuccess) return hip_fail(e, "adapter gate_up_silu launch");
   return W4A16_OK;
 }
 

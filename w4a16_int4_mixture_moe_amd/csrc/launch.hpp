@@ -18,7 +18,8 @@ hipError_t launch_pack(const uint8_t* codes, const uint16_t* scales, int32_t E, 
                        uint32_t* packed_s, hipStream_t stream);
 
 // ---- GEMM (gemm.hip)
-enum RouteKind : int { kRouteIndexed = 0, kRouteContiguous = 1, kRouteMasked = 2 };
+// kRouteDense: rows 0 .. T - 1 of one weight (the shared projection; not a C ABI value)
+enum RouteKind : int { kRouteIndexed = 0, kRouteContiguous = 1, kRouteMasked = 2, kRouteDense = 3 };
 // kEpiSilu: gate/up pairs of tiles -> bf16(silu(g) * u) at sorted positions;
 // kEpiSiluMx (MXFP4 kernels): the same activation quantised to MXFP4 rows
 enum EpilogueKind : int { kEpiStore = 0, kEpiWeighted = 1, kEpiSilu = 2, kEpiSiluMx = 3 };
@@ -158,8 +159,9 @@ hipError_t launch_mx_gemm(int epilogue, int m_tiles, int nr, int waves, int stag
 
 
 // ---- router (route.hip): dtype 0 fp32, 1 bf16, 2 fp16 logits
+// groups > 1: only the `keep` best of that many runs of consecutive experts
 hipError_t launch_route(const void* logits, int dtype, int64_t row_stride, const float* bias, int32_t T, int32_t E,
-                        int32_t topk, int sigmoid, int renorm, float scale, int32_t* ids, float* weights,
+                        int32_t groups, int32_t keep, int32_t topk, int sigmoid, int renorm, float scale, int32_t* ids, float* weights,
                         hipStream_t stream);
 
 // ---- a whole layer for a few tokens (few.hip)

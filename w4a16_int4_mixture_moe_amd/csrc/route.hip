@@ -28,6 +28,15 @@
 // enough to swap two experts that nearly tie.  The list's bound is lowered by
 // that error, and where two of its keys are closer than it the group ranks
 // the list again by s_e + b_e in 64 bits.
+//
+// Groups.  With n groups of consecutive experts only the `keep` best stay
+// (softmax: by their largest logit; sigmoid: by the sum of their two largest
+// s + b).  The keys go through LDS; the lanes of a token share its groups, a
+// power of two of lanes each, a lane keeps the two largest keys it meets and
+// the lanes of a group merge theirs; each group then counts the groups before
+// it.  Two sums that 32 bits cannot tell apart at the border (or that are not
+// finite) are formed again in 64.  Experts of the other groups then count as
+// masked.
 #include <algorithm>
 #include <type_traits>
 
@@ -162,6 +171,8 @@ struct RouteArgs {
   int64_t row_stride;          // elements between rows
   const float* bias;           // sigmoid only, or NULL
   int32_t T, E, topk;
+  int32_t groups, size, keep;  // groups of `size` experts of which `keep` stay (kGroups)
+  uint32_t group_mul;          // ceil(2^20 / size)
   int32_t renorm;
   float scale;
   int32_t* ids;
@@ -197,7 +208,101 @@ struct RouteSmem {
   int count[G];
 };
 
-template <typename T, int L, int V, bool kSigmoid>
+// of groups: a token's keys, then the groups' scores
+constexpr int kMaxGroups = 64;
+constexpr int kNarrowMaxGroups = 16;                // of 16 lanes a token
+
+template <int L, int V>
+struct GroupSmem {
+  static constexpr int G = kRouteThreads / L;
+  float key[G][L * V];
+  double score[G][kMaxGroups];
+};
+
+// the two largest of (a, b) and (c, d), a >= b and c >= d
+template <typename K>
+__device__ __forceinline__ void merge_two(K& a, K& b, K c, K d) {
+  const K low = a < c ? a : c;
+  const K next = b < d ? d : b;
+  a = a < c ? c : a;
+  b = low < next ? next : low;
+}
+
+// a group's score from its two largest keys (-inf: none)
+template <bool kSigmoid, typename K>
+__device__ __forceinline__ K group_score(K a, K b) {
+  return kSigmoid && b > -(K)INFINITY ? a + b : a;
+}
+
+// The groups that stay, a bit each.  key: this lane's keys (-inf: masked);
+// logit(e) and bias(e) of the token's expert e.
+template <typename T, int L, int V, bool kSigmoid, typename Logit>
+__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& p, GroupSmem<L, V>& sm, const float (&key)[V], bool biased,
+                                                Logit&& logit) {
+  const int g = threadIdx.x / L, l = threadIdx.x % L;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sm.key[g][i * L + l] = key[i] > -INFINITY ? key[i] : -INFINITY;   // a NaN as masked
+  __builtin_amdgcn_wave_barrier();
+  int per = 1;                                      // lanes a group
+  while (2 * per * p.groups <= L) per *= 2;
+  const int mine = l / per, sub = l % per;
+  const bool has = mine < p.groups;
+  float a = -INFINITY, b = -INFINITY;
+  if (has)
+    for (int e = sub; e < p.size; e += per) merge_two(a, b, sm.key[g][mine * p.size + e], -INFINITY);
+  for (int m = 1; m < per; m *= 2) merge_two(a, b, __shfl_xor(a, m), __shfl_xor(b, m));
+  // without a bias the keys are logits, in the order of the scores that add up
+  if (kSigmoid && !biased) {
+    if (a > -INFINITY) a = sigmoid_key(a);
+    if (b > -INFINITY) b = sigmoid_key(b);
+  }
+  double score = (double)group_score<kSigmoid>(a, b);
+  // each group's place among the groups, the scores in LDS
+  auto place = [&]() {
+    if (has && sub == 0) sm.score[g][mine] = score;
+    __builtin_amdgcn_wave_barrier();
+    int before_it = 0;
+    if (has)
+      for (int j = 0; j < p.groups; ++j) before_it += before(sm.score[g][j], j, score, mine) ? 1 : 0;
+    __builtin_amdgcn_wave_barrier();
+    return before_it;
+  };
+  int rank = place();
+  if (kSigmoid) {
+    // is the first group left out as good as the last one kept?
+    // (each key within key_error of its own size, which the sum may not show)
+    double out = -HUGE_VAL, in = HUGE_VAL;
+    float c = 0.f;
+    if (has && rank == p.keep) out = score;
+    if (has && rank == p.keep - 1) in = score;
+    if (a > -INFINITY) c = fabsf(a) + (b > -INFINITY ? fabsf(b) : 0.f);
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) {
+      out = fmax(out, __shfl_xor(out, m));
+      in = fmin(in, __shfl_xor(in, m));
+      c = fmaxf(c, __shfl_xor(c, m));
+    }
+    const bool close = out > -HUGE_VAL && !(in - out > 4.0 * (double)key_error(c));
+    if (__ballot(close)) {                          // any group of the wave
+      double x = -HUGE_VAL, y = -HUGE_VAL;
+      if (has)
+        for (int e = sub; e < p.size; e += per) {
+          const int at = mine * p.size + e;
+          if (sm.key[g][at] > -INFINITY) merge_two(x, y, exact_key(logit(at), biased ? p.bias[at] : 0.f), -HUGE_VAL);
+        }
+      for (int m = 1; m < per; m *= 2) merge_two(x, y, __shfl_xor(x, m), __shfl_xor(y, m));
+      score = group_score<kSigmoid>(x, y);
+      rank = place();
+    }
+  }
+  // one bit a group, gathered over the token's lanes
+  uint64_t kept = has && sub == 0 && rank < p.keep ? 1ull << mine : 0ull;
+#pragma unroll
+  for (int m = 1; m < L; m *= 2) kept |= __shfl_xor(kept, m);
+  return kept;
+}
+
+template <typename T, int L, int V, bool kSigmoid, bool kGroups>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p) {
   using Smem = RouteSmem<L>;
   constexpr int OWN = Smem::CAP / L;                // listed experts a lane looks after
@@ -252,9 +357,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
       if (key[i] > -INFINITY) sum += (double)expf(key[i] - top);
     sum = group_sum<L>(sum);
   }
+  uint64_t kept = 0;
+  auto group_kept = [&](int e) { return (kept >> (((uint32_t)e * p.group_mul) >> 20) & 1ull) != 0; };
+  if constexpr (kGroups) {
+    __shared__ GroupSmem<L, V> gs;
+    kept = kept_groups<T, L, V, kSigmoid>(p, gs, key, biased, [&](int e) { return logit_value(rows[row0 + e]); });
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = group_kept(i * L + l) ? key[i] : -INFINITY;
+      m = fmaxf(m, key[i]);
+    }
+  }
 
   // the k-th largest lane maximum
-  float bound = top;
+  float bound = kGroups ? group_max<L>(m) : top;
   {
     float rest = m;
     for (int j = 1; j < p.topk; ++j) {
@@ -369,6 +486,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
         const float v = logit_value(rows[row0 + e]);
         const float b = biased ? p.bias[e] : 0.f;
         if (!(v > -INFINITY && b > -INFINITY)) continue;
+        if (kGroups && !group_kept(e)) continue;
         const double c = biased ? exact_key(v, b) : (double)v;
         if (before(last, last_e, c, e) && before(c, e, best, best_e)) {
           best = c;
@@ -457,7 +575,7 @@ constexpr int kNarrowMaxExperts = 512;
 // Longer batches go in pieces, each far below.
 constexpr int kLaunchTokens = 1 << 24;
 
-template <typename T, bool kSigmoid>
+template <typename T, bool kSigmoid, bool kGroups>
 hipError_t launch_piece(const RouteArgs& a, int lanes, hipStream_t stream) {
   const int v = (a.E + lanes - 1) / lanes;
   const int per = kRouteThreads / lanes;
@@ -465,7 +583,7 @@ hipError_t launch_piece(const RouteArgs& a, int lanes, hipStream_t stream) {
   // keys per lane rounded up to a built width
 #define W4A16_ROUTE_CASE(L_, V_)                                                         \
   if (lanes == L_ && v <= V_) {                                                          \
-    hipLaunchKernelGGL((route_kernel<T, L_, V_, kSigmoid>), grid, block, 0, stream, a);  \
+    hipLaunchKernelGGL((route_kernel<T, L_, V_, kSigmoid, kGroups>), grid, block, 0, stream, a);  \
     return hipGetLastError();                                                            \
   }
   W4A16_ROUTE_CASE(16, 8) W4A16_ROUTE_CASE(16, 16) W4A16_ROUTE_CASE(16, 24) W4A16_ROUTE_CASE(16, 32)
@@ -475,16 +593,17 @@ hipError_t launch_piece(const RouteArgs& a, int lanes, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-template <typename T, bool kSigmoid>
+template <typename T, bool kSigmoid, bool kGroups>
 hipError_t launch_typed(const RouteArgs& a, hipStream_t stream) {
-  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens && a.E <= kNarrowMaxExperts;
+  const bool narrow = a.topk <= kNarrowMaxTopk && a.T >= kNarrowMinTokens && a.E <= kNarrowMaxExperts &&
+                      (!kGroups || a.groups <= kNarrowMaxGroups);
   for (int64_t t = 0; t < a.T; t += kLaunchTokens) {
     RouteArgs piece = a;
     piece.logits = static_cast<const T*>(a.logits) + t * a.row_stride;
     piece.T = (int32_t)std::min((int64_t)kLaunchTokens, a.T - t);
     piece.ids = a.ids + t * a.topk;
     piece.weights = a.weights + t * a.topk;
-    const hipError_t e = launch_piece<T, kSigmoid>(piece, narrow ? 16 : 64, stream);
+    const hipError_t e = launch_piece<T, kSigmoid, kGroups>(piece, narrow ? 16 : 64, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -493,17 +612,20 @@ hipError_t launch_typed(const RouteArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_route(const void* logits, int dtype, int64_t row_stride, const float* bias, int32_t T, int32_t E,
-                        int32_t topk, int sigmoid, int renorm, float scale, int32_t* ids, float* weights,
-                        hipStream_t stream) {
-  const RouteArgs a{logits, row_stride, bias, T, E, topk, renorm, scale, ids, weights};
-  switch (2 * dtype + (sigmoid ? 1 : 0)) {
-    case 0: return launch_typed<float, false>(a, stream);
-    case 1: return launch_typed<float, true>(a, stream);
-    case 2: return launch_typed<__bf16, false>(a, stream);
-    case 3: return launch_typed<__bf16, true>(a, stream);
-    case 4: return launch_typed<_Float16, false>(a, stream);
-    case 5: return launch_typed<_Float16, true>(a, stream);
-  }
+                        int32_t groups, int32_t keep, int32_t topk, int sigmoid, int renorm, float scale, int32_t* ids,
+                        float* weights, hipStream_t stream) {
+  if (groups < 1 || groups > kMaxGroups || E % groups) return hipErrorInvalidValue;
+  const int32_t size = E / groups;
+  // e / size = e * ceil(2^20 / size) >> 20 for e < 1024: the excess, e * (size - 1) at most, is below 2^20
+  const uint32_t mul = ((1u << 20) + (uint32_t)size - 1) / (uint32_t)size;
+  const RouteArgs a{logits, row_stride, bias, T, E, topk, groups, size, keep, mul, renorm, scale, ids, weights};
+  const int kind = 2 * dtype + (sigmoid ? 1 : 0);
+#define W4A16_ROUTE_KIND(N_, T_, S_) \
+  if (kind == N_) return groups > 1 ? launch_typed<T_, S_, true>(a, stream) : launch_typed<T_, S_, false>(a, stream);
+  W4A16_ROUTE_KIND(0, float, false) W4A16_ROUTE_KIND(1, float, true)
+  W4A16_ROUTE_KIND(2, __bf16, false) W4A16_ROUTE_KIND(3, __bf16, true)
+  W4A16_ROUTE_KIND(4, _Float16, false) W4A16_ROUTE_KIND(5, _Float16, true)
+#undef W4A16_ROUTE_KIND
   return hipErrorInvalidValue;
 }
 
