@@ -730,7 +730,8 @@ w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, c
                           int32_t T, const w4a16_adapters* adapters, int32_t silu, uint16_t* out, void* workspace,
                           size_t workspace_bytes, w4a16_stream_t stream);
 
-/* Workspace bytes of w4a16_linear (0 without adapters, and on bad arguments). */
+/* Workspace bytes of w4a16_linear (0 on bad arguments; of larger batches
+ * without adapters too). */
 size_t w4a16_linear_workspace_bytes(const w4a16_weight_desc* desc, int32_t T, const w4a16_adapters* adapters);
 
 /* w4a16_moe_gemm with the adapters of the routed experts: a slot of token t

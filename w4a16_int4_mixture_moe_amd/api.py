@@ -821,11 +821,11 @@ def _scratch(nbytes: int, workspace: Optional[torch.Tensor], dev: torch.device) 
 
 
 def linear_workspace_bytes(packed: PackedW4, T: int, adapters: Optional[Adapters] = None) -> int:
-    """Workspace bytes of w4a16_linear on T rows (0 without adapters, and where the call refuses the sizes)."""
-    if adapters is None or not 0 < T < 2**31:
+    """Workspace bytes of w4a16_linear on T rows (0 where the call refuses the sizes)."""
+    if not 0 < T < 2**31:
         return 0
-    ad = adapters.as_c(adapters.b)                        # the token list's address decides nothing here
-    return int(load().w4a16_linear_workspace_bytes(ctypes.byref(packed.desc), T, ctypes.byref(ad)))
+    ad = None if adapters is None else ctypes.byref(adapters.as_c(adapters.b))   # the token list's address decides nothing
+    return int(load().w4a16_linear_workspace_bytes(ctypes.byref(packed.desc), T, ad))
 
 
 def w4a16_linear(x: torch.Tensor, packed: PackedW4, adapters: Optional[Adapters] = None,
@@ -855,13 +855,12 @@ def w4a16_linear(x: torch.Tensor, packed: PackedW4, adapters: Optional[Adapters]
     if adapters is not None:
         c = adapters.as_c(_adapter_ids(adapter_ids, T))
         ad = ctypes.byref(c)
-        if workspace is None:
-            nbytes = load().w4a16_linear_workspace_bytes(ctypes.byref(packed.desc), T, ad)
-        else:
-            nbytes = 0
-        workspace = _scratch(nbytes, workspace, dev)
-        _same_device(x, a=adapters.a, adapter_ids=adapter_ids, workspace=workspace)
-    _same_device(x, weight=packed.w, weight_scales=packed.s, out=out)
+        _same_device(x, a=adapters.a, adapter_ids=adapter_ids)
+    nbytes = 0
+    if workspace is None:
+        nbytes = load().w4a16_linear_workspace_bytes(ctypes.byref(packed.desc), T, ad)
+    workspace = _scratch(nbytes, workspace, dev)
+    _same_device(x, weight=packed.w, weight_scales=packed.s, out=out, workspace=workspace)
     _launch(dev, load().w4a16_linear, ctypes.byref(packed.desc), packed.w.data_ptr(), packed.s.data_ptr(), x.data_ptr(),
             T, ad, int(bool(silu)), out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out

@@ -20,9 +20,14 @@
 // adapter by selection, not by the sum alone, as an infinity or a NaN in one
 // request's B times that zero would reach the other requests.
 #pragma once
+#include <type_traits>
+
 #include "adapter_launch.hpp"
 #include "device_common.hpp"
+#include "gemm_tile.hpp"
 #include "launch.hpp"
+#include "prefill_tile.hpp"
+#include "ring.hpp"
 #include "tile_common.hpp"
 
 namespace w4a16 {
@@ -72,124 +77,163 @@ __device__ __forceinline__ int setup_adapter_rows(const GemmParams& p, const Ada
   }
 }
 
-// this lane's part of a row of h at rank k0 of one slice of A's rows: the sum
-// over the slices of K, then its hi or lo bf16 part
-__device__ __forceinline__ bf16x8_t h_operand(const AdapterParams& q, int slot, int slice, int k0, bool lo) {
-  const int width = q.slices * q.rank;
-  const float* src = q.h + (int64_t)slot * width + slice * q.rank + k0;
-  f32x4_t v[2] = {*reinterpret_cast<const f32x4_t*>(src), *reinterpret_cast<const f32x4_t*>(src + 4)};
-  for (int k = 1; k < q.ks; ++k) {
-    src += q.rows * width;
-    v[0] += *reinterpret_cast<const f32x4_t*>(src);
-    v[1] += *reinterpret_cast<const f32x4_t*>(src + 4);
-  }
-  bf16x8_t r;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = v[e / 4][e % 4];
-    const __bf16 hi = (__bf16)x;
-    const float rest = x - (float)hi;                   // NaN where hi is infinite: hi stands alone there
-    r[e] = lo ? (__bf16)(rest == rest ? rest : 0.f) : hi;
-  }
-  return r;
-}
+// A row's h in LDS, 64 ranks at a time: 16 granules of 8 bf16, granule 4 j + g
+// what lane group g supplies to instruction j (16 ranks: two granules of hi,
+// two of lo).
+constexpr int kHRanks = 64;
 
 __device__ __forceinline__ bf16x8_t zero_operand() { return __builtin_bit_cast(bf16x8_t, u32x4_t{0u, 0u, 0u, 0u}); }
 
-// B_a h of weight tiles rt_base + r < NR and row tiles t < NA, 16 ranks at a
-// time: add(t, r, own, y) with y to be added to the lanes whose row is this
-// adapter's (own).  Waves that share the tiles deal the (row tile, adapter)
-// pairs among them: `step` waves, this one taking every step-th from `first`.
-template <int NR, int NA, typename Smem, typename Add>
-__device__ __forceinline__ void adapter_products(const GemmParams& p, const AdapterParams& q, const Smem& sm, int expert,
-                                                 int rt_base, int first, int step, Add&& add) {
-  constexpr int U = 4;                                  // adapters whose B is in flight together
-  if (q.L == 0) return;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int i = lane & 15, g = lane >> 4;
-  const bool lo = g >= 2;
-  const int chunks = (q.rank + 15) / 16;
-  // row i of each weight tile in B, and the slice of h it multiplies
-  int64_t brow[NR];
-  int slice[NR];
+// Ranks r0 .. of every row of the block that has an adapter: the sum over the
+// slices of K, split in two bf16 parts; zeros past the rank.  place(slice,
+// row, granule) is the granule's address.  The caller synchronises.
+template <int BM, int NTHR, typename Smem, typename Place>
+__device__ __forceinline__ void stage_h(const AdapterParams& q, const Smem& sm, int r0, Place&& place) {
+  const int width = q.slices * q.rank;
+  const int left = min(q.rank - r0, kHRanks);
+  const int eights = (left + 15) / 16 * 2;                // groups of 8 ranks, whole instructions
+  const int items = BM * q.slices * eights;
+  for (int it = threadIdx.x; it < items; it += NTHR) {
+    const int e = it % eights, rest = it / eights;
+    const int row = rest % BM, slice = rest / BM;
+    if (sm.ad[row] < 0) continue;
+    f32x4_t v[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+    if (8 * e < left) {
+      const float* src = q.h + (int64_t)sm.slot[row] * width + slice * q.rank + r0 + 8 * e;
+      const int64_t plane = q.rows * width;
+      // four slices of K in flight together (past the last one: the last again, not added)
+      for (int k0 = 0; k0 < q.ks; k0 += 4) {
+        f32x4_t w[4][2];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int n = q.n0 + logical_tile(p, min(rt_base + r, p.NT - 1)) * kRowTile;
-    slice[r] = q.slices == 2 && n >= q.N / 2 ? 1 : 0;
-    brow[r] = (int64_t)(n + i) * q.rank;
-  }
-  const int64_t per_adapter = (int64_t)q.E * q.N * q.rank, of_expert = (int64_t)expert * q.N * q.rank;
-  int turn = 0;
-#pragma unroll
-  for (int t = 0; t < NA; ++t) {
-    const int mine = sm.ad[16 * t + i];
-    const uint32_t any = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
-    if (!any) continue;
-    const int slot = sm.slot[16 * t + i];
-    const int h_row = mine >= 0 ? slot : sm.slot[16 * t + __builtin_ctz(any)];
-    uint32_t rest = any;
-    while (rest) {
-      int a[U];
-      int n = 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // the next adapter that is this wave's; none left: -1
-        a[u] = kNoAdapter;
-        while (rest && a[u] < 0) {
-          const int next = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
-          rest &= ~(uint32_t)__ballot(mine == next);
-          if (turn == first) {
-            a[u] = next;
-            ++n;
-          }
-          turn = turn + 1 == step ? 0 : turn + 1;
+        for (int k = 0; k < 4; ++k) {
+          const float* from = src + min(k0 + k, q.ks - 1) * plane;
+          w[k][0] = *reinterpret_cast<const f32x4_t*>(from);
+          w[k][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
         }
-      }
-      if (n == 0) break;
-      for (int c = 0; c < chunks; ++c) {
-        const int k0 = 16 * c + 8 * (g & 1);
-        const bool in = k0 < q.rank;
-        const int k = in ? k0 : 0;
-        bf16x8_t b[U][NR];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (u < n) {
-            const uint16_t* base = q.b + (int64_t)a[u] * per_adapter + of_expert + k;
-#pragma unroll
-            for (int r = 0; r < NR; ++r) b[u][r] = *reinterpret_cast<const bf16x8_t*>(base + brow[r]);
-          }
-        bf16x8_t h[2];
-        h[0] = h_operand(q, h_row, 0, k, lo);
-        if (q.slices == 2) h[1] = h_operand(q, h_row, 1, k, lo);
-        else h[1] = h[0];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (u < n) {
-            const bool own = mine == a[u];
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const bf16x8_t bv = in ? b[u][r] : zero_operand();
-              const bf16x8_t hv = own && in ? (slice[r] ? h[1] : h[0]) : zero_operand();
-              add(t, r, own, __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, hv, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0));
-            }
+        for (int k = 0; k < 4; ++k)
+          if (k0 + k < q.ks) {
+            v[0] += w[k][0];
+            v[1] += w[k][1];
           }
       }
     }
+    bf16x8_t hi, lo;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float x = v[c / 4][c % 4];
+      hi[c] = (__bf16)x;
+      const float part = x - (float)hi[c];                // NaN where hi is infinite: hi stands alone there
+      lo[c] = (__bf16)(part == part ? part : 0.f);
+    }
+    *place(slice, row, e / 2 * 4 + (e & 1)) = hi;
+    *place(slice, row, e / 2 * 4 + (e & 1) + 2) = lo;
   }
 }
 
-// acc = the adapters' products (zero past row tile NA, and for rows without an adapter)
-template <int MT, int NR, int NA, typename Smem>
+// What a wave multiplies its h by: row i of each of its weight tiles in B, and
+// the slice of h that the tile takes.
+template <int NR>
+struct AdapterTiles {
+  int64_t row[NR];
+  int slice[NR];
+  __device__ __forceinline__ AdapterTiles(const GemmParams& p, const AdapterParams& q, int rt_base) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int n = q.n0 + logical_tile(p, min(rt_base + r, p.NT - 1)) * kRowTile;
+      slice[r] = q.slices == 2 && n >= q.N / 2 ? 1 : 0;
+      row[r] = (int64_t)(n + (threadIdx.x & 15)) * q.rank;
+    }
+  }
+};
+
+// this lane's operand of B at instruction j of ranks r0 ..; zeros past the rank
+__device__ __forceinline__ bf16x8_t b_operand(const AdapterParams& q, const uint16_t* base, int64_t row, int k) {
+  const bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(base + row + (k < q.rank ? k : 0));
+  return k < q.rank ? v : zero_operand();
+}
+
+// acc = B_a h of the wave's weight tiles and row tiles t < NA (zero past it,
+// and for rows without an adapter).  h goes through LDS, then the adapters of
+// the block are taken in rising order: an adapter's B once for all row tiles
+// that hold it.  at(slice, row, granule): see stage_h; that memory is free
+// before the call and after it (both synchronise).
+template <int MT, int NR, int NW, int NA, typename Smem, typename Place>
 __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const AdapterParams& q, const Smem& sm,
-                                                    int expert, int rt_base, f32x4_t (&acc)[NR][MT]) {
+                                                    int expert, int rt_base, f32x4_t (&acc)[NR][MT], Place&& at) {
+  constexpr int J = kHRanks / 16;
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  adapter_products<NR, NA>(p, q, sm, expert, rt_base, 0, 1, [&](int t, int r, bool own, const f32x4_t& y) {
+  if (q.L == 0) return;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int i = lane & 15, g = lane >> 4;
+  const AdapterTiles<NR> tiles(p, q, rt_base);
+  const int64_t per_adapter = (int64_t)q.E * q.N * q.rank, of_expert = (int64_t)expert * q.N * q.rank;
+  int mine[NA];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[r][t][v] += own ? y[v] : 0.f;
-  });
+  for (int t = 0; t < NA; ++t) mine[t] = sm.ad[16 * t + i];
+  // the least adapter above a
+  auto next_after = [&](int a) {
+    int best = INT32_MAX;
+#pragma unroll
+    for (int t = 0; t < NA; ++t) best = mine[t] > a ? min(best, mine[t]) : best;
+#pragma unroll
+    for (int m = 1; m < 16; m *= 2) best = min(best, __shfl_xor(best, m));
+    return __builtin_amdgcn_readfirstlane(best);
+  };
+  const int first = next_after(-1);
+  if (first == INT32_MAX) return;                       // the whole block, so every wave
+  for (int r0 = 0; r0 < q.rank; r0 += kHRanks) {
+    if (r0 > 0) __syncthreads();
+    stage_h<16 * MT, NW * kWave>(q, sm, r0, at);
+    __syncthreads();
+    const int steps = (min(q.rank - r0, kHRanks) + 15) / 16;
+    for (int a = first; a != INT32_MAX; a = next_after(a)) {
+      const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
+      bf16x8_t b[J][NR];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (j < steps)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) b[j][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
+#pragma unroll
+      for (int t = 0; t < NA; ++t) {
+        const bool own = mine[t] == a;
+        if (!__ballot(own)) continue;
+        f32x4_t y[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) y[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (j < steps) {
+            const bf16x8_t h0 = *at(0, 16 * t + i, 4 * j + g);
+            const bf16x8_t h1 = q.slices == 2 ? *at(1, 16 * t + i, 4 * j + g) : h0;
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+              y[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][r], tiles.slice[r] ? h1 : h0, y[r], 0, 0, 0);
+          }
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[r][t][v] += own ? y[r][v] : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// addresses in the general tile's two activation buffers (rows padded by 16
+// bytes) and in the prefill tiles' (granules permuted by row): a slice each
+template <int MT>
+__device__ __forceinline__ bf16x8_t* h_place(TileSmem<MT>& sm, int slice, int row, int granule) {
+  return reinterpret_cast<bf16x8_t*>(&sm.xs[slice][row][8 * granule]);
+}
+template <int BM>
+__device__ __forceinline__ bf16x8_t* h_place(PfSmem<BM>& sm, int slice, int row, int granule) {
+  const int at = granule ^ (row & 3) ^ (row & 4 ? 12 : 0);
+  return reinterpret_cast<bf16x8_t*>(&sm.xs[slice][row * kChunk + 8 * at]);
 }
 
 // The epilogue of weight tiles rt_base .. rt_base + NR - 1: as `epilogue`, but
@@ -235,115 +279,204 @@ __device__ __forceinline__ void adapter_epilogue(const GemmParams& p, const Smem
   }
 }
 
-// Few rows: NT weight tiles of 16 MT rows a workgroup, its NW waves splitting
-// K and dealing the adapters; chunks go straight into registers, and the
-// partial sums meet in LDS, in wave order.  The adapters' products have a place
-// of their own there, since which wave takes one depends on the other rows of
-// the tile, and a row's sum must not.
-template <int MT, int NT, int NW>
-struct SplitSmem {
-  int row[16 * MT];
-  int out[16 * MT];
-  float w[16 * MT];
-  f32x4_t red[NW][MT][NT][kWave];
-  f32x4_t low[MT][NT][kWave];           // the adapters' products
+// Few rows: the NW waves of a workgroup deal the adapters of its 16 MT rows among
+// them, for NT weight tiles.  The products have a place of their own in LDS,
+// since which wave takes one depends on the other rows of the block, and a row's
+// sum must not.
+template <int MT, int NT>
+struct LowSmem {
+  f32x4_t low[MT][NT][kWave];                // the adapters' products
+  uint16_t h[2][16 * MT][2 * kHRanks + 8];   // 272-byte rows
 };
 
-// acc[r][0] = token tile `wave` of weight tile NT nt + r, in waves below MT
+// before the barrier that follows the rows' setup
+template <int MT, int NT, int NW>
+__device__ __forceinline__ void clear_low(LowSmem<MT, NT>& sm) {
+  f32x4_t* low = &sm.low[0][0][0];
+  for (int i = threadIdx.x; i < MT * NT * kWave; i += NW * kWave) low[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+}
+
+// A barrier for LDS alone: loads in flight stay in flight.
+__device__ __forceinline__ void lds_only_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Lane l = 16 g + i of a chunk's packed words holds row i's K 32 g .. 32 g + 31,
+// word j the 8 from 32 g + 8 j.  An activation row is loaded 64 bytes at a time
+// by four lanes side by side, so instruction j of its operand is K 32 j + 8 g
+// there (64 bytes in one lane would touch 64 cache lines a load, for 16 bytes
+// of each).  So the words change places instead, 4 x 4 over lane groups and
+// words: word j of group g <-> word g of group j.
+__device__ __forceinline__ void transpose_words(u32x4_t& w) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  w = u32x4_t{c[0], c[1], d[0], d[1]};
+}
+
+// ... and every lane needs the scales of all four groups
+__device__ __forceinline__ u32x4_t spread_scales(uint32_t s) {
+  const auto a = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+  return u32x4_t{b[0], b[1], c[0], c[1]};
+}
+
+// The adapters' products into sm.low, U instructions' B in flight together.
+// (Synchronises by LDS alone: loads under way stay under way.)
 template <int MT, int NT, int NW, typename Smem>
+__device__ __forceinline__ void deal_adapters(const GemmParams& p, const AdapterParams& q, Smem& sm, int expert, int rt_base) {
+  constexpr int U = 4;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 15, g = lane >> 4;
+  const AdapterTiles<NT> tiles(p, q, rt_base);
+  const int64_t per_adapter = (int64_t)q.E * q.N * q.rank, of_expert = (int64_t)expert * q.N * q.rank;
+  for (int r0 = 0; r0 < q.rank; r0 += kHRanks) {
+    if (r0 > 0) lds_only_barrier();
+    stage_h<16 * MT, NW * kWave>(q, sm, r0, [&](int slice, int row, int granule) {
+      return reinterpret_cast<bf16x8_t*>(&sm.h[slice][row][8 * granule]);
+    });
+    lds_only_barrier();
+    const int steps = (min(q.rank - r0, kHRanks) + 15) / 16;
+    int turn = 0;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int mine = sm.ad[16 * t + i];
+      uint32_t rest = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
+      // (adapter, instruction) after (adapter, instruction), U at a time
+      int a = kNoAdapter, j = steps;
+      for (bool more = true; more;) {
+        int ua[U], uj[U];
+        bf16x8_t b[U][NT];
+        int n = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (j == steps) {                             // the next adapter that is this wave's
+            a = kNoAdapter;
+            while (rest && a < 0) {
+              const int next = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
+              rest &= ~(uint32_t)__ballot(mine == next);
+              if (turn == wave) a = next;
+              turn = turn + 1 == NW ? 0 : turn + 1;
+            }
+            j = 0;
+          }
+          ua[u] = a;
+          uj[u] = j;
+          if (a >= 0) {
+            const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
+#pragma unroll
+            for (int r = 0; r < NT; ++r) b[u][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
+            ++j;
+            n = u + 1;
+          } else {
+            j = steps;
+          }
+        }
+        more = n == U;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u < n) {
+            const bool own = mine == ua[u];
+            const bf16x8_t h0 = *reinterpret_cast<const bf16x8_t*>(&sm.h[0][16 * t + i][8 * (4 * uj[u] + g)]);
+            const bf16x8_t h1 =
+                q.slices == 2 ? *reinterpret_cast<const bf16x8_t*>(&sm.h[1][16 * t + i][8 * (4 * uj[u] + g)]) : h0;
+#pragma unroll
+            for (int r = 0; r < NT; ++r) {
+              const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[u][r], tiles.slice[r] ? h1 : h0,
+                                                                        f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+              if (own) sm.low[t][r][lane] += y;         // a row's adapter is one wave's
+            }
+          }
+      }
+    }
+  }
+}
+
+// 16 rows on a small grid: NT weight tiles a workgroup, its NW waves splitting
+// K; chunks go straight into registers, and the partial sums meet in LDS, in
+// wave order.
+template <int NT, int NW>
+struct SplitSmem : LowSmem<1, NT> {
+  int row[16];
+  int out[16];
+  float w[16];
+  f32x4_t red[NW][NT][kWave];
+};
+
+// tot[r][0] = weight tile NT nt + r, in wave 0.  D: chunks in flight per wave.
+template <int NT, int NW, int D, typename Smem>
 __device__ __forceinline__ void split_product(const GemmParams& p, const AdapterParams& q, Smem& sm, int expert, int nt,
                                               f32x4_t (&tot)[NT][1]) {
-  static_assert(MT <= NW, "a wave for every token tile");
-  constexpr int KB = MT == 4 ? 2 : MT == 2 ? 4 : 8 / NT;   // chunks in flight per wave
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int g = lane >> 4;
   const int KC = p.KC;
   const int c0 = (int)((int64_t)wave * KC / NW), c1 = (int)((int64_t)(wave + 1) * KC / NW);
-  gptr_t wbase[NT], sbase[NT], xrow[MT];
+  gptr_t wbase[NT], sbase[NT];
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
     const int64_t tile = (int64_t)expert * p.w_tiles + min(NT * nt + r, p.NT - 1);
-    wbase[r] = uniform_ptr(p.packed_w + tile * KC * kWave) + lane * 16;
-    sbase[r] = uniform_ptr(p.packed_s + tile * ((KC + 1) / 2) * kWave) + lane * 4;
+    wbase[r] = uniform_ptr(p.packed_w + tile * KC * kWave);
+    sbase[r] = uniform_ptr(p.packed_s + tile * ((KC + 1) / 2) * kWave);
   }
+  const gptr_t xbase = uniform_ptr(p.a);
   // rows past the block's read its first row, for columns that nothing stores
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int r = sm.row[16 * t + (lane & 15)];
-    xrow[t] = uniform_ptr(p.a) + (int64_t)(r >= 0 ? r : sm.row[0]) * p.K * 2;
-  }
+  const int own_row = sm.row[lane & 15];
+  const uint32_t xoff = (uint32_t)(own_row >= 0 ? own_row : sm.row[0]) * (uint32_t)(p.K * 2) + 16 * g;
   const DequantMasks masks = make_dequant_masks();
-  u32x4_t w[KB][NT];
-  uint32_t sw[KB][NT];
-  bf16x8_t x[KB][MT][4];
-  auto issue = [&](int cb) {
+  u32x4_t w[D][NT];
+  uint32_t sw[D][NT];
+  u32x4_t x[D][4];
+  auto issue = [&](auto st_, int c) {
+    constexpr int st = decltype(st_)::value;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      const int c = max(min(cb + i, c1 - 1), 0);        // past the wave's chunks: loaded again, not used
-      const int k = c * kChunk + g * kGroup;
+    for (int r = 0; r < NT; ++r) {
+      w[st][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16) + lane * 16);
+      sw[st][r] = gload_u32(sbase[r] + (int64_t)(c >> 1) * (kWave * 4) + lane * 4);
+    }
 #pragma unroll
-      for (int r = 0; r < NT; ++r) {
-        w[i][r] = gload_u32x4(wbase[r] + (int64_t)c * (kWave * 16));
-        sw[i][r] = gload_u32(sbase[r] + (int64_t)(c >> 1) * (kWave * 4));
+    for (int j = 0; j < 4; ++j) x[st][j] = gload_u32x4(xbase + (c * kChunk + 32 * j) * 2 + xoff);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f32x4_t acc[NT];
+#pragma unroll
+  for (int r = 0; r < NT; ++r) acc[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](auto st_, int c) {
+    constexpr int st = decltype(st_)::value;
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      transpose_words(w[st][r]);
+      const u32x4_t scales = spread_scales((c & 1) ? (sw[st][r] & 0xFFFF0000u) : (sw[st][r] << 16));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t sbits = scales[j];
+        const float s = __builtin_bit_cast(float, sbits);
+        const bf16x8_t A = dequant8(w[st][r][j], s, -1032.0f * s, 0.0625f * s, -72.0f * s, masks);
+        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, __builtin_bit_cast(bf16x8_t, x[st][j]), acc[r], 0, 0, 0);
       }
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[i][t][j] = __builtin_bit_cast(bf16x8_t, gload_u32x4(xrow[t] + (k < p.K ? k * 2 : 0) + 16 * j));
     }
   };
-  f32x4_t acc[NT][MT];
+  const int last = max(c1 - 1, 0);
+  ring_steps<D>([&](auto st_) { issue(st_, min(c0 + decltype(st_)::value, last)); });
+  if (q.L > 0) deal_adapters<1, NT, NW>(p, q, sm, expert, NT * nt);   // while the first chunks are under way
+  ring_run<D>(c0, c1, multiply, issue);
 #pragma unroll
-  for (int r = 0; r < NT; ++r)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  issue(c0);
-  __builtin_amdgcn_sched_barrier(0);                    // the first chunks are under way while the adapters' parts are found
-  adapter_products<NT, MT>(p, q, sm, expert, NT * nt, wave, NW, [&](int t, int r, bool own, const f32x4_t& y) {
-    if (own) sm.low[t][r][lane] += y;                   // a row's adapter is one wave's
-  });
-  for (int cb = c0; cb < c1; cb += KB) {
-    if (cb > c0) issue(cb);
-#pragma unroll
-    for (int i = 0; i < KB; ++i) {
-      const int c = cb + i;
-      if (c >= c1) break;
-      const bool in = c * kChunk + g * kGroup < p.K;    // a ragged last chunk: zeros past K
-#pragma unroll
-      for (int r = 0; r < NT; ++r) {
-        const float s = __builtin_bit_cast(float, (c & 1) ? (sw[i][r] & 0xFFFF0000u) : (sw[i][r] << 16));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8_t A = dequant8(w[i][r][j], s, -1032.0f * s, 0.0625f * s, -72.0f * s, masks);
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, in ? x[i][t][j] : zero_operand(), acc[r][t], 0, 0, 0);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int r = 0; r < NT; ++r) sm.red[wave][t][r][lane] = acc[r][t];
-  __syncthreads();
-  if (wave >= MT) return;
+  for (int r = 0; r < NT; ++r) sm.red[wave][r][lane] = acc[r];
+  lds_only_barrier();
+  if (wave > 0) return;
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
-    tot[r][0] = sm.red[0][wave][r][lane];
+    tot[r][0] = sm.red[0][r][lane];
 #pragma unroll
-    for (int v = 1; v < NW; ++v) tot[r][0] += sm.red[v][wave][r][lane];
-    tot[r][0] += sm.low[wave][r][lane];
+    for (int v = 1; v < NW; ++v) tot[r][0] += sm.red[v][r][lane];
+    tot[r][0] += sm.low[0][r][lane];
   }
-}
-
-// before the barrier that follows the rows' setup
-template <int MT, int NT, int NW>
-__device__ __forceinline__ void clear_low(SplitSmem<MT, NT, NW>& sm) {
-  f32x4_t* low = &sm.low[0][0][0];
-  for (int i = threadIdx.x; i < MT * NT * kWave; i += NW * kWave) low[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 }
 
 }  // namespace w4a16

@@ -25,10 +25,11 @@ __global__ __launch_bounds__(NW * kWave) void adapter_gemm_kernel(const GemmPara
   __syncthreads();
   const uint32_t tmask = active_tiles<MT>(sm);
   const int rt_base = nt * (NW * NR) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
+  auto place = [&](int slice, int row, int granule) { return h_place<MT>(sm, slice, row, granule); };
   run_tile<MT, NR, NW, 2>(
       p, static_cast<TileSmem<MT>&>(sm), expert, nt, tmask, 0, p.KC,
       [&](f32x4_t(&acc)[NR][MT], auto na) {
-        start_from_adapters<MT, NR, decltype(na)::value>(p, q, sm, expert, rt_base, acc);
+        start_from_adapters<MT, NR, NW, decltype(na)::value>(p, q, sm, expert, rt_base, acc, place);
       },
       [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
         if constexpr (EPI == kEpiWeighted && 16 * NR * NW <= 128)
@@ -47,11 +48,12 @@ __global__ __launch_bounds__(NW * kWave, 8 / NW) void adapter_prefill_kernel(con
   const int expert = setup_adapter_rows<MT, NW, kRouteIndexed, EPI>(p, q, mb, sm);
   if (expert < 0) return;
   __syncthreads();
+  auto place = [&](int slice, int row, int granule) { return h_place<C::BM>(sm, slice, row, granule); };
   pf_run<C, false>(
       p, static_cast<PfSmem<C::BM>&>(sm), expert, nt, nt + 1, active_tiles<MT>(sm),
       [&](auto& acc, auto na, int) {
         const int rt_base = nt * (NW * NR) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
-        start_from_adapters<MT, NR, decltype(na)::value>(p, q, sm, expert, rt_base, acc);
+        start_from_adapters<MT, NR, NW, decltype(na)::value>(p, q, sm, expert, rt_base, acc, place);
       },
       [&](const auto& acc, uint32_t tm, int) { adapter_epilogue<MT, NR, NW, EPI>(p, sm, nt, tm, acc); });
 }
@@ -61,15 +63,15 @@ __global__ __launch_bounds__(NW * kWave, 8 / NW) void adapter_prefill_kernel(con
 template <int EPI>
 __global__ __launch_bounds__(kKwWaves * kWave) void adapter_kwave_kernel(const GemmParams p, const AdapterParams q) {
   constexpr int NT = EPI == kEpiSilu ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) AdapterSmem<SplitSmem<1, NT, kKwWaves>, 16> sm;
+  __shared__ __attribute__((aligned(16))) AdapterSmem<SplitSmem<NT, kKwWaves>, 16> sm;
   int mb, nt;
   if (!block_of(p, blockIdx.x, p.n_tiles, mb, nt)) return;
   const int expert = setup_adapter_rows<1, kKwWaves, kRouteIndexed, EPI>(p, q, mb, sm);
   if (expert < 0) return;
-  clear_low(sm);
+  clear_low<1, NT, kKwWaves>(sm);
   __syncthreads();
   f32x4_t acc[NT][1];
-  split_product<1, NT, kKwWaves>(p, q, sm, expert, nt, acc);
+  split_product<NT, kKwWaves, 7>(p, q, sm, expert, nt, acc);
   if (threadIdx.x >= kWave) return;
   adapter_epilogue<1, NT, 1, EPI>(p, sm, nt, 1u, acc);
 }

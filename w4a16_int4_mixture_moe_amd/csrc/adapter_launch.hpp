@@ -35,14 +35,23 @@ struct ShrinkParams {
   int32_t* order;               // out, with sorted_ids == NULL: see AdapterParams; or NULL
 };
 constexpr int kOrderMaxRows = 16384;     // more rows than one workgroup orders while the others work
+struct ShrinkGrid {
+  int32_t z, parts;             // waves that share a 64-row tile's adapters, parts of A's rows
+  int32_t blocks;
+  int64_t items;                // waves with work
+};
 int shrink_slices(int64_t positions, int32_t width, int32_t KC);
+hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* grid);
 hipError_t launch_adapter_shrink(const ShrinkParams& p, hipStream_t stream);
 
 // The indexed product with adapters (adapter_gemm.hip): tiles of launch_gemm, K not split
 bool adapter_gemm_supported(int epilogue, int m_tiles, int nr, int waves, int stages, int K);
 hipError_t launch_adapter_gemm(int epilogue, int m_tiles, int nr, int waves, int stages, const GemmParams& p,
                                const AdapterParams& q, hipStream_t stream);
-// One weight for all rows, with or without adapters (linear.hip); epilogue kEpiStore or kEpiSilu
-hipError_t launch_linear(int epilogue, const GemmParams& p, const AdapterParams& q, hipStream_t stream);
+// One weight for all rows, with or without adapters (linear.hip); epilogue
+// kEpiStore or kEpiSilu.  sp: what launch_adapter_shrink takes, with p's rows
+// and sp.ad.L == 0 without adapters; parts: linear_parts_bytes(T, N, KC) bytes.
+size_t linear_parts_bytes(int64_t T, int32_t N, int32_t KC);
+hipError_t launch_linear(int epilogue, const GemmParams& p, const ShrinkParams& sp, float* parts, hipStream_t stream);
 
 }  // namespace w4a16

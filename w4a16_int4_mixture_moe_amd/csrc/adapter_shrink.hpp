@@ -1,0 +1,224 @@
+// The first half of a low-rank adapter (adapter.hpp): h_i = s_a A_a x_i in
+// fp32 for every row i that has an adapter a, of an expert e where the rows
+// are routed (A [L][E][S r][K], S r rows of K).
+//
+// Few rows are bound by reading A (S r K bf16 of each adapter in use), many by
+// reading x.  A wave takes 64 consecutive rows, one slice of K and up to 32
+// rows of A; it gathers the rows that share an (adapter, expert) by ballot,
+// 16 of them make one v_mfma_f32_16x16x32_bf16 operand against 16 rows of A,
+// and each such group is one pass over the slice.  So an A is read once for
+// every 64 rows that use it however the requests are mixed, nothing is
+// sorted first, and no wave waits for another: sums of one row from different
+// slices of K go to different planes of h, which the product's start adds in
+// slice order.
+//
+#pragma once
+#include <type_traits>
+
+#include "adapter_launch.hpp"
+#include "device_common.hpp"
+#include "ring.hpp"
+
+namespace w4a16 {
+
+constexpr int kShrinkWaves = 4;
+constexpr int kShrinkThreads = kShrinkWaves * kWave;
+constexpr int kShrinkRows = 64;                 // positions of a wave
+constexpr int kShrinkWidth = 32;                // rows of A of a wave
+constexpr int kMaxAdapters = 1024;
+
+// This lane's operands of chunk c: instruction j takes the 32 K at 32 j, lane
+// group g of them the 8 at 8 g, so four lanes read 64 consecutive bytes of a
+// row.  Past K the row's start is read and cleared before use.
+// (base: the same for the wave; at: the lane's row, and 16 g)
+__device__ __forceinline__ void load_k(gptr_t base, uint32_t at, int c, int K, u32x4_t (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = c * kChunk + 32 * j;
+    v[j] = gload_u32x4(base + (k < K ? k * 2 : 0) + at);
+  }
+}
+
+__device__ __forceinline__ void clear_past(int c, int K, u32x4_t (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c * kChunk + 32 * j >= K) v[j] = u32x4_t{0u, 0u, 0u, 0u};
+}
+
+// the chunks [c0, c1) of 16 M rows of x against 16 W rows of A, D chunks in flight
+template <int M, int W, int D>
+__device__ __forceinline__ void shrink_pass(const ShrinkParams& p, gptr_t abase, const uint32_t (&arow)[2], gptr_t xbase,
+                                            const uint32_t (&xrow)[M], int c0, int c1, f32x4_t (&acc)[M][W]) {
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  u32x4_t a[D][W][4], x[D][M][4];
+  auto request = [&](auto st_, int c) {
+    constexpr int st = decltype(st_)::value;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < W; ++j) load_k(abase, arow[j], c, p.K, a[st][j]);
+#pragma unroll
+    for (int m = 0; m < M; ++m) load_k(xbase, xrow[m], c, p.K, x[st][m]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto use = [&](auto st_, int c) {
+    constexpr int st = decltype(st_)::value;
+    if ((c + 1) * kChunk > p.K) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) clear_past(c, p.K, a[st][j]);
+#pragma unroll
+      for (int m = 0; m < M; ++m) clear_past(c, p.K, x[st][m]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          acc[m][w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[st][w][j]),
+                                                              __builtin_bit_cast(bf16x8_t, x[st][m][j]), acc[m][w], 0, 0, 0);
+  };
+  ring_steps<D>([&](auto st_) { request(st_, min(c0 + decltype(st_)::value, c1 - 1)); });
+  ring_run<D>(c0, c1, use, request);
+}
+
+// The rows in order of their adapters, rows without one last: what makes a
+// product's 16-row tiles hold few adapters each.  Rows of one adapter come in
+// any order (a row's result does not depend on where it stands).
+__device__ __forceinline__ void order_rows(const ShrinkParams& p) {
+  __shared__ int start[kMaxAdapters + 1];
+  const int L = p.ad.L, T = (int)p.positions;
+  for (int b = threadIdx.x; b <= L; b += kShrinkThreads) start[b] = 0;
+  __syncthreads();
+  auto bucket = [&](int t) {
+    const int a = p.ad.ids[t];
+    return (unsigned)a < (unsigned)L ? a : L;
+  };
+  for (int t = threadIdx.x; t < T; t += kShrinkThreads) atomicAdd(&start[bucket(t)], 1);
+  __syncthreads();
+  if (threadIdx.x < kWave) {                            // exclusive sums, a run of buckets a lane
+    const int per = (L + kWave) / kWave;
+    const int b0 = min((int)threadIdx.x * per, L + 1), b1 = min(b0 + per, L + 1);
+    int own = 0;
+    for (int b = b0; b < b1; ++b) own += start[b];
+    int incl = own;
+    for (int d = 1; d < kWave; d *= 2) {
+      const int v = __shfl_up(incl, d);
+      if ((int)threadIdx.x >= d) incl += v;
+    }
+    int run = incl - own;
+    for (int b = b0; b < b1; ++b) {
+      const int n = start[b];
+      start[b] = run;
+      run += n;
+    }
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < T; t += kShrinkThreads) p.order[atomicAdd(&start[bucket(t)], 1)] = t;
+}
+
+// The work of workgroup `block` of the grid (kShrinkThreads threads).  M16: 16-row
+// operands of one pass where an adapter has more than 16 of the 64 rows (4: A is
+// read once for all 64, at the price of 256 registers).
+template <int M16>
+__device__ __forceinline__ void shrink_block(const ShrinkParams& p, const ShrinkGrid& grid, int block) {
+  if (p.order != nullptr) {
+    if (block == 0) {
+      order_rows(p);
+      return;
+    }
+    --block;
+  }
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t item = (int64_t)block * kShrinkWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (item >= grid.items) return;
+  const AdapterParams& q = p.ad;
+  const int part = (int)(item % grid.parts);
+  int64_t left = item / grid.parts;
+  const int z = (int)(left % grid.z);
+  left /= grid.z;
+  const int ks = (int)(left % q.ks);
+  const int64_t pos = (left / q.ks) * kShrinkRows + lane;
+
+  // this lane's row: its (adapter, expert), row of x and row of h
+  int key = -1, x_row = 0, h_row = 0;
+  if (p.sorted_ids != nullptr) {
+    const int64_t end = min(p.positions, (int64_t)*p.num_tokens_padded);
+    if (pos < end) {
+      const int s = p.sorted_ids[pos];
+      const int e = p.expert_ids[pos >> p.block_shift];
+      if ((unsigned)s < (unsigned)p.sentinel && (unsigned)e < (unsigned)q.E) {
+        const int a = q.ids[s / q.topk];
+        if ((unsigned)a < (unsigned)q.L) key = a * q.E + e;
+        x_row = p.a_row_div > 0 ? s / p.a_row_div : (int)pos;
+        h_row = s;
+      }
+    }
+  } else if (pos < p.positions) {
+    const int a = q.ids[pos];
+    if ((unsigned)a < (unsigned)q.L) key = a;
+    x_row = (int)pos;
+    h_row = (int)pos;
+  }
+
+  const int width = q.slices * q.rank;
+  const int i = lane & 15, g = lane >> 4;
+  const int c0 = (int)((int64_t)ks * p.KC / q.ks), c1 = (int)((int64_t)(ks + 1) * p.KC / q.ks);
+  const int j0 = part * kShrinkWidth;
+  const bool both = j0 + 16 < width;
+  float* const plane = q.h + (int64_t)ks * q.rows * width;
+  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (kWave - lane);
+  uint64_t rest = __ballot(key >= 0);
+  for (int d = 0; rest; d = d + 1 == grid.z ? 0 : d + 1) {
+    const int k = __builtin_amdgcn_readlane(key, __builtin_ctzll(rest));
+    const uint64_t same = __ballot(key == k);
+    rest &= ~same;
+    if (d != z) continue;
+    const int n = __popcll(same);
+    // lane j learns the lane of the group's j-th row (a permutation: the others fill the places after them)
+    const int place = (same >> lane) & 1 ? __popcll(same & below) : n + __popcll(~same & below);
+    const int from = __builtin_amdgcn_ds_permute(place * 4, lane);
+    const gptr_t abase = uniform_ptr(q.a + (int64_t)k * width * p.K), xbase = uniform_ptr(p.x);
+    uint32_t arow[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) arow[j] = (uint32_t)min(j0 + 16 * j + i, width - 1) * (uint32_t)(p.K * 2) + 16 * g;
+    float s = 1.f;
+    if (q.scale != nullptr) s = q.scale[k / q.E];
+    auto rows = [&](int m0, auto tiles, auto widths, auto chunks) {
+      constexpr int M = decltype(tiles)::value, W = decltype(widths)::value;
+      uint32_t xrow[M];
+      int out[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int r = 16 * (m0 + m) + i;
+        const int src = __shfl(from, r < n ? r : 0);
+        xrow[m] = (uint32_t)__shfl(x_row, src) * (uint32_t)(p.K * 2) + 16 * g;
+        out[m] = __shfl(h_row, src);
+        if (r >= n) out[m] = -1;
+      }
+      f32x4_t acc[M][W];
+      shrink_pass<M, W, decltype(chunks)::value>(p, abase, arow, xbase, xrow, c0, c1, acc);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int r = j0 + 16 * j + 4 * g;
+          if (out[m] >= 0 && r < width)
+            *reinterpret_cast<f32x4_t*>(plane + (int64_t)out[m] * width + r) = s * acc[m][j];
+        }
+    };
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I4 = std::integral_constant<int, 4>;
+    if (n > 16)
+      for (int m0 = 0; 16 * m0 < n; m0 += M16) rows(m0, std::integral_constant<int, M16>{}, I2{}, I2{});
+    else if (both)
+      rows(0, I1{}, I2{}, I4{});
+    else
+      rows(0, I1{}, I1{}, I4{});
+  }
+}
+
+}  // namespace w4a16

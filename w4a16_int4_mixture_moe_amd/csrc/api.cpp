@@ -1551,6 +1551,8 @@ w4a16_status check_adapters(const w4a16_adapters* ad, const w4a16_weight_desc* d
     return fail(W4A16_ERR_SHAPE, "adapters of [%d, %d, %d] beside a weight [%d, %d, %d]", ad->E, ad->N, ad->K, d->E, d->N,
                 d->K);
   if (ad->slices == 2 && d->N % 32) return fail(W4A16_ERR_SHAPE, "two slices need N %% 32 == 0 (got %d)", d->N);
+  if ((int64_t)ad->slices * ad->rank * ad->K * 2 > ((int64_t)1 << 32))
+    return fail(W4A16_ERR_SHAPE, "one adapter's a of %d x %d values exceeds 4 GiB", ad->slices * ad->rank, ad->K);
   if ((int64_t)ad->L * ad->E >= ((int64_t)1 << 30)) return fail(W4A16_ERR_SHAPE, "L * E = %d * %d too large", ad->L, ad->E);
   if (!ad->a || !ad->b || (T > 0 && !ad->token_adapter)) return fail(W4A16_ERR_ARG, "NULL pointer in adapters");
   if (!aligned16(ad->a) || !aligned16(ad->b)) return fail(W4A16_ERR_ARG, "adapters' a and b must be 16-byte aligned");
@@ -1587,6 +1589,21 @@ w4a16_status check_workspace(size_t need, const void* workspace, size_t workspac
     return fail(W4A16_ERR_WORKSPACE, "this call needs %zu bytes of 16-byte aligned workspace, got %zu", need,
                 workspace ? workspace_bytes : (size_t)0);
   return W4A16_OK;
+}
+
+struct LinearWorkspace {
+  size_t h = 0, order = 0, parts = 0;
+  size_t total() const { return h + order + parts; }
+};
+
+LinearWorkspace linear_workspace(const w4a16_weight_desc* d, int32_t T, const w4a16::AdapterParams* q) {
+  LinearWorkspace w;
+  if (q) {
+    w.h = h_bytes(*q);
+    w.order = al256((size_t)T * sizeof(int32_t));
+  }
+  w.parts = al256(w4a16::linear_parts_bytes(T, d->N, d->chunks));
+  return w;
 }
 
 // Positions of the routing that may hold a slot.
@@ -1648,8 +1665,11 @@ AdapterWorkspace adapter_workspace(const w4a16_config& c, const w4a16_weight_des
 extern "C" {
 
 size_t w4a16_linear_workspace_bytes(const w4a16_weight_desc* desc, int32_t T, const w4a16_adapters* adapters) {
-  if (check_int4_desc(desc) != W4A16_OK || !adapters || T <= 0 || check_adapters(adapters, desc, T) != W4A16_OK) return 0;
-  return h_bytes(adapter_params(*adapters, 1, T, T)) + al256((size_t)T * sizeof(int32_t));
+  if (check_int4_desc(desc) != W4A16_OK || T <= 0) return 0;
+  if (adapters && check_adapters(adapters, desc, T) != W4A16_OK) return 0;
+  w4a16::AdapterParams q;
+  if (adapters) q = adapter_params(*adapters, 1, T, T);
+  return linear_workspace(desc, T, adapters ? &q : nullptr).total();
 }
 
 w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s, const uint16_t* x,
@@ -1666,38 +1686,30 @@ w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, c
     return fail(W4A16_ERR_ARG, "packed weights, activations and output must be 16-byte aligned");
   st = check_offset_range(T, desc->K, "activations");
   if (st != W4A16_OK) return st;
-  w4a16::AdapterParams q;
-  std::memset(&q, 0, sizeof q);
-  q.rows = T;
-  size_t h = 0;
+  w4a16::ShrinkParams sp;
+  std::memset(&sp, 0, sizeof sp);
   if (adapters) {
     st = check_adapters(adapters, desc, T);
     if (st != W4A16_OK) return st;
-    if (T == 0) return W4A16_OK;
-    q = adapter_params(*adapters, 1, T, T);
-    h = h_bytes(q);
-    st = check_workspace(h + al256((size_t)T * sizeof(int32_t)), workspace, workspace_bytes);
-    if (st != W4A16_OK) return st;
   }
   if (T == 0) return W4A16_OK;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (adapters) {
-    q.h = static_cast<float*>(workspace);
-    w4a16::ShrinkParams sp;
-    std::memset(&sp, 0, sizeof sp);
-    sp.ad = q;
-    sp.x = x;
-    sp.K = desc->K;
-    sp.KC = desc->chunks;
-    sp.positions = T;
-    // in one block of 16 rows no order changes anything
-    if (T > 16 && T <= w4a16::kOrderMaxRows) sp.order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + h);
-    q.order = sp.order;
-    const hipError_t e = w4a16::launch_adapter_shrink(sp, s);
-    if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
-  }
+  if (adapters) sp.ad = adapter_params(*adapters, 1, T, T);
+  sp.ad.rows = T;
+  const LinearWorkspace wl = linear_workspace(desc, T, adapters ? &sp.ad : nullptr);
+  st = check_workspace(wl.total(), workspace, workspace_bytes);
+  if (st != W4A16_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  sp.ad.h = reinterpret_cast<float*>(ws);
+  sp.x = x;
+  sp.K = desc->K;
+  sp.KC = desc->chunks;
+  sp.positions = T;
+  // in one block of 16 rows no order changes anything
+  if (adapters && T > 16 && T <= w4a16::kOrderMaxRows) sp.order = reinterpret_cast<int32_t*>(ws + wl.h);
+  sp.ad.order = sp.order;
   const w4a16::GemmParams p = base_params(desc, packed_w, packed_s, x, out, 1, 1);
-  const hipError_t e = w4a16::launch_linear(silu ? w4a16::kEpiSilu : w4a16::kEpiStore, p, q, s);
+  const hipError_t e = w4a16::launch_linear(silu ? w4a16::kEpiSilu : w4a16::kEpiStore, p, sp,
+                                            reinterpret_cast<float*>(ws + wl.h + wl.order), static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "linear launch");
   return W4A16_OK;
 }

@@ -3,14 +3,20 @@
 // (AdapterParams::order), so that a 16-row tile mixes few of them; results go
 // back to the rows' own places.
 //
-// Up to 64 rows, and more where whole tiles would leave most CUs idle: one or
-// two weight tiles a workgroup, its eight waves splitting K (split_product).
-// Otherwise the general 64-row tile or, with K a multiple of 128, the prefill
-// tiles.
+// Where 64-row tiles over all of K would leave CUs idle, K is cut and two kernels
+// do it: the first one's workgroups leave fp32 sums of a slice of K, or, for the
+// adapters, h = s A x, which needs none of those; the second one adds the slices
+// and the adapters' products and stores.  (A CU takes about 32 bytes a ns from
+// its L2, so at few rows the activations count as much as the weights: 64 rows x
+// 7168 x 4096 with a workgroup's waves splitting K, all of x in every CU, took
+// 29 us without adapters.)  More rows run whole tiles, whose accumulators start
+// from the adapters' products.
+#include <algorithm>
 #include <type_traits>
 
 #include "adapter.hpp"
 #include "adapter_launch.hpp"
+#include "adapter_shrink.hpp"
 #include "device_common.hpp"
 #include "gemm_tile.hpp"
 #include "launch.hpp"
@@ -21,22 +27,111 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kSplitWaves = 8;
+// ---- few rows
 
-template <int MT, int NT, int EPI>
-__global__ __launch_bounds__(kSplitWaves * kWave) void linear_split_kernel(const GemmParams p, const AdapterParams q) {
-  __shared__ __attribute__((aligned(16))) AdapterSmem<SplitSmem<MT, NT, kSplitWaves>, 16 * MT> sm;
-  // the blocks of one pair of weight tiles next to each other: they read the same weights
-  const int mb = blockIdx.x % p.grid_blocks, nt = blockIdx.x / p.grid_blocks;
-  setup_adapter_rows<MT, kSplitWaves, kRouteDense, EPI>(p, q, mb, sm);
-  clear_low(sm);
+constexpr int kPartWaves = 4;
+constexpr int kPartTiles = 8;                   // weight tiles of a workgroup of the first kernel
+constexpr int kJoinWaves = 8;
+static_assert(kPartWaves * kWave == kShrinkThreads, "both kinds of workgroup in one launch");
+
+struct PartsParams {
+  float* parts;                 // [slices][T][N], columns in packed order
+  int32_t slices;
+  int32_t shrink_blocks;        // workgroups before the product's
+};
+
+// slice s of the rows of block mb and 128 packed columns
+template <int MT>
+__global__ __launch_bounds__(kPartWaves * kWave, 2) void linear_parts_kernel(const GemmParams p, const ShrinkParams sp,
+                                                                           const ShrinkGrid grid, const PartsParams w) {
+  if ((int)blockIdx.x < w.shrink_blocks) {
+    shrink_block<2>(sp, grid, blockIdx.x);
+    return;
+  }
+  constexpr int NR = kPartTiles / kPartWaves;
+  __shared__ __attribute__((aligned(16))) TileSmem<MT> sm;
+  const int item = (int)blockIdx.x - w.shrink_blocks;
+  const int s = item % w.slices;
+  const int mb = item / w.slices % p.grid_blocks, nt = item / w.slices / p.grid_blocks;
+  const int64_t T = sp.positions;
+  for (int i = threadIdx.x; i < 16 * MT; i += kPartWaves * kWave) sm.row[i] = mb * 16 * MT + i < T ? mb * 16 * MT + i : -1;
   __syncthreads();
-  f32x4_t acc[NT][1];
-  split_product<MT, NT, kSplitWaves>(p, q, sm, 0, nt, acc);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  if (wave >= MT) return;
-  store_tiles<1, NT, EPI>(p, sm.out + 16 * wave, NT * nt, 1u, acc);
+  const int KC2 = (p.KC + 1) / 2;               // whole pairs of chunks, none empty
+  const int c0 = 2 * (int)((int64_t)s * KC2 / w.slices), c1 = min(p.KC, 2 * (int)((int64_t)(s + 1) * KC2 / w.slices));
+  const int lane = threadIdx.x & (kWave - 1);
+  const int rt_base = nt * kPartTiles + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
+  run_tile<MT, NR, kPartWaves, 2>(p, sm, 0, nt, active_tiles<MT>(sm), c0, c1, ZeroStart{},
+                                  [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (rt_base + r >= p.NT) continue;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int row = sm.row[16 * t + (lane & 15)];
+        if (!((tm >> t) & 1u) || row < 0) continue;
+        *reinterpret_cast<f32x4_t*>(w.parts + ((int64_t)s * T + row) * p.N + (rt_base + r) * kRowTile + 4 * (lane >> 4)) =
+            acc[r][t];
+      }
+    }
+  });
 }
+
+template <int MT, int NT>
+struct JoinSmem : LowSmem<MT, NT> {
+  int row[16 * MT];
+  int out[16 * MT];
+  f32x4_t red[kJoinWaves][NT][kWave];
+};
+
+// 16 MT rows (in order of their adapters) and NT packed weight tiles.  Wave v
+// adds every (8 / MT)-th slice of row tile v % MT.
+template <int MT, int NT, int EPI>
+__global__ __launch_bounds__(kJoinWaves * kWave) void linear_join_kernel(const GemmParams p, const AdapterParams q,
+                                                                         const PartsParams w) {
+  __shared__ __attribute__((aligned(16))) AdapterSmem<JoinSmem<MT, NT>, 16 * MT> sm;
+  constexpr int P = kJoinWaves / MT;            // waves of a row tile
+  const int mb = blockIdx.x % p.grid_blocks, nt = blockIdx.x / p.grid_blocks;
+  setup_adapter_rows<MT, kJoinWaves, kRouteDense, EPI>(p, q, mb, sm);
+  clear_low<MT, NT, kJoinWaves>(sm);
+  __syncthreads();
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int t = wave % MT;
+  const int row = max(sm.row[16 * t + (lane & 15)], 0);
+  f32x4_t sum[NT];
+#pragma unroll
+  for (int r = 0; r < NT; ++r) sum[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = wave / MT; s0 < w.slices; s0 += 4 * P) {
+    f32x4_t v[4][NT];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int r = 0; r < NT; ++r)              // past the last slice or tile: loaded again, not added
+        v[u][r] = *reinterpret_cast<const f32x4_t*>(w.parts + ((int64_t)min(s0 + u * P, w.slices - 1) * q.rows + row) * p.N +
+                                                    min(NT * nt + r, p.NT - 1) * kRowTile + 4 * (lane >> 4));
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s0 + u * P < w.slices)
+#pragma unroll
+        for (int r = 0; r < NT; ++r) sum[r] += v[u][r];
+  }
+  if (q.L > 0) deal_adapters<MT, NT, kJoinWaves>(p, q, sm, 0, NT * nt);
+#pragma unroll
+  for (int r = 0; r < NT; ++r) sm.red[wave][r][lane] = sum[r];
+  lds_only_barrier();
+  if (wave >= MT) return;
+  f32x4_t tot[NT][1];
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    tot[r][0] = sm.red[wave][r][lane];
+#pragma unroll
+    for (int v = 1; v < P; ++v) tot[r][0] += sm.red[wave + v * MT][r][lane];
+    tot[r][0] += sm.low[wave][r][lane];
+  }
+  store_tiles<1, NT, EPI>(p, sm.out + 16 * wave, NT * nt, 1u, tot);
+}
+
+// ---- whole tiles
 
 template <int MT, int NR, int EPI>
 __global__ __launch_bounds__(4 * kWave) void linear_tile_kernel(const GemmParams p, const AdapterParams q) {
@@ -47,9 +142,12 @@ __global__ __launch_bounds__(4 * kWave) void linear_tile_kernel(const GemmParams
   setup_adapter_rows<MT, NW, kRouteDense, EPI>(p, q, mb, sm);
   __syncthreads();
   const int rt_base = nt * (NW * NR) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
+  auto place = [&](int slice, int row, int granule) { return h_place<MT>(sm, slice, row, granule); };
   run_tile<MT, NR, NW, 2>(
       p, static_cast<TileSmem<MT>&>(sm), 0, nt, active_tiles<MT>(sm), 0, p.KC,
-      [&](f32x4_t(&acc)[NR][MT], auto na) { start_from_adapters<MT, NR, decltype(na)::value>(p, q, sm, 0, rt_base, acc); },
+      [&](f32x4_t(&acc)[NR][MT], auto na) {
+        start_from_adapters<MT, NR, NW, decltype(na)::value>(p, q, sm, 0, rt_base, acc, place);
+      },
       [&](const f32x4_t(&acc)[NR][MT], uint32_t tm) { store_tiles<MT, NR, EPI>(p, sm.out, rt_base, tm, acc); });
 }
 
@@ -62,50 +160,99 @@ __global__ __launch_bounds__(NW * kWave, 8 / NW) void linear_prefill_kernel(cons
   setup_adapter_rows<MT, NW, kRouteDense, EPI>(p, q, mb, sm);
   __syncthreads();
   const int rt_base = nt * (NW * NR) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * NR;
+  auto place = [&](int slice, int row, int granule) { return h_place<C::BM>(sm, slice, row, granule); };
   pf_run<C, false>(
       p, static_cast<PfSmem<C::BM>&>(sm), 0, nt, nt + 1, active_tiles<MT>(sm),
-      [&](auto& acc, auto na, int) { start_from_adapters<MT, NR, decltype(na)::value>(p, q, sm, 0, rt_base, acc); },
+      [&](auto& acc, auto na, int) {
+        start_from_adapters<MT, NR, NW, decltype(na)::value>(p, q, sm, 0, rt_base, acc, place);
+      },
       [&](const auto& acc, uint32_t tm, int) { store_tiles<MT, NR, EPI>(p, sm.out, rt_base, tm, acc); });
 }
 
 typedef void (*LinearKernel)(const GemmParams, const AdapterParams);
 
-constexpr int64_t kTileMinWorkgroups = 256;     // one a CU
+constexpr int64_t kTileMinWorkgroups = 512;     // 64-row tiles: two a CU
+// Slices of K: about one workgroup of the product a CU, at most 8.  Measured on
+// MI355X, us without / with 32 adapters of rank 16, 7168 x 4096, slices 1 2 4 8 16:
+//   64 rows  43.9 27.6 19.6 16.7 20.6 / 52.3 39.5 31.6 28.3 32.0
+//   128      44.3 29.0 21.5 22.8 29.4 / 56.6 52.2 39.0 39.0 44.1
+// and 2048 x 7168, 64 rows, slices 1 2 4 8: 19.5 16.6 16.8 23.0 / 26.0 22.8 24.9 26.9
+constexpr int64_t kPartWorkgroups = 256;
+constexpr int kMaxSlices = 8;
+constexpr int64_t kPrefillMinWorkgroups = 256;  // 128- and 256-row tiles
 
-hipError_t launch(LinearKernel k, GemmParams p, const AdapterParams& q, int rows, int tiles, int waves, bool split,
+struct LinearPlan {
+  int mt;                       // row tiles of a block; 0: whole tiles
+  int slices;
+};
+
+LinearPlan linear_plan(int64_t T, int32_t N, int32_t KC) {
+  const int64_t cols = (N / 16 + kPartTiles - 1) / kPartTiles;
+  if ((T + 63) / 64 * cols >= kTileMinWorkgroups) return {0, 0};
+  const int mt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  const int64_t tiles = (T + 16 * mt - 1) / (16 * mt) * cols;
+  return {mt, (int)std::max<int64_t>(1, std::min<int64_t>({(kPartWorkgroups + tiles / 2) / tiles, kMaxSlices, (KC + 1) / 2}))};
+}
+
+hipError_t launch(LinearKernel k, GemmParams p, const AdapterParams& q, int rows, int tiles, int waves,
                   hipStream_t stream) {
   p.grid_blocks = (int32_t)((q.rows + rows - 1) / rows);
   p.n_tiles = (p.NT + tiles - 1) / tiles;
-  p.xcd_group = split ? 0 : xcd_group_for(1, p.n_tiles);
-  const int64_t grid = split ? (int64_t)p.grid_blocks * p.n_tiles : grid_of(p, p.n_tiles);
+  p.xcd_group = xcd_group_for(1, p.n_tiles);
+  const int64_t grid = grid_of(p, p.n_tiles);
   if (grid > INT32_MAX / (waves * kWave)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(waves * kWave), 0, stream, p, q);
   return hipGetLastError();
 }
 
-template <int EPI>
-hipError_t launch_of(const GemmParams& p, const AdapterParams& q, hipStream_t stream) {
-  constexpr int ONE = EPI == kEpiSilu ? 2 : 1;
-  const int64_t T = q.rows;
-  auto grid = [&](int rows, int tiles) { return (T + rows - 1) / rows * ((p.NT + tiles - 1) / tiles); };
-  if (T <= 16) return launch(linear_split_kernel<1, ONE, EPI>, p, q, 16, ONE, kSplitWaves, true, stream);
-  if (T <= 32) return launch(linear_split_kernel<2, 2, EPI>, p, q, 32, 2, kSplitWaves, true, stream);
-  if (grid(64, 8) < kTileMinWorkgroups)
-    return launch(linear_split_kernel<4, 2, EPI>, p, q, 64, 2, kSplitWaves, true, stream);
-  if (p.K % kChunk == 0) {
-    if (grid(256, 16) >= kTileMinWorkgroups)
-      return launch(linear_prefill_kernel<16, 2, 8, EPI>, p, q, 256, 16, 8, false, stream);
-    if (grid(128, 16) >= kTileMinWorkgroups)
-      return launch(linear_prefill_kernel<8, 4, 4, EPI>, p, q, 128, 16, 4, false, stream);
+template <int MT, int EPI>
+hipError_t launch_few(GemmParams p, const ShrinkParams& sp, int slices, float* parts, hipStream_t stream) {
+  ShrinkGrid grid{};
+  if (sp.ad.L > 0) {
+    const hipError_t e = shrink_grid(sp, &grid);
+    if (e != hipSuccess) return e;
   }
-  return launch(linear_tile_kernel<4, 2, EPI>, p, q, 64, 8, 4, false, stream);
+  const PartsParams w{parts, slices, grid.blocks};
+  p.grid_blocks = (int32_t)((sp.positions + 16 * MT - 1) / (16 * MT));
+  const int64_t first = (int64_t)grid.blocks + (int64_t)((p.NT + kPartTiles - 1) / kPartTiles) * p.grid_blocks * slices;
+  if (first > INT32_MAX / (kPartWaves * kWave)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(linear_parts_kernel<MT>, dim3((unsigned)first), dim3(kPartWaves * kWave), 0, stream, p, sp, grid, w);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  constexpr int NT = EPI == kEpiSilu ? 2 : 1;
+  const int64_t second = (int64_t)((p.NT + NT - 1) / NT) * p.grid_blocks;
+  if (second > INT32_MAX / (kJoinWaves * kWave)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((linear_join_kernel<MT, NT, EPI>), dim3((unsigned)second), dim3(kJoinWaves * kWave), 0, stream, p,
+                     sp.ad, w);
+  return hipGetLastError();
+}
+
+template <int EPI>
+hipError_t launch_of(const GemmParams& p, const ShrinkParams& sp, float* parts, hipStream_t stream) {
+  const AdapterParams& q = sp.ad;
+  const LinearPlan plan = linear_plan(q.rows, p.N, p.KC);
+  if (plan.mt == 1) return launch_few<1, EPI>(p, sp, plan.slices, parts, stream);
+  if (plan.mt == 2) return launch_few<2, EPI>(p, sp, plan.slices, parts, stream);
+  if (plan.mt == 4) return launch_few<4, EPI>(p, sp, plan.slices, parts, stream);
+  const hipError_t e = launch_adapter_shrink(sp, stream);
+  if (e != hipSuccess) return e;
+  if (p.K % kChunk == 0) {
+    auto grid = [&](int rows) { return (q.rows + rows - 1) / rows * ((p.NT + 15) / 16); };
+    if (grid(256) >= kPrefillMinWorkgroups) return launch(linear_prefill_kernel<16, 2, 8, EPI>, p, q, 256, 16, 8, stream);
+    if (grid(128) >= kPrefillMinWorkgroups) return launch(linear_prefill_kernel<8, 4, 4, EPI>, p, q, 128, 16, 4, stream);
+  }
+  return launch(linear_tile_kernel<4, 2, EPI>, p, q, 64, 8, 4, stream);
 }
 
 }  // namespace
 
-hipError_t launch_linear(int epilogue, const GemmParams& p, const AdapterParams& q, hipStream_t stream) {
-  if (q.rows <= 0) return hipSuccess;
-  return epilogue == kEpiSilu ? launch_of<kEpiSilu>(p, q, stream) : launch_of<kEpiStore>(p, q, stream);
+size_t linear_parts_bytes(int64_t T, int32_t N, int32_t KC) {
+  return (size_t)linear_plan(T, N, KC).slices * (size_t)T * N * sizeof(float);
+}
+
+hipError_t launch_linear(int epilogue, const GemmParams& p, const ShrinkParams& sp, float* parts, hipStream_t stream) {
+  if (sp.ad.rows <= 0) return hipSuccess;
+  return epilogue == kEpiSilu ? launch_of<kEpiSilu>(p, sp, parts, stream) : launch_of<kEpiStore>(p, sp, parts, stream);
 }
 
 }  // namespace w4a16

@@ -1,0 +1,45 @@
+// A ring of registers: D chunks in flight, the next one requested as soon as a
+// chunk has been used.
+#pragma once
+#include <type_traits>
+
+#include "device_common.hpp"
+
+namespace w4a16 {
+
+// step(0), step(1), ..., step(D - 1) with compile-time indices (registers take no other)
+template <int D, int I = 0, typename Step>
+__device__ __forceinline__ void ring_steps(Step&& step) {
+  if constexpr (I < D) {
+    step(std::integral_constant<int, I>{});
+    ring_steps<D, I + 1>(step);
+  }
+}
+
+// use(st, c) of the chunks c = c0 .. c1 - 1, request(st, c) D chunks ahead; the
+// caller has requested the first D.  Requests are never conditional (a load that
+// a branch may skip would make the compiler count fewer in flight and wait too
+// early), so the ring turns while all of its refills exist, and what is left
+// is requested together, the last chunk again in the places past it.
+template <int D, typename Use, typename Request>
+__device__ __forceinline__ void ring_run(int c0, int c1, Use&& use, Request&& request) {
+  int cb = c0;
+  for (; cb + 2 * D <= c1; cb += D)
+    ring_steps<D>([&](auto st) {
+      use(st, cb + decltype(st)::value);
+      request(st, cb + decltype(st)::value + D);
+    });
+  auto drain = [&]() {
+    ring_steps<D>([&](auto st) {
+      if (cb + decltype(st)::value < c1) use(st, cb + decltype(st)::value);
+    });
+    cb += D;
+  };
+  drain();
+  if (cb < c1) {
+    ring_steps<D>([&](auto st) { request(st, min(cb + decltype(st)::value, c1 - 1)); });
+    drain();
+  }
+}
+
+}  // namespace w4a16
