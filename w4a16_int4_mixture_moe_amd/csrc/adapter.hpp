@@ -101,17 +101,17 @@ __device__ __forceinline__ void stage_h(const AdapterParams& q, const Smem& sm, 
     if (8 * e < left) {
       const float* src = q.h + (int64_t)sm.slot[row] * width + slice * q.rank + r0 + 8 * e;
       const int64_t plane = q.rows * width;
-      // four slices of K in flight together (past the last one: the last again, not added)
-      for (int k0 = 0; k0 < q.ks; k0 += 4) {
-        f32x4_t w[4][2];
+      // eight slices of K in flight together (past the last one: the last again, not added)
+      for (int k0 = 0; k0 < q.ks; k0 += 8) {
+        f32x4_t w[8][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const float* from = src + min(k0 + k, q.ks - 1) * plane;
           w[k][0] = *reinterpret_cast<const f32x4_t*>(from);
           w[k][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (k0 + k < q.ks) {
             v[0] += w[k][0];
             v[1] += w[k][1];
@@ -279,9 +279,9 @@ __device__ __forceinline__ void adapter_epilogue(const GemmParams& p, const Smem
   }
 }
 
-// Few rows: the NW waves of a workgroup deal the adapters of its 16 MT rows among
-// them, for NT weight tiles.  The products have a place of their own in LDS,
-// since which wave takes one depends on the other rows of the block, and a row's
+// Few rows: NW / MT waves for each of a block's MT row tiles, which deal the
+// tile's adapters among them.  The products have a place of their own in LDS,
+// since which wave takes one depends on the other rows of the tile, and a row's
 // sum must not.
 template <int MT, int NT>
 struct LowSmem {
@@ -325,76 +325,89 @@ __device__ __forceinline__ u32x4_t spread_scales(uint32_t s) {
   return u32x4_t{b[0], b[1], c[0], c[1]};
 }
 
-// The adapters' products into sm.low, U instructions' B in flight together.
-// (Synchronises by LDS alone: loads under way stay under way.)
+// The adapters' products of row tile wave % MT into sm.low, U instructions' B in
+// flight together, the first ones while h is on its way.  (Synchronises by LDS
+// alone: loads under way stay under way.)
 template <int MT, int NT, int NW, typename Smem>
 __device__ __forceinline__ void deal_adapters(const GemmParams& p, const AdapterParams& q, Smem& sm, int expert, int rt_base) {
-  constexpr int U = 4;
+  constexpr int U = 8 / NT;
+  constexpr int P = NW / MT;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int i = lane & 15, g = lane >> 4;
+  const int t = wave % MT;
   const AdapterTiles<NT> tiles(p, q, rt_base);
   const int64_t per_adapter = (int64_t)q.E * q.N * q.rank, of_expert = (int64_t)expert * q.N * q.rank;
+  const int mine = sm.ad[16 * t + i];
+  const uint32_t rows = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
+  f32x4_t low[NT];
+#pragma unroll
+  for (int r = 0; r < NT; ++r) low[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  bool took = false;                                    // this wave has the lane's row
   for (int r0 = 0; r0 < q.rank; r0 += kHRanks) {
+    const int steps = (min(q.rank - r0, kHRanks) + 15) / 16;
+    // (adapter, instruction) after (adapter, instruction) of every P-th adapter
+    uint32_t rest = rows;
+    int turn = 0, a = kNoAdapter, j = steps;
+    int ua[U], uj[U], n;
+    bf16x8_t b[U][NT];
+    auto request = [&]() {
+      n = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j == steps) {
+          a = kNoAdapter;
+          while (rest && a < 0) {
+            const int next = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
+            rest &= ~(uint32_t)__ballot(mine == next);
+            if (turn == wave / MT) a = next;
+            turn = turn + 1 == P ? 0 : turn + 1;
+          }
+          j = 0;
+        }
+        ua[u] = a;
+        uj[u] = j;
+        if (a < 0) {
+          j = steps;
+          continue;
+        }
+        const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
+#pragma unroll
+        for (int r = 0; r < NT; ++r) b[u][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
+        ++j;
+        n = u + 1;
+      }
+    };
+    request();
     if (r0 > 0) lds_only_barrier();
     stage_h<16 * MT, NW * kWave>(q, sm, r0, [&](int slice, int row, int granule) {
       return reinterpret_cast<bf16x8_t*>(&sm.h[slice][row][8 * granule]);
     });
     lds_only_barrier();
-    const int steps = (min(q.rank - r0, kHRanks) + 15) / 16;
-    int turn = 0;
+    while (n > 0) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int mine = sm.ad[16 * t + i];
-      uint32_t rest = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
-      // (adapter, instruction) after (adapter, instruction), U at a time
-      int a = kNoAdapter, j = steps;
-      for (bool more = true; more;) {
-        int ua[U], uj[U];
-        bf16x8_t b[U][NT];
-        int n = 0;
+      for (int u = 0; u < U; ++u)
+        if (u < n) {
+          const bool own = mine == ua[u];
+          took = took || own;
+          const bf16x8_t h0 = *reinterpret_cast<const bf16x8_t*>(&sm.h[0][16 * t + i][8 * (4 * uj[u] + g)]);
+          const bf16x8_t h1 =
+              q.slices == 2 ? *reinterpret_cast<const bf16x8_t*>(&sm.h[1][16 * t + i][8 * (4 * uj[u] + g)]) : h0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (j == steps) {                             // the next adapter that is this wave's
-            a = kNoAdapter;
-            while (rest && a < 0) {
-              const int next = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
-              rest &= ~(uint32_t)__ballot(mine == next);
-              if (turn == wave) a = next;
-              turn = turn + 1 == NW ? 0 : turn + 1;
-            }
-            j = 0;
-          }
-          ua[u] = a;
-          uj[u] = j;
-          if (a >= 0) {
-            const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
+          for (int r = 0; r < NT; ++r) {
+            const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[u][r], tiles.slice[r] ? h1 : h0,
+                                                                      f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < NT; ++r) b[u][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
-            ++j;
-            n = u + 1;
-          } else {
-            j = steps;
+            for (int v = 0; v < 4; ++v) low[r][v] += own ? y[v] : 0.f;
           }
         }
-        more = n == U;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (u < n) {
-            const bool own = mine == ua[u];
-            const bf16x8_t h0 = *reinterpret_cast<const bf16x8_t*>(&sm.h[0][16 * t + i][8 * (4 * uj[u] + g)]);
-            const bf16x8_t h1 =
-                q.slices == 2 ? *reinterpret_cast<const bf16x8_t*>(&sm.h[1][16 * t + i][8 * (4 * uj[u] + g)]) : h0;
-#pragma unroll
-            for (int r = 0; r < NT; ++r) {
-              const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[u][r], tiles.slice[r] ? h1 : h0,
-                                                                        f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-              if (own) sm.low[t][r][lane] += y;         // a row's adapter is one wave's
-            }
-          }
-      }
+      if (n < U) break;
+      request();
     }
   }
+  if (took)
+#pragma unroll
+    for (int r = 0; r < NT; ++r) sm.low[t][r][lane] = low[r];
 }
 
 // 16 rows on a small grid: NT weight tiles a workgroup, its NW waves splitting

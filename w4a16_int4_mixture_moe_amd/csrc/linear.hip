@@ -32,6 +32,7 @@ namespace {
 constexpr int kPartWaves = 4;
 constexpr int kPartTiles = 8;                   // weight tiles of a workgroup of the first kernel
 constexpr int kJoinWaves = 8;
+constexpr int kMaxSlices = 8;
 static_assert(kPartWaves * kWave == kShrinkThreads, "both kinds of workgroup in one launch");
 
 struct PartsParams {
@@ -98,26 +99,26 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void linear_join_kernel(const G
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int t = wave % MT;
   const int row = max(sm.row[16 * t + (lane & 15)], 0);
+  constexpr int S = kMaxSlices / P;             // slices of a wave, at most
+  f32x4_t v[S][NT];
+#pragma unroll
+  for (int u = 0; u < S; ++u)
+    if (wave / MT + u * P < w.slices)
+#pragma unroll
+      for (int r = 0; r < NT; ++r)              // past the last tile: loaded again, not stored
+        v[u][r] = *reinterpret_cast<const f32x4_t*>(w.parts + ((int64_t)(wave / MT + u * P) * q.rows + row) * p.N +
+                                                    min(NT * nt + r, p.NT - 1) * kRowTile + 4 * (lane >> 4));
+  __builtin_amdgcn_sched_barrier(0);
+  if (q.L > 0) deal_adapters<MT, NT, kJoinWaves>(p, q, sm, 0, NT * nt);
   f32x4_t sum[NT];
 #pragma unroll
-  for (int r = 0; r < NT; ++r) sum[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int s0 = wave / MT; s0 < w.slices; s0 += 4 * P) {
-    f32x4_t v[4][NT];
+  for (int r = 0; r < NT; ++r) {
+    sum[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int r = 0; r < NT; ++r)              // past the last slice or tile: loaded again, not added
-        v[u][r] = *reinterpret_cast<const f32x4_t*>(w.parts + ((int64_t)min(s0 + u * P, w.slices - 1) * q.rows + row) * p.N +
-                                                    min(NT * nt + r, p.NT - 1) * kRowTile + 4 * (lane >> 4));
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (s0 + u * P < w.slices)
-#pragma unroll
-        for (int r = 0; r < NT; ++r) sum[r] += v[u][r];
+    for (int u = 0; u < S; ++u)
+      if (wave / MT + u * P < w.slices) sum[r] += v[u][r];
+    sm.red[wave][r][lane] = sum[r];
   }
-  if (q.L > 0) deal_adapters<MT, NT, kJoinWaves>(p, q, sm, 0, NT * nt);
-#pragma unroll
-  for (int r = 0; r < NT; ++r) sm.red[wave][r][lane] = sum[r];
   lds_only_barrier();
   if (wave >= MT) return;
   f32x4_t tot[NT][1];
@@ -171,14 +172,12 @@ __global__ __launch_bounds__(NW * kWave, 8 / NW) void linear_prefill_kernel(cons
 
 typedef void (*LinearKernel)(const GemmParams, const AdapterParams);
 
-constexpr int64_t kTileMinWorkgroups = 512;     // 64-row tiles: two a CU
-// Slices of K: about one workgroup of the product a CU, at most 8.  Measured on
+// Slices of K: about one workgroup of the product a CU, at most kMaxSlices.  Measured on
 // MI355X, us without / with 32 adapters of rank 16, 7168 x 4096, slices 1 2 4 8 16:
 //   64 rows  43.9 27.6 19.6 16.7 20.6 / 52.3 39.5 31.6 28.3 32.0
 //   128      44.3 29.0 21.5 22.8 29.4 / 56.6 52.2 39.0 39.0 44.1
 // and 2048 x 7168, 64 rows, slices 1 2 4 8: 19.5 16.6 16.8 23.0 / 26.0 22.8 24.9 26.9
 constexpr int64_t kPartWorkgroups = 256;
-constexpr int kMaxSlices = 8;
 constexpr int64_t kPrefillMinWorkgroups = 256;  // 128- and 256-row tiles
 
 struct LinearPlan {
@@ -187,11 +186,11 @@ struct LinearPlan {
 };
 
 LinearPlan linear_plan(int64_t T, int32_t N, int32_t KC) {
-  const int64_t cols = (N / 16 + kPartTiles - 1) / kPartTiles;
-  if ((T + 63) / 64 * cols >= kTileMinWorkgroups) return {0, 0};
   const int mt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-  const int64_t tiles = (T + 16 * mt - 1) / (16 * mt) * cols;
-  return {mt, (int)std::max<int64_t>(1, std::min<int64_t>({(kPartWorkgroups + tiles / 2) / tiles, kMaxSlices, (KC + 1) / 2}))};
+  const int64_t tiles = (T + 16 * mt - 1) / (16 * mt) * ((N / 16 + kPartTiles - 1) / kPartTiles);
+  const int64_t slices = (kPartWorkgroups + tiles / 2) / tiles;
+  if (T > 64 && slices <= 1) return {0, 0};
+  return {mt, (int)std::max<int64_t>(1, std::min<int64_t>({slices, kMaxSlices, (KC + 1) / 2}))};
 }
 
 hipError_t launch(LinearKernel k, GemmParams p, const AdapterParams& q, int rows, int tiles, int waves,
