@@ -87,7 +87,8 @@ __device__ __forceinline__ bf16x8_t zero_operand() { return __builtin_bit_cast(b
 // Ranks r0 .. of every row of the block that has an adapter: the sum over the
 // slices of K, split in two bf16 parts; zeros past the rank.  place(slice,
 // row, granule) is the granule's address.  The caller synchronises.
-template <int BM, int NTHR, typename Smem, typename Place>
+// KP: slices in flight together.
+template <int BM, int NTHR, int KP, typename Smem, typename Place>
 __device__ __forceinline__ void stage_h(const AdapterParams& q, const Smem& sm, int r0, Place&& place) {
   const int width = q.slices * q.rank;
   const int left = min(q.rank - r0, kHRanks);
@@ -101,17 +102,16 @@ __device__ __forceinline__ void stage_h(const AdapterParams& q, const Smem& sm, 
     if (8 * e < left) {
       const float* src = q.h + (int64_t)sm.slot[row] * width + slice * q.rank + r0 + 8 * e;
       const int64_t plane = q.rows * width;
-      // eight slices of K in flight together (past the last one: the last again, not added)
-      for (int k0 = 0; k0 < q.ks; k0 += 8) {
-        f32x4_t w[8][2];
+      for (int k0 = 0; k0 < q.ks; k0 += KP) {             // past the last one: the last again, not added
+        f32x4_t w[KP][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < KP; ++k) {
           const float* from = src + min(k0 + k, q.ks - 1) * plane;
           w[k][0] = *reinterpret_cast<const f32x4_t*>(from);
           w[k][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < KP; ++k)
           if (k0 + k < q.ks) {
             v[0] += w[k][0];
             v[1] += w[k][1];
@@ -161,7 +161,7 @@ __device__ __forceinline__ bf16x8_t b_operand(const AdapterParams& q, const uint
 template <int MT, int NR, int NW, int NA, typename Smem, typename Place>
 __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const AdapterParams& q, const Smem& sm,
                                                     int expert, int rt_base, f32x4_t (&acc)[NR][MT], Place&& at) {
-  constexpr int J = kHRanks / 16;
+  constexpr int U = NR == 4 ? 2 : 4;
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -187,37 +187,43 @@ __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const A
   if (first == INT32_MAX) return;                       // the whole block, so every wave
   for (int r0 = 0; r0 < q.rank; r0 += kHRanks) {
     if (r0 > 0) __syncthreads();
-    stage_h<16 * MT, NW * kWave>(q, sm, r0, at);
+    stage_h<16 * MT, NW * kWave, MT <= 4 ? 4 : 2>(q, sm, r0, at);
     __syncthreads();
     const int steps = (min(q.rank - r0, kHRanks) + 15) / 16;
-    for (int a = first; a != INT32_MAX; a = next_after(a)) {
-      const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
-      bf16x8_t b[J][NR];
+    // (adapter, instruction) after (adapter, instruction), U of them in flight
+    for (int a = first, j = 0; a != INT32_MAX;) {
+      int ua[U], uj[U];
+      bf16x8_t b[U][NR];
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (j < steps)
+      for (int u = 0; u < U; ++u) {
+        ua[u] = a;
+        uj[u] = j;
+        if (a == INT32_MAX) continue;
+        const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
 #pragma unroll
-          for (int r = 0; r < NR; ++r) b[j][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
+        for (int r = 0; r < NR; ++r) b[u][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
+        if (++j == steps) {
+          j = 0;
+          a = next_after(a);
+        }
+      }
 #pragma unroll
-      for (int t = 0; t < NA; ++t) {
-        const bool own = mine[t] == a;
-        if (!__ballot(own)) continue;
-        f32x4_t y[NR];
+      for (int u = 0; u < U; ++u) {
+        if (ua[u] == INT32_MAX) continue;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) y[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < NA; ++t) {
+          const bool own = mine[t] == ua[u];
+          if (!__ballot(own)) continue;
+          const bf16x8_t h0 = *at(0, 16 * t + i, 4 * uj[u] + g);
+          const bf16x8_t h1 = q.slices == 2 ? *at(1, 16 * t + i, 4 * uj[u] + g) : h0;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (j < steps) {
-            const bf16x8_t h0 = *at(0, 16 * t + i, 4 * j + g);
-            const bf16x8_t h1 = q.slices == 2 ? *at(1, 16 * t + i, 4 * j + g) : h0;
+          for (int r = 0; r < NR; ++r) {
+            const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[u][r], tiles.slice[r] ? h1 : h0,
+                                                                      f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-              y[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][r], tiles.slice[r] ? h1 : h0, y[r], 0, 0, 0);
+            for (int v = 0; v < 4; ++v) acc[r][t][v] += own ? y[v] : 0.f;
           }
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[r][t][v] += own ? y[r][v] : 0.f;
+        }
       }
     }
   }
@@ -380,7 +386,7 @@ __device__ __forceinline__ void deal_adapters(const GemmParams& p, const Adapter
     };
     request();
     if (r0 > 0) lds_only_barrier();
-    stage_h<16 * MT, NW * kWave>(q, sm, r0, [&](int slice, int row, int granule) {
+    stage_h<16 * MT, NW * kWave, 4>(q, sm, r0, [&](int slice, int row, int granule) {
       return reinterpret_cast<bf16x8_t*>(&sm.h[slice][row][8 * granule]);
     });
     lds_only_barrier();

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kKwWaves * kWave) void adapter_kwave_kernel(const G
   clear_low<1, NT, kKwWaves>(sm);
   __syncthreads();
   f32x4_t acc[NT][1];
-  split_product<NT, kKwWaves, 7>(p, q, sm, expert, nt, acc);
+  split_product<NT, kKwWaves, 4>(p, q, sm, expert, nt, acc);
   if (threadIdx.x >= kWave) return;
   adapter_epilogue<1, NT, 1, EPI>(p, sm, nt, 1u, acc);
 }

@@ -32,15 +32,18 @@ struct ShrinkParams {
   int32_t block_shift;          // log2 of the routing's block_m
   int32_t sentinel, a_row_div;  // as in GemmParams
   int64_t positions;            // bound of the sorted positions, or the rows
+  int64_t expected;             // under uniform routing: positions in use, with their blocks' padding,
+  int64_t expected_rows;        // and rows in them
   int32_t* order;               // out, with sorted_ids == NULL: see AdapterParams; or NULL
+  int32_t in_order;             // the rows are taken in the order ad.order says, which is there already
 };
 constexpr int kOrderMaxRows = 16384;     // more rows than one workgroup orders while the others work
 struct ShrinkGrid {
-  int32_t z, parts;             // waves that share a 64-row tile's adapters, parts of A's rows
-  int32_t blocks;
-  int64_t items;                // waves with work
+  int32_t z;                    // workgroups that share a 64-row tile's adapters
+  int32_t parts, kw;            // parts of A's rows, 32 kw rows each
+  int32_t items, blocks;        // workgroups of the rows, and of the launch
 };
-int shrink_slices(int64_t positions, int32_t width, int32_t KC);
+int shrink_slices(int64_t expected, int32_t width, int32_t KC);
 hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* grid);
 hipError_t launch_adapter_shrink(const ShrinkParams& p, hipStream_t stream);
 

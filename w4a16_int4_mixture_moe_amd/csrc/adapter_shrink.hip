@@ -4,49 +4,214 @@
 #include "adapter_launch.hpp"
 #include "adapter_shrink.hpp"
 #include "device_common.hpp"
+#include "prefill_tile.hpp"
 
 namespace w4a16 {
 
 namespace {
 
 __global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_kernel(const ShrinkParams p, const ShrinkGrid grid) {
-  shrink_block<4>(p, grid, blockIdx.x);
+  shrink_block<2>(p, grid, blockIdx.x);
 }
 
-constexpr int64_t kShrinkItems = 2048;          // waves that keep 1024 SIMDs busy
-constexpr int kShrinkMaxSlices = 16;
+// Many rows: 128 positions and 128 rows of A a workgroup, the rows of x staged
+// by LDS-DMA for its four waves, which take 32 rows of A each.  What bounds the
+// first kernel there is what a CU can load (about 25 bytes a ns from L2): every
+// wave of it loads x for itself.  Measured on MI355X, 8192 rows of 24 requests x
+// 7168, rank 64 twice: SHRINK_FIRST us that way, SHRINK_TILE us this way.
+//
+// A chunk of a row is 16 granules of 16 bytes, granule q at position
+// q ^ (row % 16) of the row's 256 bytes, so that the 16 rows that a lane group
+// reads at once lie in different banks.
+constexpr int kTileRows = 128;
+
+struct ShrinkTileSmem {
+  uint16_t xs[2][kTileRows * kChunk];
+  uint32_t xoff[kTileRows];
+  int key[kTileRows];
+  int h[kTileRows];
+};
+
+__global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_tile_kernel(const ShrinkParams p, int parts) {
+  __shared__ __attribute__((aligned(16))) ShrinkTileSmem sm;
+  const AdapterParams& q = p.ad;
+  constexpr int MT = kTileRows / 16;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int i = lane & 15, g = lane >> 4;
+  int left = blockIdx.x / parts;
+  const int j0 = ((int)blockIdx.x - left * parts) * (kShrinkWaves * kShrinkWidth) + wave * kShrinkWidth;
+  const int ks = left % q.ks;
+  const int64_t tile = left / q.ks;
+  if (threadIdx.x < kTileRows) {
+    const ShrinkRow r = shrink_row(p, tile * kTileRows + threadIdx.x);
+    sm.key[threadIdx.x] = r.key;
+    sm.xoff[threadIdx.x] = (uint32_t)r.x * (uint32_t)(p.K * 2);
+    sm.h[threadIdx.x] = r.h;
+  }
+  __syncthreads();
+  const int width = q.slices * q.rank;
+  const int c0 = (int)((int64_t)ks * p.KC / q.ks), c1 = (int)((int64_t)(ks + 1) * p.KC / q.ks);
+  float* const plane = q.h + (int64_t)ks * q.rows * width;
+  int mine[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) mine[t] = sm.key[16 * t + i];
+  // the least key above k
+  auto next_after = [&](int k) {
+    int best = INT32_MAX;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) best = mine[t] > k ? min(best, mine[t]) : best;
+#pragma unroll
+    for (int m = 1; m < 16; m *= 2) best = min(best, __shfl_xor(best, m));
+    return __builtin_amdgcn_readfirstlane(best);
+  };
+  const gptr_t xbase = uniform_ptr(p.x);
+  for (int k = next_after(-1); k != INT32_MAX; k = next_after(k)) {
+    uint32_t active = 0;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      if (__ballot(mine[t] == k)) active |= 1u << t;
+    // LDS-DMA of a chunk: instruction wave + 4 t writes rows 16 t + 4 wave .. + 3 (one row tile a turn), lane l
+    // position l % 16 of row l / 16 of them
+    const int row = 4 * wave + g;
+    const uint32_t gran = (uint32_t)((i ^ row) * 16);
+    auto stage = [&](int c) {
+      const gptr_t base = xbase + (int64_t)c * (kChunk * 2) + gran;
+      char* to = reinterpret_cast<char*>(&sm.xs[c & 1][0]) + wave * 1024;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if ((active >> t) & 1u) dma16(base + sm.xoff[16 * t + row], (lds_ptr_t)(to + t * 4096));
+    };
+    const gptr_t abase = uniform_ptr(q.a + (int64_t)k * width * p.K);
+    uint32_t arow[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) arow[j] = (uint32_t)min(j0 + 16 * j + i, width - 1) * (uint32_t)(p.K * 2) + 16 * g;
+    u32x4_t a[2][2][4];
+    f32x4_t acc[MT][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto request = [&](auto st_, int c) {
+      constexpr int st = decltype(st_)::value;
+      stage(c);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_k(abase, arow[j], c, p.K, a[st][j]);
+    };
+    auto use = [&](auto st_, int c) {
+      constexpr int st = decltype(st_)::value;
+      const char* xs = reinterpret_cast<const char*>(&sm.xs[c & 1][0]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = (uint32_t)(i * 256 + ((4 * j + g) ^ i) * 16);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          if ((active >> t) & 1u) {
+            const bf16x8_t x = *reinterpret_cast<const bf16x8_t*>(xs + t * 4096 + at);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              acc[t][w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[st][w][j]), x, acc[t][w], 0, 0, 0);
+          }
+      }
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    // a chunk ahead; c0 may be odd, so the LDS buffer goes by c and the registers by c - c0
+    request(I0{}, c0);
+    wait_vmcnt<0>();                                    // this wave's part of the chunk is in LDS ...
+    __syncthreads();                                    // ... and every wave's
+    for (int c = c0; c < c1; c += 2) {
+      if (c + 1 < c1) request(I1{}, c + 1);
+      use(I0{}, c);
+      wait_vmcnt<0>();
+      __syncthreads();
+      if (c + 1 >= c1) break;
+      if (c + 2 < c1) request(I0{}, c + 2);
+      use(I1{}, c + 1);
+      wait_vmcnt<0>();
+      __syncthreads();
+    }
+    const float s = q.scale != nullptr ? q.scale[k / q.E] : 1.f;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = j0 + 16 * j + 4 * g;
+        if (mine[t] == k && r < width)
+          *reinterpret_cast<f32x4_t*>(plane + (int64_t)sm.h[16 * t + i] * width + r) = s * acc[t][j];
+      }
+  }
+}
+
+constexpr int64_t kTileMinRows = 1024;
+constexpr int kOrderThreads = 1024;
+
+__global__ __launch_bounds__(kOrderThreads) void adapter_order_kernel(const ShrinkParams p) { order_rows<kOrderThreads>(p); }
+
+constexpr int64_t kShrinkGroups = 512;          // workgroups with work: two a CU
+constexpr int kShrinkMaxPlanes = 4;
+
+int waves_wide(int32_t width) { return width > 2 * kShrinkWidth ? 4 : width > kShrinkWidth ? 2 : 1; }
+
+int64_t tiles_of(int64_t positions) { return (positions + kShrinkRows - 1) / kShrinkRows; }
+
+int parts_of(int32_t width) { return (width + kShrinkWidth * waves_wide(width) - 1) / (kShrinkWidth * waves_wide(width)); }
 
 }  // namespace
 
-// K is cut where the 64-row tiles alone leave waves idle, not below four chunks a slice
-int shrink_slices(int64_t positions, int32_t width, int32_t KC) {
-  const int64_t items = (positions + kShrinkRows - 1) / kShrinkRows * ((width + kShrinkWidth - 1) / kShrinkWidth);
-  const int64_t want = (kShrinkItems + std::max<int64_t>(items, 1) - 1) / std::max<int64_t>(items, 1);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, kShrinkMaxSlices, KC / 4}));
+// Planes of h: K is cut where the 64-row tiles alone leave CUs idle, not below two chunks a wave
+int shrink_slices(int64_t expected, int32_t width, int32_t KC) {
+  const int64_t items = std::max<int64_t>(tiles_of(expected) * parts_of(width), 1);
+  const int deep = kShrinkWaves / waves_wide(width);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(kShrinkGroups + items - 1) / items, kShrinkMaxPlanes, KC / (2 * deep)}));
 }
 
 hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* out) {
   ShrinkGrid grid;
   if (p.ad.L > kMaxAdapters) return hipErrorInvalidValue;
   if (p.order != nullptr && (p.sorted_ids != nullptr || p.positions > kOrderMaxRows)) return hipErrorInvalidValue;
-  const int64_t tiles = (p.positions + kShrinkRows - 1) / kShrinkRows;
-  grid.parts = (p.ad.slices * p.ad.rank + kShrinkWidth - 1) / kShrinkWidth;
-  const int64_t per = tiles * p.ad.ks * grid.parts;
-  grid.z = (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * kShrinkItems / per, kShrinkRows, p.positions}));
-  grid.items = per * grid.z;
-  const int64_t blocks = (grid.items + kShrinkWaves - 1) / kShrinkWaves + (p.order != nullptr);
+  const int32_t width = p.ad.slices * p.ad.rank;
+  grid.kw = waves_wide(width);
+  grid.parts = parts_of(width);
+  // workgroups that deal a tile's adapters: no more than a tile can hold (a block of the routing holds one expert's
+  // tokens, each once)
+  const int64_t block = p.sorted_ids != nullptr ? std::min<int64_t>((int64_t)1 << p.block_shift, kShrinkRows) : kShrinkRows;
+  const int64_t tokens = p.sorted_ids != nullptr ? p.sentinel / p.ad.topk : p.positions;
+  const int64_t hold = kShrinkRows / block * std::min<int64_t>({block, tokens, p.ad.L});
+  const int64_t busy = std::max<int64_t>(tiles_of(p.expected) * p.ad.ks * grid.parts, 1);
+  const int64_t likely = (p.expected_rows * kShrinkRows + p.expected - 1) / std::max<int64_t>(p.expected, 1);   // rows of a tile
+  grid.z = (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * kShrinkGroups / busy, hold, likely}));
+  const int64_t items = tiles_of(p.positions) * p.ad.ks * grid.parts * grid.z;
+  const int64_t blocks = items + (p.order != nullptr);
   if (blocks > INT32_MAX / kShrinkThreads) return hipErrorInvalidConfiguration;
+  grid.items = (int32_t)items;
   grid.blocks = (int32_t)blocks;
   *out = grid;
   return hipSuccess;
 }
 
+bool shrink_tiles_apply(const ShrinkParams& p) { return p.expected_rows >= kTileMinRows && p.K % kChunk == 0; }
+
 hipError_t launch_adapter_shrink(const ShrinkParams& p, hipStream_t stream) {
   if (p.positions <= 0 || p.ad.L <= 0) return hipSuccess;
   ShrinkGrid grid;
-  const hipError_t e = shrink_grid(p, &grid);
+  hipError_t e = shrink_grid(p, &grid);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(adapter_shrink_kernel, dim3((unsigned)grid.blocks), dim3(kShrinkThreads), 0, stream, p, grid);
+  if (!shrink_tiles_apply(p)) {
+    hipLaunchKernelGGL(adapter_shrink_kernel, dim3((unsigned)grid.blocks), dim3(kShrinkThreads), 0, stream, p, grid);
+    return hipGetLastError();
+  }
+  ShrinkParams q = p;
+  if (p.order != nullptr) {
+    hipLaunchKernelGGL(adapter_order_kernel, dim3(1), dim3(kOrderThreads), 0, stream, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    q.in_order = 1;
+  }
+  const int parts = (p.ad.slices * p.ad.rank + kShrinkWaves * kShrinkWidth - 1) / (kShrinkWaves * kShrinkWidth);
+  const int64_t blocks = (p.positions + kTileRows - 1) / kTileRows * p.ad.ks * parts;
+  if (blocks > INT32_MAX / kShrinkThreads) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(adapter_shrink_tile_kernel, dim3((unsigned)blocks), dim3(kShrinkThreads), 0, stream, q, parts);
   return hipGetLastError();
 }
 

@@ -3,15 +3,15 @@
 // are routed (A [L][E][S r][K], S r rows of K).
 //
 // Few rows are bound by reading A (S r K bf16 of each adapter in use), many by
-// reading x.  A wave takes 64 consecutive rows, one slice of K and up to 32
-// rows of A; it gathers the rows that share an (adapter, expert) by ballot,
-// 16 of them make one v_mfma_f32_16x16x32_bf16 operand against 16 rows of A,
-// and each such group is one pass over the slice.  So an A is read once for
-// every 64 rows that use it however the requests are mixed, nothing is
-// sorted first, and no wave waits for another: sums of one row from different
-// slices of K go to different planes of h, which the product's start adds in
-// slice order.
-//
+// reading x.  A workgroup takes 64 consecutive rows, a slice of K and up to 128
+// rows of A: its four waves take 32 rows of A each, or parts of the slice where
+// A has fewer, whose sums meet in LDS in wave order.  A wave gathers the rows
+// that share an (adapter, expert) by ballot, 16 of them make one
+// v_mfma_f32_16x16x32_bf16 operand against 16 rows of A, and each such group is
+// one pass over the slice.  So an A is read once for every 64 rows that use it
+// however the requests are mixed, nothing is sorted first, and no workgroup
+// waits for another: sums of one row from different slices of K go to different
+// planes of h, which the product's start adds in slice order.
 #pragma once
 #include <type_traits>
 
@@ -45,7 +45,7 @@ __device__ __forceinline__ void clear_past(int c, int K, u32x4_t (&v)[4]) {
     if (c * kChunk + 32 * j >= K) v[j] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
-// the chunks [c0, c1) of 16 M rows of x against 16 W rows of A, D chunks in flight
+// the chunks [c0, c1) (none: zeros) of 16 M rows of x against 16 W rows of A, D chunks in flight
 template <int M, int W, int D>
 __device__ __forceinline__ void shrink_pass(const ShrinkParams& p, gptr_t abase, const uint32_t (&arow)[2], gptr_t xbase,
                                             const uint32_t (&xrow)[M], int c0, int c1, f32x4_t (&acc)[M][W]) {
@@ -80,6 +80,7 @@ __device__ __forceinline__ void shrink_pass(const ShrinkParams& p, gptr_t abase,
           acc[m][w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[st][w][j]),
                                                               __builtin_bit_cast(bf16x8_t, x[st][m][j]), acc[m][w], 0, 0, 0);
   };
+  if (c0 >= c1) return;
   ring_steps<D>([&](auto st_) { request(st_, min(c0 + decltype(st_)::value, c1 - 1)); });
   ring_run<D>(c0, c1, use, request);
 }
@@ -87,16 +88,17 @@ __device__ __forceinline__ void shrink_pass(const ShrinkParams& p, gptr_t abase,
 // The rows in order of their adapters, rows without one last: what makes a
 // product's 16-row tiles hold few adapters each.  Rows of one adapter come in
 // any order (a row's result does not depend on where it stands).
+template <int THREADS>
 __device__ __forceinline__ void order_rows(const ShrinkParams& p) {
   __shared__ int start[kMaxAdapters + 1];
   const int L = p.ad.L, T = (int)p.positions;
-  for (int b = threadIdx.x; b <= L; b += kShrinkThreads) start[b] = 0;
+  for (int b = threadIdx.x; b <= L; b += THREADS) start[b] = 0;
   __syncthreads();
   auto bucket = [&](int t) {
     const int a = p.ad.ids[t];
     return (unsigned)a < (unsigned)L ? a : L;
   };
-  for (int t = threadIdx.x; t < T; t += kShrinkThreads) atomicAdd(&start[bucket(t)], 1);
+  for (int t = threadIdx.x; t < T; t += THREADS) atomicAdd(&start[bucket(t)], 1);
   __syncthreads();
   if (threadIdx.x < kWave) {                            // exclusive sums, a run of buckets a lane
     const int per = (L + kWave) / kWave;
@@ -116,7 +118,35 @@ __device__ __forceinline__ void order_rows(const ShrinkParams& p) {
     }
   }
   __syncthreads();
-  for (int t = threadIdx.x; t < T; t += kShrinkThreads) p.order[atomicAdd(&start[bucket(t)], 1)] = t;
+  for (int t = threadIdx.x; t < T; t += THREADS) p.order[atomicAdd(&start[bucket(t)], 1)] = t;
+}
+
+// a position's (adapter, expert), -1: none; its row of x and of h
+struct ShrinkRow {
+  int key, x, h;
+};
+
+__device__ __forceinline__ ShrinkRow shrink_row(const ShrinkParams& p, int64_t pos) {
+  const AdapterParams& q = p.ad;
+  ShrinkRow r{-1, 0, 0};
+  if (p.sorted_ids != nullptr) {
+    if (pos < min(p.positions, (int64_t)*p.num_tokens_padded)) {
+      const int s = p.sorted_ids[pos];
+      const int e = p.expert_ids[pos >> p.block_shift];
+      if ((unsigned)s < (unsigned)p.sentinel && (unsigned)e < (unsigned)q.E) {
+        const int a = q.ids[s / q.topk];
+        if ((unsigned)a < (unsigned)q.L) r.key = a * q.E + e;
+        r.x = p.a_row_div > 0 ? s / p.a_row_div : (int)pos;
+        r.h = s;
+      }
+    }
+  } else if (pos < p.positions) {
+    const int row = p.in_order ? q.order[pos] : (int)pos;
+    const int a = q.ids[row];
+    if ((unsigned)a < (unsigned)q.L) r.key = a;
+    r.x = r.h = row;
+  }
+  return r;
 }
 
 // The work of workgroup `block` of the grid (kShrinkThreads threads).  M16: 16-row
@@ -126,48 +156,33 @@ template <int M16>
 __device__ __forceinline__ void shrink_block(const ShrinkParams& p, const ShrinkGrid& grid, int block) {
   if (p.order != nullptr) {
     if (block == 0) {
-      order_rows(p);
+      order_rows<kShrinkThreads>(p);
       return;
     }
     --block;
   }
+  __shared__ f32x4_t red[kShrinkWaves][2 * M16][kWave];
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t item = (int64_t)block * kShrinkWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  if (item >= grid.items) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (block >= grid.items) return;
   const AdapterParams& q = p.ad;
-  const int part = (int)(item % grid.parts);
-  int64_t left = item / grid.parts;
-  const int z = (int)(left % grid.z);
+  // the workgroup's 32 kw rows of A, kw waves side by side and kShrinkWaves / kw one after another along K
+  int left = block / grid.parts;
+  const int part = (block - left * grid.parts) * grid.kw + wave % grid.kw;
+  const int z = left % grid.z;
   left /= grid.z;
-  const int ks = (int)(left % q.ks);
-  const int64_t pos = (left / q.ks) * kShrinkRows + lane;
+  const int ks = left % q.ks;
+  const int64_t pos = (int64_t)(left / q.ks) * kShrinkRows + lane;
 
-  // this lane's row: its (adapter, expert), row of x and row of h
-  int key = -1, x_row = 0, h_row = 0;
-  if (p.sorted_ids != nullptr) {
-    const int64_t end = min(p.positions, (int64_t)*p.num_tokens_padded);
-    if (pos < end) {
-      const int s = p.sorted_ids[pos];
-      const int e = p.expert_ids[pos >> p.block_shift];
-      if ((unsigned)s < (unsigned)p.sentinel && (unsigned)e < (unsigned)q.E) {
-        const int a = q.ids[s / q.topk];
-        if ((unsigned)a < (unsigned)q.L) key = a * q.E + e;
-        x_row = p.a_row_div > 0 ? s / p.a_row_div : (int)pos;
-        h_row = s;
-      }
-    }
-  } else if (pos < p.positions) {
-    const int a = q.ids[pos];
-    if ((unsigned)a < (unsigned)q.L) key = a;
-    x_row = (int)pos;
-    h_row = (int)pos;
-  }
+  const ShrinkRow own_row = shrink_row(p, pos);
+  const int key = own_row.key, x_row = own_row.x, h_row = own_row.h;
 
   const int width = q.slices * q.rank;
   const int i = lane & 15, g = lane >> 4;
-  const int c0 = (int)((int64_t)ks * p.KC / q.ks), c1 = (int)((int64_t)(ks + 1) * p.KC / q.ks);
+  const int deep = kShrinkWaves / grid.kw, cut = ks * deep + wave / grid.kw;
+  const int c0 = (int)((int64_t)cut * p.KC / (q.ks * deep)), c1 = (int)((int64_t)(cut + 1) * p.KC / (q.ks * deep));
   const int j0 = part * kShrinkWidth;
-  const bool both = j0 + 16 < width;
+  const bool both = width > 16;                         // the same for the whole workgroup, whose waves meet below
   float* const plane = q.h + (int64_t)ks * q.rows * width;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (kWave - lane);
   uint64_t rest = __ballot(key >= 0);
@@ -200,6 +215,20 @@ __device__ __forceinline__ void shrink_block(const ShrinkParams& p, const Shrink
       }
       f32x4_t acc[M][W];
       shrink_pass<M, W, decltype(chunks)::value>(p, abase, arow, xbase, xrow, c0, c1, acc);
+      if (deep > 1) {
+        __syncthreads();                                // the sums before have been read
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int j = 0; j < W; ++j) red[wave][m * W + j][lane] = acc[m][j];
+        __syncthreads();
+        if (wave >= grid.kw) return;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            for (int d = 1; d < deep; ++d) acc[m][j] += red[wave + d * grid.kw][m * W + j][lane];
+      }
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll

@@ -1561,8 +1561,8 @@ w4a16_status check_adapters(const w4a16_adapters* ad, const w4a16_weight_desc* d
   return W4A16_OK;
 }
 
-// `rows` rows of h, of `positions` positions to look through
-w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, int32_t topk, int64_t rows, int64_t positions) {
+// `rows` rows of h, `expected` of them written under uniform routing
+w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, int32_t topk, int64_t rows, int64_t expected) {
   w4a16::AdapterParams q;
   std::memset(&q, 0, sizeof q);
   q.a = ad.a;
@@ -1576,7 +1576,7 @@ w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, int32_t topk, int6
   q.N = ad.N;
   q.topk = topk;
   q.rows = rows;
-  q.ks = w4a16::shrink_slices(positions, ad.slices * ad.rank, (ad.K + 127) / 128);
+  q.ks = w4a16::shrink_slices(expected, ad.slices * ad.rank, (ad.K + 127) / 128);
   return q;
 }
 
@@ -1611,6 +1611,18 @@ int64_t position_bound(const w4a16_indexed_routing& r) {
   return indexed_block_bound(r, r.block_m) * r.block_m;
 }
 
+// local slots under uniform routing
+double expected_slots(const w4a16_indexed_routing& r) {
+  return (double)r.T * r.topk * (r.E_glob > 0 ? std::min(1.0, (double)r.E_loc / r.E_glob) : 1.0);
+}
+
+// ... and the positions of their blocks
+int64_t expected_positions(const w4a16_indexed_routing& r) {
+  const double slots = expected_slots(r);
+  const double pad = std::min<double>(r.E_loc, slots) * (r.block_m / 2);
+  return std::min<int64_t>(position_bound(r), (int64_t)(slots + pad));
+}
+
 // The config of an indexed call with adapters: whole tiles, not split along K.
 w4a16_status adapter_call_config(const w4a16_indexed_routing& r, const w4a16_weight_desc* d, int epi,
                                  const w4a16_config* cfg, w4a16_config* c) {
@@ -1642,6 +1654,8 @@ hipError_t shrink_routed(const w4a16::AdapterParams& q, const uint16_t* a, int32
   sp.sentinel = r.T * r.topk;
   sp.a_row_div = a_layout == W4A16_A_TOKEN ? r.topk : a_layout == W4A16_A_SLOT ? 1 : 0;
   sp.positions = position_bound(r);
+  sp.expected = expected_positions(r);
+  sp.expected_rows = (int64_t)std::ceil(expected_slots(r));
   return w4a16::launch_adapter_shrink(sp, stream);
 }
 
@@ -1704,6 +1718,7 @@ w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, c
   sp.K = desc->K;
   sp.KC = desc->chunks;
   sp.positions = T;
+  sp.expected = sp.expected_rows = T;
   // in one block of 16 rows no order changes anything
   if (adapters && T > 16 && T <= w4a16::kOrderMaxRows) sp.order = reinterpret_cast<int32_t*>(ws + wl.h);
   sp.ad.order = sp.order;
@@ -1723,7 +1738,7 @@ size_t w4a16_moe_adapter_workspace_bytes(const w4a16_weight_desc* desc, const w4
   w4a16_config c{};
   // the config steers only the combine's columns, which do not depend on the epilogue's tile
   if (adapter_call_config(r, desc, combine ? w4a16::kEpiWeighted : w4a16::kEpiStore, cfg, &c) != W4A16_OK) return 0;
-  const w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, position_bound(r));
+  const w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, expected_positions(r));
   return adapter_workspace(c, desc, r, q, combine != 0).total();
 }
 
@@ -1755,7 +1770,7 @@ w4a16_status w4a16_moe_adapter_gemm(const w4a16_weight_desc* desc, const void* p
   if (st != W4A16_OK) return st;
   if (combine && !r.topk_ids) return fail(W4A16_ERR_ARG, "combine needs routing.topk_ids");
   if (r.T == 0) return W4A16_OK;
-  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, position_bound(r));
+  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, expected_positions(r));
   const AdapterWorkspace wl = adapter_workspace(c, desc, r, q, combine);
   st = check_workspace(wl.total(), workspace, workspace_bytes);
   if (st != W4A16_OK) return st;
@@ -1812,7 +1827,7 @@ w4a16_status w4a16_moe_adapter_gate_up_silu(const w4a16_weight_desc* desc, const
   st = adapter_call_config(r, desc, w4a16::kEpiSilu, cfg, &c);
   if (st != W4A16_OK) return st;
   if (r.T == 0) return W4A16_OK;
-  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, position_bound(r));
+  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, expected_positions(r));
   st = check_workspace(h_bytes(q), workspace, workspace_bytes);
   if (st != W4A16_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
