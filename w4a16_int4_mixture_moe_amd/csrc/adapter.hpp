@@ -87,47 +87,83 @@ __device__ __forceinline__ bf16x8_t zero_operand() { return __builtin_bit_cast(b
 // Ranks r0 .. of every row of the block that has an adapter: the sum over the
 // slices of K, split in two bf16 parts; zeros past the rank.  place(slice,
 // row, granule) is the granule's address.  The caller synchronises.
-// KP: slices in flight together.
-template <int BM, int NTHR, int KP, typename Smem, typename Place>
+// IP groups of 8 ranks a thread and KP slices of each in flight together.
+template <int BM, int NTHR, int IP, int KP, typename Smem, typename Place>
 __device__ __forceinline__ void stage_h(const AdapterParams& q, const Smem& sm, int r0, Place&& place) {
   const int width = q.slices * q.rank;
+  const int64_t plane = q.rows * width;
   const int left = min(q.rank - r0, kHRanks);
   const int eights = (left + 15) / 16 * 2;                // groups of 8 ranks, whole instructions
   const int items = BM * q.slices * eights;
-  for (int it = threadIdx.x; it < items; it += NTHR) {
-    const int e = it % eights, rest = it / eights;
-    const int row = rest % BM, slice = rest / BM;
-    if (sm.ad[row] < 0) continue;
-    f32x4_t v[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
-    if (8 * e < left) {
-      const float* src = q.h + (int64_t)sm.slot[row] * width + slice * q.rank + r0 + 8 * e;
-      const int64_t plane = q.rows * width;
-      for (int k0 = 0; k0 < q.ks; k0 += KP) {             // past the last one: the last again, not added
-        f32x4_t w[KP][2];
+  for (int it0 = threadIdx.x; it0 < items; it0 += IP * NTHR) {
+    int row[IP], slice[IP], e[IP];
+    const float* src[IP];
+    f32x4_t v[IP][2];
 #pragma unroll
-        for (int k = 0; k < KP; ++k) {
-          const float* from = src + min(k0 + k, q.ks - 1) * plane;
-          w[k][0] = *reinterpret_cast<const f32x4_t*>(from);
-          w[k][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
+    for (int n = 0; n < IP; ++n) {
+      const int it = min(it0 + n * NTHR, items - 1);      // past the last: the last again
+      const int rest = it / eights;
+      e[n] = it - rest * eights;
+      slice[n] = rest / BM;
+      row[n] = rest - slice[n] * BM;
+      // rows without an adapter: any address of h, for values that are never used
+      const bool in = sm.ad[row[n]] >= 0 && 8 * e[n] < left;
+      src[n] = q.h + (in ? (int64_t)sm.slot[row[n]] * width + slice[n] * q.rank + r0 + 8 * e[n] : 0);
+      v[n][0] = v[n][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int k0 = 0; k0 < q.ks; k0 += KP) {               // past the last slice: the last again, not added
+      f32x4_t w[KP][IP][2];
+#pragma unroll
+      for (int k = 0; k < KP; ++k)
+#pragma unroll
+        for (int n = 0; n < IP; ++n) {
+          const float* from = src[n] + min(k0 + k, q.ks - 1) * plane;
+          w[k][n][0] = *reinterpret_cast<const f32x4_t*>(from);
+          w[k][n][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
         }
 #pragma unroll
-        for (int k = 0; k < KP; ++k)
-          if (k0 + k < q.ks) {
-            v[0] += w[k][0];
-            v[1] += w[k][1];
-          }
-      }
-    }
-    bf16x8_t hi, lo;
+      for (int k = 0; k < KP; ++k)
+        if (k0 + k < q.ks)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float x = v[c / 4][c % 4];
-      hi[c] = (__bf16)x;
-      const float part = x - (float)hi[c];                // NaN where hi is infinite: hi stands alone there
-      lo[c] = (__bf16)(part == part ? part : 0.f);
+          for (int n = 0; n < IP; ++n) {
+            v[n][0] += w[k][n][0];
+            v[n][1] += w[k][n][1];
+          }
     }
-    *place(slice, row, e / 2 * 4 + (e & 1)) = hi;
-    *place(slice, row, e / 2 * 4 + (e & 1) + 2) = lo;
+#pragma unroll
+    for (int n = 0; n < IP; ++n) {
+      if (sm.ad[row[n]] < 0) continue;
+      if (8 * e[n] >= left) v[n][0] = v[n][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      bf16x8_t hi, lo;
+      split_bf16(v[n], hi, lo);
+      *place(slice[n], row[n], e[n] / 2 * 4 + (e[n] & 1)) = hi;
+      *place(slice[n], row[n], e[n] / 2 * 4 + (e[n] & 1) + 2) = lo;
+    }
+  }
+}
+
+// The same from a packed h, IP granules a thread in flight.
+template <int BM, int NTHR, int IP, typename Smem, typename Place>
+__device__ __forceinline__ void stage_packed_h(const AdapterParams& q, const Smem& sm, int r0, Place&& place) {
+  const int all = (q.rank + 15) / 16 * 4, from = r0 / 16 * 4;   // a row's granules, and the first of these ranks
+  const int count = min(all - from, kHRanks / 4);
+  const int items = BM * q.slices * count;
+  for (int it0 = threadIdx.x; it0 < items; it0 += IP * NTHR) {
+    u32x4_t v[IP];
+    int row[IP], slice[IP], at[IP];
+#pragma unroll
+    for (int n = 0; n < IP; ++n) {
+      const int it = min(it0 + n * NTHR, items - 1);      // past the last: the last again
+      const int rest = it / count;
+      at[n] = it - rest * count;
+      slice[n] = rest / BM;
+      row[n] = rest - slice[n] * BM;
+      const int64_t src = sm.ad[row[n]] >= 0 ? ((int64_t)sm.slot[row[n]] * q.slices + slice[n]) * all + from + at[n] : 0;
+      v[n] = *reinterpret_cast<const u32x4_t*>(q.packed + src * 8);
+    }
+#pragma unroll
+    for (int n = 0; n < IP; ++n)
+      if (sm.ad[row[n]] >= 0) *place(slice[n], row[n], at[n]) = __builtin_bit_cast(bf16x8_t, v[n]);
   }
 }
 
@@ -161,12 +197,17 @@ __device__ __forceinline__ bf16x8_t b_operand(const AdapterParams& q, const uint
 template <int MT, int NR, int NW, int NA, typename Smem, typename Place>
 __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const AdapterParams& q, const Smem& sm,
                                                     int expert, int rt_base, f32x4_t (&acc)[NR][MT], Place&& at) {
-  constexpr int U = NR == 4 ? 2 : 4;
+  constexpr int U = MT >= 8 ? 2 : 4;
+  // decode tiles stream weights with as many waves as their registers allow, and a block of theirs holds few adapters:
+  // nothing ahead
+  constexpr int SETS = MT >= 4 ? 2 : 1;
+  auto clear = [&]() {
 #pragma unroll
-  for (int r = 0; r < NR; ++r)
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  if (q.L == 0) return;
+      for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  if (q.L == 0) return clear();
   const int lane = threadIdx.x & (kWave - 1);
   const int i = lane & 15, g = lane >> 4;
   const AdapterTiles<NR> tiles(p, q, rt_base);
@@ -184,47 +225,79 @@ __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const A
     return __builtin_amdgcn_readfirstlane(best);
   };
   const int first = next_after(-1);
-  if (first == INT32_MAX) return;                       // the whole block, so every wave
+  if (first == INT32_MAX) return clear();               // the whole block, so every wave
+  // the first ranks before the accumulators take their registers
+  if (q.packed != nullptr) stage_packed_h<16 * MT, NW * kWave, MT >= 4 ? 16 : 2>(q, sm, 0, at);
+  else stage_h<16 * MT, NW * kWave, MT >= 4 ? 2 : 1, 4>(q, sm, 0, at);
+  clear();
   for (int r0 = 0; r0 < q.rank; r0 += kHRanks) {
-    if (r0 > 0) __syncthreads();
-    stage_h<16 * MT, NW * kWave, MT <= 4 ? 4 : 2>(q, sm, r0, at);
+    if (r0 > 0) {
+      __syncthreads();
+      if (q.packed != nullptr) stage_packed_h<16 * MT, NW * kWave, 4>(q, sm, r0, at);
+      else stage_h<16 * MT, NW * kWave, 1, 2>(q, sm, r0, at);
+    }
     __syncthreads();
     const int steps = (min(q.rank - r0, kHRanks) + 15) / 16;
-    // (adapter, instruction) after (adapter, instruction), U of them in flight
-    for (int a = first, j = 0; a != INT32_MAX;) {
-      int ua[U], uj[U];
-      bf16x8_t b[U][NR];
+    // (adapter, instruction) after (adapter, instruction): U of them, with two sets the next U on their way
+    int a = first, j = 0;
+    int ua[SETS][U], uj[SETS][U];
+    bf16x8_t b[SETS][U][NR];
+    auto request = [&](auto set_) {
+      constexpr int set = decltype(set_)::value;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        ua[u] = a;
-        uj[u] = j;
+        ua[set][u] = a;
+        uj[set][u] = j;
         if (a == INT32_MAX) continue;
         const uint16_t* base = q.b + (int64_t)a * per_adapter + of_expert;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) b[u][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
+        for (int r = 0; r < NR; ++r) b[set][u][r] = b_operand(q, base, tiles.row[r], r0 + 16 * j + 8 * (g & 1));
         if (++j == steps) {
           j = 0;
           a = next_after(a);
         }
       }
+    };
+    auto use = [&](auto set_) {
+      constexpr int set = decltype(set_)::value;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (ua[u] == INT32_MAX) continue;
+        if (ua[set][u] == INT32_MAX) continue;
 #pragma unroll
         for (int t = 0; t < NA; ++t) {
-          const bool own = mine[t] == ua[u];
+          const bool own = mine[t] == ua[set][u];
           if (!__ballot(own)) continue;
-          const bf16x8_t h0 = *at(0, 16 * t + i, 4 * uj[u] + g);
-          const bf16x8_t h1 = q.slices == 2 ? *at(1, 16 * t + i, 4 * uj[u] + g) : h0;
+          const bf16x8_t h0 = *at(0, 16 * t + i, 4 * uj[set][u] + g);
+          const bf16x8_t h1 = q.slices == 2 ? *at(1, 16 * t + i, 4 * uj[set][u] + g) : h0;
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[u][r], tiles.slice[r] ? h1 : h0,
+            const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[set][u][r], tiles.slice[r] ? h1 : h0,
                                                                       f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[r][t][v] += own ? y[v] : 0.f;
           }
         }
       }
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, SETS - 1>;
+    if constexpr (SETS == 1) {
+      while (a != INT32_MAX) {
+        request(I0{});
+        use(I0{});
+      }
+      continue;
+    }
+    request(I0{});
+    while (true) {
+      const bool more = a != INT32_MAX;
+      if (more) request(I1{});
+      use(I0{});
+      if (!more) break;
+      const bool again = a != INT32_MAX;
+      if (again) request(I0{});
+      use(I1{});
+      if (!again) break;
     }
   }
   __syncthreads();
@@ -386,7 +459,7 @@ __device__ __forceinline__ void deal_adapters(const GemmParams& p, const Adapter
     };
     request();
     if (r0 > 0) lds_only_barrier();
-    stage_h<16 * MT, NW * kWave, 4>(q, sm, r0, [&](int slice, int row, int granule) {
+    stage_h<16 * MT, NW * kWave, 2, 4>(q, sm, r0, [&](int slice, int row, int granule) {
       return reinterpret_cast<bf16x8_t*>(&sm.h[slice][row][8 * granule]);
     });
     lds_only_barrier();

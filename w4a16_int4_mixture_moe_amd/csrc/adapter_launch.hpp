@@ -17,6 +17,8 @@ struct AdapterParams {
   int64_t rows;                 // rows of h: T * topk slots, or T
   float* h;                     // [ks][rows][slices * rank], of rows with an adapter
   int32_t ks;                   // slices of K that left their sums in h
+  uint16_t* packed;             // NULL, or [rows][slices][rank / 16, rounded up][32]: h's two bf16 parts, in granules of 8
+                                // ranks: hi, hi, lo, lo of 16 ranks
   const int32_t* order;         // kRouteDense: the rows in order of their adapters, or NULL
 };
 
@@ -43,7 +45,7 @@ struct ShrinkGrid {
   int32_t parts, kw;            // parts of A's rows, 32 kw rows each
   int32_t items, blocks;        // workgroups of the rows, and of the launch
 };
-int shrink_slices(int64_t expected, int32_t width, int32_t KC);
+int shrink_slices(bool routed, int64_t expected, int32_t width, int32_t K, bool packed);
 hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* grid);
 hipError_t launch_adapter_shrink(const ShrinkParams& p, hipStream_t stream);
 
@@ -54,6 +56,7 @@ hipError_t launch_adapter_gemm(int epilogue, int m_tiles, int nr, int waves, int
 // One weight for all rows, with or without adapters (linear.hip); epilogue
 // kEpiStore or kEpiSilu.  sp: what launch_adapter_shrink takes, with p's rows
 // and sp.ad.L == 0 without adapters; parts: linear_parts_bytes(T, N, KC) bytes.
+bool linear_whole_tiles(int64_t T, int32_t N, int32_t KC);   // not cut along K
 size_t linear_parts_bytes(int64_t T, int32_t N, int32_t KC);
 hipError_t launch_linear(int epilogue, const GemmParams& p, const ShrinkParams& sp, float* parts, hipStream_t stream);
 

@@ -14,11 +14,16 @@ __global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_kernel(const
   shrink_block<2>(p, grid, blockIdx.x);
 }
 
+constexpr int kShrinkMaxPlanes = 4;             // twice as many where they are packed
+constexpr int64_t kTileMinRows = 2048;
+constexpr int64_t kTileMinInner = 1 << 17;
+constexpr int kOrderThreads = 1024;
+
 // Many rows: 128 positions and 128 rows of A a workgroup, the rows of x staged
 // by LDS-DMA for its four waves, which take 32 rows of A each.  What bounds the
 // first kernel there is what a CU can load (about 25 bytes a ns from L2): every
 // wave of it loads x for itself.  Measured on MI355X, 8192 rows of 24 requests x
-// 7168, rank 64 twice: SHRINK_FIRST us that way, SHRINK_TILE us this way.
+// 7168, rank 64 twice: 209 us that way, 79 us this way.
 //
 // A chunk of a row is 16 granules of 16 bytes, granule q at position
 // q ^ (row % 16) of the row's 256 bytes, so that the 16 rows that a lane group
@@ -143,13 +148,49 @@ __global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_tile_kernel(
   }
 }
 
-constexpr int64_t kTileMinRows = 1024;
-constexpr int kOrderThreads = 1024;
+
+// The planes' sum of each row that has an adapter, as the two bf16 parts that the products take
+// (AdapterParams::packed): where many workgroups read a row's h they would each add the planes.
+__global__ __launch_bounds__(kShrinkThreads) void adapter_pack_kernel(const ShrinkParams p, int64_t threads) {
+  const int64_t at = (int64_t)blockIdx.x * kShrinkThreads + threadIdx.x;
+  if (at >= threads) return;
+  const AdapterParams& q = p.ad;
+  const int eights = (q.rank + 15) / 16 * 2;
+  const int e = (int)(at % eights);
+  const int64_t rs = at / eights;                       // (row, slice)
+  const int64_t row = rs / q.slices;
+  const int slice = (int)(rs - row * q.slices);
+  const int a = q.ids[row / q.topk];
+  if ((unsigned)a >= (unsigned)q.L) return;
+  // a routed row that no expert held here has is packed as well, from whatever its place holds: nothing reads it
+  const int width = q.slices * q.rank;
+  f32x4_t v[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+  if (8 * e < q.rank) {
+    const float* src = q.h + row * width + slice * q.rank + 8 * e;
+    f32x4_t w[kShrinkMaxPlanes * 2][2];
+#pragma unroll
+    for (int k = 0; k < kShrinkMaxPlanes * 2; ++k) {    // past the last plane: the last again, not added
+      const float* from = src + min(k, q.ks - 1) * q.rows * width;
+      w[k][0] = *reinterpret_cast<const f32x4_t*>(from);
+      w[k][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
+    }
+#pragma unroll
+    for (int k = 0; k < kShrinkMaxPlanes * 2; ++k)
+      if (k < q.ks) {
+        v[0] += w[k][0];
+        v[1] += w[k][1];
+      }
+  }
+  bf16x8_t hi, lo;
+  split_bf16(v, hi, lo);
+  bf16x8_t* to = reinterpret_cast<bf16x8_t*>(q.packed) + rs * (2 * eights) + e / 2 * 4 + (e & 1);
+  to[0] = hi;
+  to[2] = lo;
+}
 
 __global__ __launch_bounds__(kOrderThreads) void adapter_order_kernel(const ShrinkParams p) { order_rows<kOrderThreads>(p); }
 
 constexpr int64_t kShrinkGroups = 512;          // workgroups with work: two a CU
-constexpr int kShrinkMaxPlanes = 4;
 
 int waves_wide(int32_t width) { return width > 2 * kShrinkWidth ? 4 : width > kShrinkWidth ? 2 : 1; }
 
@@ -157,13 +198,25 @@ int64_t tiles_of(int64_t positions) { return (positions + kShrinkRows - 1) / kSh
 
 int parts_of(int32_t width) { return (width + kShrinkWidth * waves_wide(width) - 1) / (kShrinkWidth * waves_wide(width)); }
 
+// The staged tile where x outweighs A by far: rows of requests side by side (one weight), from 2048 rows and
+// 2^17 inner values on
+bool tiles_apply(bool routed, int64_t rows, int32_t width, int32_t K) {
+  return !routed && K % kChunk == 0 && rows >= kTileMinRows &&
+         rows * std::min(width, kShrinkWaves * kShrinkWidth) >= kTileMinInner;
+}
+
 }  // namespace
 
-// Planes of h: K is cut where the 64-row tiles alone leave CUs idle, not below two chunks a wave
-int shrink_slices(int64_t expected, int32_t width, int32_t KC) {
-  const int64_t items = std::max<int64_t>(tiles_of(expected) * parts_of(width), 1);
-  const int deep = kShrinkWaves / waves_wide(width);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(kShrinkGroups + items - 1) / items, kShrinkMaxPlanes, KC / (2 * deep)}));
+// Planes of h: K is cut where the tiles alone leave CUs idle, not below two chunks a wave; every reader of h adds the
+// planes, unless they are packed first
+int shrink_slices(bool routed, int64_t expected, int32_t width, int32_t K, bool packed) {
+  const bool staged = tiles_apply(routed, expected, width, K);
+  const int64_t tiles = (expected + (staged ? kTileRows : kShrinkRows) - 1) / (staged ? kTileRows : kShrinkRows);
+  const int64_t items = std::max<int64_t>(tiles * parts_of(width), 1);
+  const int deep = staged ? 1 : kShrinkWaves / waves_wide(width);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(kShrinkGroups + items - 1) / items,
+                                                      packed ? kShrinkMaxPlanes * 2 : kShrinkMaxPlanes,
+                                                      (K + kChunk - 1) / kChunk / (2 * deep)}));
 }
 
 hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* out) {
@@ -190,28 +243,36 @@ hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* out) {
   return hipSuccess;
 }
 
-bool shrink_tiles_apply(const ShrinkParams& p) { return p.expected_rows >= kTileMinRows && p.K % kChunk == 0; }
-
 hipError_t launch_adapter_shrink(const ShrinkParams& p, hipStream_t stream) {
   if (p.positions <= 0 || p.ad.L <= 0) return hipSuccess;
-  ShrinkGrid grid;
-  hipError_t e = shrink_grid(p, &grid);
-  if (e != hipSuccess) return e;
-  if (!shrink_tiles_apply(p)) {
-    hipLaunchKernelGGL(adapter_shrink_kernel, dim3((unsigned)grid.blocks), dim3(kShrinkThreads), 0, stream, p, grid);
-    return hipGetLastError();
-  }
   ShrinkParams q = p;
-  if (p.order != nullptr) {
+  if (p.order != nullptr) {                             // first, so that 64 or 128 rows hold few adapters
+    if (p.sorted_ids != nullptr || p.positions > kOrderMaxRows || p.ad.L > kMaxAdapters) return hipErrorInvalidValue;
     hipLaunchKernelGGL(adapter_order_kernel, dim3(1), dim3(kOrderThreads), 0, stream, p);
-    e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    q.order = nullptr;
     q.in_order = 1;
   }
-  const int parts = (p.ad.slices * p.ad.rank + kShrinkWaves * kShrinkWidth - 1) / (kShrinkWaves * kShrinkWidth);
-  const int64_t blocks = (p.positions + kTileRows - 1) / kTileRows * p.ad.ks * parts;
+  const int32_t width = p.ad.slices * p.ad.rank;
+  if (tiles_apply(p.sorted_ids != nullptr, p.positions, width, p.K)) {
+    const int parts = parts_of(width);
+    const int64_t blocks = (p.positions + kTileRows - 1) / kTileRows * p.ad.ks * parts;
+    if (blocks > INT32_MAX / kShrinkThreads) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(adapter_shrink_tile_kernel, dim3((unsigned)blocks), dim3(kShrinkThreads), 0, stream, q, parts);
+  } else {
+    ShrinkGrid grid;
+    const hipError_t e = shrink_grid(q, &grid);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(adapter_shrink_kernel, dim3((unsigned)grid.blocks), dim3(kShrinkThreads), 0, stream, q, grid);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ad.packed == nullptr) return e;
+  // rows of a packed h: a thread for 8 ranks
+  const int64_t threads = p.ad.rows * p.ad.slices * ((p.ad.rank + 15) / 16 * 2);
+  const int64_t blocks = (threads + kShrinkThreads - 1) / kShrinkThreads;
   if (blocks > INT32_MAX / kShrinkThreads) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(adapter_shrink_tile_kernel, dim3((unsigned)blocks), dim3(kShrinkThreads), 0, stream, q, parts);
+  hipLaunchKernelGGL(adapter_pack_kernel, dim3((unsigned)blocks), dim3(kShrinkThreads), 0, stream, p, threads);
   return hipGetLastError();
 }
 

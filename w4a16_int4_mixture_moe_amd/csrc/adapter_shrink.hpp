@@ -92,13 +92,30 @@ template <int THREADS>
 __device__ __forceinline__ void order_rows(const ShrinkParams& p) {
   __shared__ int start[kMaxAdapters + 1];
   const int L = p.ad.L, T = (int)p.positions;
+  constexpr int B = 8;                                  // ids in flight per thread
   for (int b = threadIdx.x; b <= L; b += THREADS) start[b] = 0;
   __syncthreads();
-  auto bucket = [&](int t) {
-    const int a = p.ad.ids[t];
-    return (unsigned)a < (unsigned)L ? a : L;
+  auto rows = [&](auto&& each) {
+    for (int t0 = threadIdx.x; t0 < T; t0 += B * THREADS) {
+      int id[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) id[u] = p.ad.ids[min(t0 + u * THREADS, T - 1)];
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+        if (t0 + u * THREADS < T) each(t0 + u * THREADS, (unsigned)id[u] < (unsigned)L ? id[u] : L);
+    }
   };
-  for (int t = threadIdx.x; t < T; t += THREADS) atomicAdd(&start[bucket(t)], 1);
+  // one update for a wave whose rows share a bucket (long requests: nearly every wave; 64 updates of one address take
+  // 64 turns), else one each
+  auto take = [&](int bucket) {
+    const uint64_t on = __ballot(1);
+    const int lead = __builtin_ctzll(on), lane = threadIdx.x & (kWave - 1);
+    if (__ballot(bucket == __builtin_amdgcn_readlane(bucket, lead)) != on) return (int)atomicAdd(&start[bucket], 1);
+    int base = 0;
+    if (lane == lead) base = atomicAdd(&start[bucket], __popcll(on));
+    return (int)__builtin_amdgcn_readlane(base, lead) + (int)__popcll(on & (lane == 0 ? 0ull : ~0ull >> (kWave - lane)));
+  };
+  rows([&](int, int bucket) { take(bucket); });
   __syncthreads();
   if (threadIdx.x < kWave) {                            // exclusive sums, a run of buckets a lane
     const int per = (L + kWave) / kWave;
@@ -118,7 +135,7 @@ __device__ __forceinline__ void order_rows(const ShrinkParams& p) {
     }
   }
   __syncthreads();
-  for (int t = threadIdx.x; t < T; t += THREADS) p.order[atomicAdd(&start[bucket(t)], 1)] = t;
+  rows([&](int t, int bucket) { p.order[take(bucket)] = t; });
 }
 
 // a position's (adapter, expert), -1: none; its row of x and of h

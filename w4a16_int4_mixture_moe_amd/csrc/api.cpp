@@ -1561,8 +1561,10 @@ w4a16_status check_adapters(const w4a16_adapters* ad, const w4a16_weight_desc* d
   return W4A16_OK;
 }
 
-// `rows` rows of h, `expected` of them written under uniform routing
-w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, int32_t topk, int64_t rows, int64_t expected) {
+// `rows` rows of h, in `expected` positions under uniform routing (of a dense product: the rows).  With `packed` the
+// planes are added once, by a launch of their own.
+w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, bool routed, int32_t topk, int64_t rows, int64_t expected,
+                                    bool packed) {
   w4a16::AdapterParams q;
   std::memset(&q, 0, sizeof q);
   q.a = ad.a;
@@ -1576,8 +1578,12 @@ w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, int32_t topk, int6
   q.N = ad.N;
   q.topk = topk;
   q.rows = rows;
-  q.ks = w4a16::shrink_slices(expected, ad.slices * ad.rank, (ad.K + 127) / 128);
+  q.ks = w4a16::shrink_slices(routed, expected, ad.slices * ad.rank, ad.K, packed);
   return q;
+}
+
+size_t packed_bytes(const w4a16::AdapterParams& q, bool packed) {
+  return packed ? al256((size_t)q.rows * q.slices * ((q.rank + 15) / 16) * 64) : 0;
 }
 
 size_t h_bytes(const w4a16::AdapterParams& q) {
@@ -1592,15 +1598,27 @@ w4a16_status check_workspace(size_t need, const void* workspace, size_t workspac
 }
 
 struct LinearWorkspace {
-  size_t h = 0, order = 0, parts = 0;
-  size_t total() const { return h + order + parts; }
+  size_t h = 0, order = 0, packed = 0, parts = 0;
+  size_t total() const { return h + order + packed + parts; }
 };
+
+// rows from which the dense product packs h
+constexpr int32_t kPackMinRows = 1024;
+
+bool linear_packs(const w4a16_weight_desc* d, int32_t T) {
+  return T >= kPackMinRows && w4a16::linear_whole_tiles(T, d->N, d->chunks);
+}
+
+w4a16::AdapterParams linear_adapters(const w4a16_adapters& ad, const w4a16_weight_desc* d, int32_t T) {
+  return adapter_params(ad, false, 1, T, T, linear_packs(d, T));
+}
 
 LinearWorkspace linear_workspace(const w4a16_weight_desc* d, int32_t T, const w4a16::AdapterParams* q) {
   LinearWorkspace w;
   if (q) {
     w.h = h_bytes(*q);
     w.order = al256((size_t)T * sizeof(int32_t));
+    w.packed = packed_bytes(*q, linear_packs(d, T));
   }
   w.parts = al256(w4a16::linear_parts_bytes(T, d->N, d->chunks));
   return w;
@@ -1621,6 +1639,15 @@ int64_t expected_positions(const w4a16_indexed_routing& r) {
   const double slots = expected_slots(r);
   const double pad = std::min<double>(r.E_loc, slots) * (r.block_m / 2);
   return std::min<int64_t>(position_bound(r), (int64_t)(slots + pad));
+}
+
+// Local slots from which the routed products pack h
+constexpr double kPackMinSlots = 1024;
+
+bool routed_packs(const w4a16_indexed_routing& r) { return expected_slots(r) >= kPackMinSlots; }
+
+w4a16::AdapterParams routed_adapters(const w4a16_adapters& ad, const w4a16_indexed_routing& r) {
+  return adapter_params(ad, true, r.topk, (int64_t)r.T * r.topk, expected_positions(r), routed_packs(r));
 }
 
 // The config of an indexed call with adapters: whole tiles, not split along K.
@@ -1660,15 +1687,16 @@ hipError_t shrink_routed(const w4a16::AdapterParams& q, const uint16_t* a, int32
 }
 
 struct AdapterWorkspace {
-  size_t h = 0, combine = 0;
+  size_t h = 0, packed = 0, combine = 0;
   int32_t cols = 0;
-  size_t total() const { return h + combine; }
+  size_t total() const { return h + packed + combine; }
 };
 
 AdapterWorkspace adapter_workspace(const w4a16_config& c, const w4a16_weight_desc* d, const w4a16_indexed_routing& r,
                                    const w4a16::AdapterParams& q, bool combine) {
   AdapterWorkspace w;
   w.h = h_bytes(q);
+  w.packed = packed_bytes(q, routed_packs(r));
   w.cols = combine ? combine_cols_of(c, d->N, r.T, r.topk, r.E_glob, r.E_loc) : d->N;
   if (combine) w.combine = al256((size_t)r.T * r.topk * w.cols * sizeof(float));
   return w;
@@ -1682,7 +1710,7 @@ size_t w4a16_linear_workspace_bytes(const w4a16_weight_desc* desc, int32_t T, co
   if (check_int4_desc(desc) != W4A16_OK || T <= 0) return 0;
   if (adapters && check_adapters(adapters, desc, T) != W4A16_OK) return 0;
   w4a16::AdapterParams q;
-  if (adapters) q = adapter_params(*adapters, 1, T, T);
+  if (adapters) q = linear_adapters(*adapters, desc, T);
   return linear_workspace(desc, T, adapters ? &q : nullptr).total();
 }
 
@@ -1707,7 +1735,7 @@ w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, c
     if (st != W4A16_OK) return st;
   }
   if (T == 0) return W4A16_OK;
-  if (adapters) sp.ad = adapter_params(*adapters, 1, T, T);
+  if (adapters) sp.ad = linear_adapters(*adapters, desc, T);
   sp.ad.rows = T;
   const LinearWorkspace wl = linear_workspace(desc, T, adapters ? &sp.ad : nullptr);
   st = check_workspace(wl.total(), workspace, workspace_bytes);
@@ -1722,9 +1750,11 @@ w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, c
   // in one block of 16 rows no order changes anything
   if (adapters && T > 16 && T <= w4a16::kOrderMaxRows) sp.order = reinterpret_cast<int32_t*>(ws + wl.h);
   sp.ad.order = sp.order;
+  if (wl.packed) sp.ad.packed = reinterpret_cast<uint16_t*>(ws + wl.h + wl.order);
   const w4a16::GemmParams p = base_params(desc, packed_w, packed_s, x, out, 1, 1);
   const hipError_t e = w4a16::launch_linear(silu ? w4a16::kEpiSilu : w4a16::kEpiStore, p, sp,
-                                            reinterpret_cast<float*>(ws + wl.h + wl.order), static_cast<hipStream_t>(stream));
+                                            reinterpret_cast<float*>(ws + wl.h + wl.order + wl.packed),
+                                            static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "linear launch");
   return W4A16_OK;
 }
@@ -1738,7 +1768,7 @@ size_t w4a16_moe_adapter_workspace_bytes(const w4a16_weight_desc* desc, const w4
   w4a16_config c{};
   // the config steers only the combine's columns, which do not depend on the epilogue's tile
   if (adapter_call_config(r, desc, combine ? w4a16::kEpiWeighted : w4a16::kEpiStore, cfg, &c) != W4A16_OK) return 0;
-  const w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, expected_positions(r));
+  const w4a16::AdapterParams q = routed_adapters(*adapters, r);
   return adapter_workspace(c, desc, r, q, combine != 0).total();
 }
 
@@ -1770,13 +1800,15 @@ w4a16_status w4a16_moe_adapter_gemm(const w4a16_weight_desc* desc, const void* p
   if (st != W4A16_OK) return st;
   if (combine && !r.topk_ids) return fail(W4A16_ERR_ARG, "combine needs routing.topk_ids");
   if (r.T == 0) return W4A16_OK;
-  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, expected_positions(r));
+  w4a16::AdapterParams q = routed_adapters(*adapters, r);
   const AdapterWorkspace wl = adapter_workspace(c, desc, r, q, combine);
   st = check_workspace(wl.total(), workspace, workspace_bytes);
   if (st != W4A16_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  q.h = static_cast<float*>(workspace);
-  float* comb = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.h);
+  char* ws = static_cast<char*>(workspace);
+  q.h = reinterpret_cast<float*>(ws);
+  if (wl.packed) q.packed = reinterpret_cast<uint16_t*>(ws + wl.h);
+  float* comb = reinterpret_cast<float*>(ws + wl.h + wl.packed);
   hipError_t e = shrink_routed(q, a, a_layout, desc, r, s);
   if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, a, combine ? (void*)comb : (void*)out, c.nr, c.waves);
@@ -1827,11 +1859,13 @@ w4a16_status w4a16_moe_adapter_gate_up_silu(const w4a16_weight_desc* desc, const
   st = adapter_call_config(r, desc, w4a16::kEpiSilu, cfg, &c);
   if (st != W4A16_OK) return st;
   if (r.T == 0) return W4A16_OK;
-  w4a16::AdapterParams q = adapter_params(*adapters, r.topk, (int64_t)r.T * r.topk, expected_positions(r));
-  st = check_workspace(h_bytes(q), workspace, workspace_bytes);
+  w4a16::AdapterParams q = routed_adapters(*adapters, r);
+  const AdapterWorkspace wl = adapter_workspace(c, desc, r, q, false);
+  st = check_workspace(wl.total(), workspace, workspace_bytes);
   if (st != W4A16_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   q.h = static_cast<float*>(workspace);
+  if (wl.packed) q.packed = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + wl.h);
   hipError_t e = shrink_routed(q, x, W4A16_A_TOKEN, desc, r, s);
   if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, x, out, c.nr, c.waves);

@@ -245,6 +245,8 @@ hipError_t launch_of(const GemmParams& p, const ShrinkParams& sp, float* parts, 
 
 }  // namespace
 
+bool linear_whole_tiles(int64_t T, int32_t N, int32_t KC) { return linear_plan(T, N, KC).mt == 0; }
+
 size_t linear_parts_bytes(int64_t T, int32_t N, int32_t KC) {
   return (size_t)linear_plan(T, N, KC).slices * (size_t)T * N * sizeof(float);
 }

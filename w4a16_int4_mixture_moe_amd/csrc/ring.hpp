@@ -1,5 +1,6 @@
-// A ring of registers: D chunks in flight, the next one requested as soon as a
-// chunk has been used.
+// Shared by the adapters' kernels: a ring of registers (D chunks in flight, the
+// next one requested as soon as a chunk has been used), and the two bf16 parts of
+// an fp32 value.
 #pragma once
 #include <type_traits>
 
@@ -39,6 +40,17 @@ __device__ __forceinline__ void ring_run(int c0, int c1, Use&& use, Request&& re
   if (cb < c1) {
     ring_steps<D>([&](auto st) { request(st, min(cb + decltype(st)::value, c1 - 1)); });
     drain();
+  }
+}
+
+// v = hi + lo up to 2^-17 of it; where hi is infinite it stands alone
+__device__ __forceinline__ void split_bf16(const f32x4_t (&v)[2], bf16x8_t& hi, bf16x8_t& lo) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float x = v[c / 4][c % 4];
+    hi[c] = (__bf16)x;
+    const float part = x - (float)hi[c];
+    lo[c] = (__bf16)(part == part ? part : 0.f);
   }
 }
 
