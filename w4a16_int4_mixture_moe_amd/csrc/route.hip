@@ -216,10 +216,17 @@ template <int L, int V>
 struct GroupSmem {
   static constexpr int G = kRouteThreads / L;
   float key[G][L * V];
-  double score[G][kMaxGroups];
+  float score[G][(L == 16 ? kNarrowMaxGroups : kMaxGroups) + 4];   // read four at a time, -inf behind the last
+  float edge[G][2];                                 // the last score kept, the first one left out
 };
 
-// the two largest of (a, b) and (c, d), a >= b and c >= d
+// the two largest of (a, b) and c; a >= b
+__device__ __forceinline__ void take_one(float& a, float& b, float c) {
+  b = __builtin_amdgcn_fmed3f(a, b, c);
+  a = fmaxf(a, c);
+}
+
+// ... and of (a, b) and (c, d), c >= d
 template <typename K>
 __device__ __forceinline__ void merge_two(K& a, K& b, K c, K d) {
   const K low = a < c ? a : c;
@@ -234,76 +241,116 @@ __device__ __forceinline__ K group_score(K a, K b) {
   return kSigmoid && b > -(K)INFINITY ? a + b : a;
 }
 
-// The groups that stay, a bit each.  key: this lane's keys (-inf: masked);
-// logit(e) and bias(e) of the token's expert e.
-template <typename T, int L, int V, bool kSigmoid, typename Logit>
+// The groups that stay: bit (group << shift) of the result, shift = log2 of the
+// lanes a group has.  key: this lane's keys (-inf: masked; a NaN as well);
+// logit(e) of the token's expert e.
+template <int L, int V, bool kSigmoid, typename Logit>
 __device__ __forceinline__ uint64_t kept_groups(const RouteArgs& p, GroupSmem<L, V>& sm, const float (&key)[V], bool biased,
-                                                Logit&& logit) {
+                                                int& shift, Logit&& logit) {
   const int g = threadIdx.x / L, l = threadIdx.x % L;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sm.key[g][i * L + l] = key[i] > -INFINITY ? key[i] : -INFINITY;   // a NaN as masked
+  for (int i = 0; i < V; ++i) sm.key[g][i * L + l] = key[i] > -INFINITY ? key[i] : -INFINITY;
   __builtin_amdgcn_wave_barrier();
-  int per = 1;                                      // lanes a group
-  while (2 * per * p.groups <= L) per *= 2;
-  const int mine = l / per, sub = l % per;
+  shift = 0;
+  while ((2 << shift) * p.groups <= L) ++shift;
+  const int per = 1 << shift;
+  const int mine = l >> shift, sub = l & (per - 1);
   const bool has = mine < p.groups;
   float a = -INFINITY, b = -INFINITY;
-  if (has)
-    for (int e = sub; e < p.size; e += per) merge_two(a, b, sm.key[g][mine * p.size + e], -INFINITY);
+  if (has) {
+    const float* keys = &sm.key[g][mine * p.size];
+    if (p.size % 4 == 0) {
+#pragma unroll 2
+      for (int e = 4 * sub; e < p.size; e += 4 * per) {
+        const float4 k = *reinterpret_cast<const float4*>(keys + e);
+        take_one(a, b, k.x);
+        take_one(a, b, k.y);
+        take_one(a, b, k.z);
+        take_one(a, b, k.w);
+      }
+    } else {
+#pragma unroll 4
+      for (int e = sub; e < p.size; e += per) take_one(a, b, keys[e]);
+    }
+  }
   for (int m = 1; m < per; m *= 2) merge_two(a, b, __shfl_xor(a, m), __shfl_xor(b, m));
+  const float key1 = a, key2 = b;
   // without a bias the keys are logits, in the order of the scores that add up
   if (kSigmoid && !biased) {
     if (a > -INFINITY) a = sigmoid_key(a);
     if (b > -INFINITY) b = sigmoid_key(b);
   }
-  double score = (double)group_score<kSigmoid>(a, b);
-  // each group's place among the groups, the scores in LDS
-  auto place = [&]() {
-    if (has && sub == 0) sm.score[g][mine] = score;
-    __builtin_amdgcn_wave_barrier();
-    int before_it = 0;
-    if (has)
-      for (int j = 0; j < p.groups; ++j) before_it += before(sm.score[g][j], j, score, mine) ? 1 : 0;
-    __builtin_amdgcn_wave_barrier();
-    return before_it;
-  };
-  int rank = place();
-  if (kSigmoid) {
-    // is the first group left out as good as the last one kept?
-    // (each key within key_error of its own size, which the sum may not show)
-    double out = -HUGE_VAL, in = HUGE_VAL;
-    float c = 0.f;
-    if (has && rank == p.keep) out = score;
-    if (has && rank == p.keep - 1) in = score;
-    if (a > -INFINITY) c = fabsf(a) + (b > -INFINITY ? fabsf(b) : 0.f);
-#pragma unroll
-    for (int m = 1; m < L; m *= 2) {
-      out = fmax(out, __shfl_xor(out, m));
-      in = fmin(in, __shfl_xor(in, m));
-      c = fmaxf(c, __shfl_xor(c, m));
+  const float score = group_score<kSigmoid>(a, b);
+  // each group's place among the groups
+  if (has && sub == 0) sm.score[g][mine] = score;
+  if (l < 4) sm.score[g][p.groups + l] = -INFINITY;
+  __builtin_amdgcn_wave_barrier();
+  int rank = 0;
+  if (has)
+#pragma unroll 2
+    for (int j = 0; j < p.groups; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&sm.score[g][j]);
+      rank += (o.x > score || (o.x == score && j < mine)) + (o.y > score || (o.y == score && j + 1 < mine)) +
+              (o.z > score || (o.z == score && j + 2 < mine)) + (o.w > score || (o.w == score && j + 3 < mine));
     }
-    const bool close = out > -HUGE_VAL && !(in - out > 4.0 * (double)key_error(c));
-    if (__ballot(close)) {                          // any group of the wave
+  bool stays = has && sub == 0 && rank < p.keep;
+  if (kSigmoid) {
+    // is the first group left out as good as the last one kept, within what 32 bits tell (each key within key_error of
+    // its own size, which the sum may not show)?
+    if (has && sub == 0 && (rank == p.keep || rank == p.keep - 1)) sm.edge[g][rank == p.keep] = score;
+    const float size = a > -INFINITY ? fabsf(a) + (b > -INFINITY ? fabsf(b) : 0.f) : 0.f;
+    const float c = group_max<L>(size);
+    __builtin_amdgcn_wave_barrier();
+    const float in = sm.edge[g][0], out = sm.edge[g][1];
+    const bool close = out > -INFINITY && !((double)in - (double)out > 4.0 * (double)key_error(c));
+    if (__ballot(close)) {                          // any group of the wave: once more in 64 bits
       double x = -HUGE_VAL, y = -HUGE_VAL;
-      if (has)
-        for (int e = sub; e < p.size; e += per) {
-          const int at = mine * p.size + e;
-          if (sm.key[g][at] > -INFINITY) merge_two(x, y, exact_key(logit(at), biased ? p.bias[at] : 0.f), -HUGE_VAL);
+      if (!biased) {                                // keys are the logits themselves: the two largest are known
+        if (close && key1 > -INFINITY) x = exact_key(key1, 0.f);
+        if (close && key2 > -INFINITY) y = exact_key(key2, 0.f);
+      } else {
+        // only the experts that may be among the two: a lane seldom has more than four
+        const float least = key2 - 2.f * key_error(fmaxf(fabsf(key1), fabsf(key2)));
+        int found[4] = {-1, -1, -1, -1}, n = 0;
+        if (has && close)
+          for (int e = sub; e < p.size; e += per) {
+            const int at = mine * p.size + e;
+            const float k = sm.key[g][at];
+            if (!(k > -INFINITY) || k < least) continue;
+            found[3] = found[2];
+            found[2] = found[1];
+            found[1] = found[0];
+            found[0] = at;
+            ++n;
+          }
+        if (!__ballot(n > 4)) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (found[u] >= 0) merge_two(x, y, exact_key(logit(found[u]), p.bias[found[u]]), -HUGE_VAL);
+        } else if (has && close) {
+          for (int e = sub; e < p.size; e += per) {
+            const int at = mine * p.size + e;
+            if (sm.key[g][at] > -INFINITY) merge_two(x, y, exact_key(logit(at), p.bias[at]), -HUGE_VAL);
+          }
         }
-      for (int m = 1; m < per; m *= 2) merge_two(x, y, __shfl_xor(x, m), __shfl_xor(y, m));
-      score = group_score<kSigmoid>(x, y);
-      rank = place();
+        for (int m = 1; m < per; m *= 2) merge_two(x, y, __shfl_xor(x, m), __shfl_xor(y, m));
+      }
+      const double sum = group_score<kSigmoid>(x, y);
+      rank = 0;
+      const int token = (threadIdx.x % 64) & ~(L - 1);   // its first lane in the wave
+      for (int j = 0; j < p.groups; ++j) {
+        const double o = __shfl(sum, token + (j << shift));
+        rank += before(o, j, sum, mine) ? 1 : 0;
+      }
+      if (close) stays = has && sub == 0 && rank < p.keep;
     }
   }
-  // one bit a group, gathered over the token's lanes
-  uint64_t kept = has && sub == 0 && rank < p.keep ? 1ull << mine : 0ull;
-#pragma unroll
-  for (int m = 1; m < L; m *= 2) kept |= __shfl_xor(kept, m);
-  return kept;
+  const uint64_t lanes = __ballot(stays);
+  return L == 64 ? lanes : lanes >> (threadIdx.x % 64 & ~(L - 1)) & 0xFFFFull;
 }
 
 template <typename T, int L, int V, bool kSigmoid, bool kGroups>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p) {
+__global__ __launch_bounds__(kRouteThreads, kGroups && L == 16 && V <= 24 ? 4 : 1) void route_kernel(const RouteArgs p) {
   using Smem = RouteSmem<L>;
   constexpr int OWN = Smem::CAP / L;                // listed experts a lane looks after
   __shared__ Smem sm;
@@ -358,10 +405,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs p)
     sum = group_sum<L>(sum);
   }
   uint64_t kept = 0;
-  auto group_kept = [&](int e) { return (kept >> (((uint32_t)e * p.group_mul) >> 20) & 1ull) != 0; };
+  int group_shift = 0;
+  auto group_kept = [&](int e) { return (kept >> ((((uint32_t)e * p.group_mul) >> 20) << group_shift) & 1ull) != 0; };
   if constexpr (kGroups) {
     __shared__ GroupSmem<L, V> gs;
-    kept = kept_groups<T, L, V, kSigmoid>(p, gs, key, biased, [&](int e) { return logit_value(rows[row0 + e]); });
+    kept = kept_groups<L, V, kSigmoid>(p, gs, key, biased, group_shift, [&](int e) { return logit_value(rows[row0 + e]); });
     m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
