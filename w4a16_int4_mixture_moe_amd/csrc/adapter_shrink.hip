@@ -14,7 +14,7 @@ __global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_kernel(const
   shrink_block<2>(p, grid, blockIdx.x);
 }
 
-constexpr int kShrinkMaxPlanes = 4;             // twice as many where they are packed
+constexpr int kShrinkMaxPlanes = 8;
 constexpr int64_t kTileMinRows = 2048;
 constexpr int64_t kTileMinInner = 1 << 17;
 constexpr int kOrderThreads = 1024;
@@ -167,15 +167,15 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_pack_kernel(const Shri
   f32x4_t v[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
   if (8 * e < q.rank) {
     const float* src = q.h + row * width + slice * q.rank + 8 * e;
-    f32x4_t w[kShrinkMaxPlanes * 2][2];
+    f32x4_t w[kShrinkMaxPlanes][2];
 #pragma unroll
-    for (int k = 0; k < kShrinkMaxPlanes * 2; ++k) {    // past the last plane: the last again, not added
+    for (int k = 0; k < kShrinkMaxPlanes; ++k) {    // past the last plane: the last again, not added
       const float* from = src + min(k, q.ks - 1) * q.rows * width;
       w[k][0] = *reinterpret_cast<const f32x4_t*>(from);
       w[k][1] = *reinterpret_cast<const f32x4_t*>(from + 4);
     }
 #pragma unroll
-    for (int k = 0; k < kShrinkMaxPlanes * 2; ++k)
+    for (int k = 0; k < kShrinkMaxPlanes; ++k)
       if (k < q.ks) {
         v[0] += w[k][0];
         v[1] += w[k][1];
@@ -215,7 +215,7 @@ int shrink_slices(bool routed, int64_t expected, int32_t width, int32_t K, bool 
   const int64_t items = std::max<int64_t>(tiles * parts_of(width), 1);
   const int deep = staged ? 1 : kShrinkWaves / waves_wide(width);
   return (int)std::max<int64_t>(1, std::min<int64_t>({(kShrinkGroups + items - 1) / items,
-                                                      packed ? kShrinkMaxPlanes * 2 : kShrinkMaxPlanes,
+                                                      packed || routed ? kShrinkMaxPlanes : kShrinkMaxPlanes / 2,
                                                       (K + kChunk - 1) / kChunk / (2 * deep)}));
 }
 

@@ -147,9 +147,10 @@ __device__ __forceinline__ ShrinkRow shrink_row(const ShrinkParams& p, int64_t p
   const AdapterParams& q = p.ad;
   ShrinkRow r{-1, 0, 0};
   if (p.sorted_ids != nullptr) {
-    if (pos < min(p.positions, (int64_t)*p.num_tokens_padded)) {
-      const int s = p.sorted_ids[pos];
-      const int e = p.expert_ids[pos >> p.block_shift];
+    // read together, positions past the padded total as well (they are inside the buffers)
+    const int64_t at = min(pos, p.positions - 1);
+    const int s = p.sorted_ids[at], e = p.expert_ids[at >> p.block_shift], total = *p.num_tokens_padded;
+    if (pos < min(p.positions, (int64_t)total)) {
       if ((unsigned)s < (unsigned)p.sentinel && (unsigned)e < (unsigned)q.E) {
         const int a = q.ids[s / q.topk];
         if ((unsigned)a < (unsigned)q.L) r.key = a * q.E + e;
