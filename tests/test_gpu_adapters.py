@@ -238,6 +238,27 @@ def test_linear_ranks(T, rank):
     Shared(T, 640, 160, 3, rank, 1).check()
 
 
+@pytest.mark.parametrize("T,K,N,rank,slices", [(2100, 256, 512, 128, 2), (1100, 384, 1024, 72, 1), (8200, 128, 64, 24, 1),
+                                                 (2300, 160, 256, 104, 2), (17000, 128, 64, 16, 2)])
+@pytest.mark.parametrize("runs", [7, 0])
+def test_linear_many_rows(T, K, N, rank, slices, runs):
+    """Inner values packed once, A in parts of 128 rows, the staged first half; K that it does not take; no order of
+    the rows."""
+    ids = None
+    if runs:
+        ids = torch.arange(T, device=dev()).mul(runs).div(T, rounding_mode="floor").to(torch.int32) - 1
+    P = Shared(T, K, N, 6, rank, slices, ids=ids)
+    P.check()
+    assert torch.equal(bits_t(P.run()), bits_t(P.run()))
+
+
+@pytest.mark.parametrize("T", [5, 40, 400])
+def test_linear_one_slice_for_gate_and_up(T):
+    P = Shared(T, 384, 160, 4, 16, 1, gate_up=True)
+    P.check(silu=True)
+    P.check()
+
+
 @pytest.mark.parametrize("T,La", [(64, 1024), (300, 1024), (16, 64), (64, 64), (640, 1)])
 def test_linear_adapter_counts(T, La):
     Shared(T, 256, 128, La, 8).check()
@@ -385,7 +406,8 @@ def _positions(r, T, k):
 SHAPES = [dict(T=1, k=8, E=16, first=0, El=16, K=256, N=64, La=2, r=16),
           dict(T=37, k=3, E=12, first=2, El=7, K=1120, N=96, La=5, r=24),
           dict(T=130, k=4, E=10, first=4, El=5, K=384, N=160, La=7, r=8),
-          dict(T=600, k=2, E=3, first=0, El=2, K=128, N=288, La=3, r=40)]
+          dict(T=600, k=2, E=3, first=0, El=2, K=128, N=288, La=3, r=40),
+          dict(T=900, k=2, E=4, first=1, El=3, K=256, N=64, La=4, r=72)]      # enough slots for packed inner values
 
 
 @pytest.mark.parametrize("shape", SHAPES)
