@@ -697,8 +697,8 @@ size_t w4a16_moe_few_tokens_workspace_bytes(const w4a16_weight_desc* gate_up, in
  * adapter, or with another one, gives does not depend on an adapter's values,
  * finite or not.
  * Sizes: rank a multiple of 8 up to W4A16_ADAPTER_MAX_RANK, L up to
- * W4A16_ADAPTER_MAX, L * E below 2^30, N % 32 == 0 with two slices; E, N and K
- * are the weight's (ERR_SHAPE).
+ * W4A16_ADAPTER_MAX, L * E below 2^30, N % 32 == 0 with two slices, slices *
+ * rank * K * 2 bytes at most 4 GiB; E, N and K are the weight's (ERR_SHAPE).
  * Pointers: a, b 16-byte aligned; scale, token_adapter 4.
  * ---------------------------------------------------------------------- */
 #define W4A16_ADAPTER_MAX 1024

@@ -193,8 +193,8 @@ __device__ __forceinline__ bf16x8_t b_operand(const AdapterParams& q, const uint
 // and for rows without an adapter).  h goes through LDS, then the adapters of
 // the block are taken in rising order: an adapter's B once for all row tiles
 // that hold it.  at(slice, row, granule): see stage_h; that memory is free
-// before the call and after it (both synchronise).
-template <int MT, int NR, int NW, int NA, typename Smem, typename Place>
+// before the call and after it (both synchronise).  PACKS: h may be packed.
+template <int MT, int NR, int NW, int NA, bool PACKS, typename Smem, typename Place>
 __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const AdapterParams& q, const Smem& sm,
                                                     int expert, int rt_base, f32x4_t (&acc)[NR][MT], Place&& at) {
   constexpr int U = MT >= 8 ? 2 : 4;
@@ -227,13 +227,14 @@ __device__ __forceinline__ void start_from_adapters(const GemmParams& p, const A
   const int first = next_after(-1);
   if (first == INT32_MAX) return clear();               // the whole block, so every wave
   // the first ranks before the accumulators take their registers
-  if (q.packed != nullptr) stage_packed_h<16 * MT, NW * kWave, MT >= 4 ? 16 : 2>(q, sm, 0, at);
+  const bool packed = PACKS && q.packed != nullptr;
+  if (packed) stage_packed_h<16 * MT, NW * kWave, 16>(q, sm, 0, at);
   else stage_h<16 * MT, NW * kWave, MT >= 4 ? 2 : 1, 4>(q, sm, 0, at);
   clear();
   for (int r0 = 0; r0 < q.rank; r0 += kHRanks) {
     if (r0 > 0) {
       __syncthreads();
-      if (q.packed != nullptr) stage_packed_h<16 * MT, NW * kWave, 4>(q, sm, r0, at);
+      if (packed) stage_packed_h<16 * MT, NW * kWave, 4>(q, sm, r0, at);
       else stage_h<16 * MT, NW * kWave, 1, 2>(q, sm, r0, at);
     }
     __syncthreads();

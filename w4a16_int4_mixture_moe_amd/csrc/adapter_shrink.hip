@@ -15,6 +15,7 @@ __global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_kernel(const
 }
 
 constexpr int kShrinkMaxPlanes = 8;
+constexpr int64_t kFewRows = 64;
 constexpr int64_t kTileMinRows = 2048;
 constexpr int64_t kTileMinInner = 1 << 17;
 constexpr int kOrderThreads = 1024;
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(kShrinkThreads, 2) void adapter_shrink_tile_kernel(
 }
 
 
-// The planes' sum of each row that has an adapter, as the two bf16 parts that the products take
+// The planes' sum of each row that has an adapter, as the two bf16 parts that the product takes
 // (AdapterParams::packed): where many workgroups read a row's h they would each add the planes.
 __global__ __launch_bounds__(kShrinkThreads) void adapter_pack_kernel(const ShrinkParams p, int64_t threads) {
   const int64_t at = (int64_t)blockIdx.x * kShrinkThreads + threadIdx.x;
@@ -160,9 +161,8 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_pack_kernel(const Shri
   const int64_t rs = at / eights;                       // (row, slice)
   const int64_t row = rs / q.slices;
   const int slice = (int)(rs - row * q.slices);
-  const int a = q.ids[row / q.topk];
+  const int a = q.ids[row];
   if ((unsigned)a >= (unsigned)q.L) return;
-  // a routed row that no expert held here has is packed as well, from whatever its place holds: nothing reads it
   const int width = q.slices * q.rank;
   f32x4_t v[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
   if (8 * e < q.rank) {
@@ -199,7 +199,9 @@ int64_t tiles_of(int64_t positions) { return (positions + kShrinkRows - 1) / kSh
 int parts_of(int32_t width) { return (width + kShrinkWidth * waves_wide(width) - 1) / (kShrinkWidth * waves_wide(width)); }
 
 // The staged tile where x outweighs A by far: rows of requests side by side (one weight), from 2048 rows and
-// 2^17 inner values on
+// 2^17 inner values on.  Measured on MI355X, us of the whole call with / without it, 32 adapters by row at random: 7168 x
+// 4096, 32 inner values, 1024 rows 133 / 103, 2048 rows 189 / 180, 4096 rows 239 / 243, 8192 rows 436 / 459; 128 inner
+// values, 2048 rows 182 / 252, 8192 rows 465 / 617.  Routed rows, few of an (adapter, expert) in 128: 86 us against 56 for 4096 tokens.
 bool tiles_apply(bool routed, int64_t rows, int32_t width, int32_t K) {
   return !routed && K % kChunk == 0 && rows >= kTileMinRows &&
          rows * std::min(width, kShrinkWaves * kShrinkWidth) >= kTileMinInner;
@@ -207,16 +209,20 @@ bool tiles_apply(bool routed, int64_t rows, int32_t width, int32_t K) {
 
 }  // namespace
 
-// Planes of h: K is cut where the tiles alone leave CUs idle, not below two chunks a wave; every reader of h adds the
-// planes, unless they are packed first
+// Planes of h: K is cut where the tiles alone leave CUs idle, not below two chunks a wave.  Every reader of h adds the
+// planes unless they are packed first, so a dense product's are at most four; at few rows eight where four would leave a
+// wave more than six chunks.  Measured on MI355X, us of the whole call with four / eight: 7168 x 4096, rank 16 twice
+// (3.5 chunks a wave), 64 rows 25.3 / 26.7, 128 rows 28.7 / 36.1; rank 64 twice (14 chunks), 16 rows 32.0 / 25.9, 64
+// rows 40.0 / 34.3, 200 rows 60 / 72; 2048 x 7168, rank 128 (4 chunks), 64 rows 44.8 / 49.5.
 int shrink_slices(bool routed, int64_t expected, int32_t width, int32_t K, bool packed) {
   const bool staged = tiles_apply(routed, expected, width, K);
   const int64_t tiles = (expected + (staged ? kTileRows : kShrinkRows) - 1) / (staged ? kTileRows : kShrinkRows);
   const int64_t items = std::max<int64_t>(tiles * parts_of(width), 1);
   const int deep = staged ? 1 : kShrinkWaves / waves_wide(width);
+  const int64_t chunks = (K + kChunk - 1) / kChunk;
+  const bool wide = packed || routed || (expected <= kFewRows && chunks > 6 * deep * (kShrinkMaxPlanes / 2));
   return (int)std::max<int64_t>(1, std::min<int64_t>({(kShrinkGroups + items - 1) / items,
-                                                      packed || routed ? kShrinkMaxPlanes : kShrinkMaxPlanes / 2,
-                                                      (K + kChunk - 1) / kChunk / (2 * deep)}));
+                                                      wide ? kShrinkMaxPlanes : kShrinkMaxPlanes / 2, chunks / (2 * deep)}));
 }
 
 hipError_t shrink_grid(const ShrinkParams& p, ShrinkGrid* out) {

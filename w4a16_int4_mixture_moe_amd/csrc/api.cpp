@@ -1582,10 +1582,6 @@ w4a16::AdapterParams adapter_params(const w4a16_adapters& ad, bool routed, int32
   return q;
 }
 
-size_t packed_bytes(const w4a16::AdapterParams& q, bool packed) {
-  return packed ? al256((size_t)q.rows * q.slices * ((q.rank + 15) / 16) * 64) : 0;
-}
-
 size_t h_bytes(const w4a16::AdapterParams& q) {
   return al256((size_t)q.ks * (size_t)q.rows * q.slices * q.rank * sizeof(float));
 }
@@ -1602,23 +1598,30 @@ struct LinearWorkspace {
   size_t total() const { return h + order + packed + parts; }
 };
 
-// rows from which the dense product packs h
-constexpr int32_t kPackMinRows = 1024;
+// The dense product packs h (a launch that adds the planes once, instead of every column tile) from kPackMinRows rows
+// and kPackMinPlanes planes on.  Measured on MI355X, us of the whole call with / without: 7168 x 4096, rank 64 twice, 600
+// rows 121 / 168, 1024 rows 167 / 243, 8192 rows 478 / 502, 301 rows 78 / 77; rank 16 twice, 512 rows 80 / 77, 1024 rows
+// 104 / 126; 2048 x 7168, rank 128, 1024 rows 106 / 120, rank 32 (two planes), 1024 rows 77 / 71.
+constexpr int32_t kPackMinRows = 512;
+constexpr int32_t kPackMinPlanes = 4;
 
-bool linear_packs(const w4a16_weight_desc* d, int32_t T) {
-  return T >= kPackMinRows && w4a16::linear_whole_tiles(T, d->N, d->chunks);
+struct LinearAdapters {
+  w4a16::AdapterParams q;
+  bool packs;
+};
+
+LinearAdapters linear_adapters(const w4a16_adapters& ad, const w4a16_weight_desc* d, int32_t T) {
+  const LinearAdapters plain{adapter_params(ad, false, 1, T, T, false), false};
+  if (T < kPackMinRows || plain.q.ks < kPackMinPlanes || !w4a16::linear_whole_tiles(T, d->N, d->chunks)) return plain;
+  return {adapter_params(ad, false, 1, T, T, true), true};
 }
 
-w4a16::AdapterParams linear_adapters(const w4a16_adapters& ad, const w4a16_weight_desc* d, int32_t T) {
-  return adapter_params(ad, false, 1, T, T, linear_packs(d, T));
-}
-
-LinearWorkspace linear_workspace(const w4a16_weight_desc* d, int32_t T, const w4a16::AdapterParams* q) {
+LinearWorkspace linear_workspace(const w4a16_weight_desc* d, int32_t T, const LinearAdapters* ad) {
   LinearWorkspace w;
-  if (q) {
-    w.h = h_bytes(*q);
+  if (ad) {
+    w.h = h_bytes(ad->q);
     w.order = al256((size_t)T * sizeof(int32_t));
-    w.packed = packed_bytes(*q, linear_packs(d, T));
+    if (ad->packs) w.packed = al256((size_t)T * ad->q.slices * ((ad->q.rank + 15) / 16) * 64);
   }
   w.parts = al256(w4a16::linear_parts_bytes(T, d->N, d->chunks));
   return w;
@@ -1641,13 +1644,10 @@ int64_t expected_positions(const w4a16_indexed_routing& r) {
   return std::min<int64_t>(position_bound(r), (int64_t)(slots + pad));
 }
 
-// Local slots from which the routed products pack h
-constexpr double kPackMinSlots = 1024;
-
-bool routed_packs(const w4a16_indexed_routing& r) { return expected_slots(r) >= kPackMinSlots; }
-
+// (h is not packed here, where that pays at no size.  Measured on MI355X, 48 of 384 experts, 7168 and 2048, us of gate/up and down + combine with / without: 4096 tokens, rank 16
+// 383 / 371 and 270 / 260, rank 64 494 / 492 and 330 / 327; 512 tokens, rank 16 216 / 213 and 116 / 111.)
 w4a16::AdapterParams routed_adapters(const w4a16_adapters& ad, const w4a16_indexed_routing& r) {
-  return adapter_params(ad, true, r.topk, (int64_t)r.T * r.topk, expected_positions(r), routed_packs(r));
+  return adapter_params(ad, true, r.topk, (int64_t)r.T * r.topk, expected_positions(r), false);
 }
 
 // The config of an indexed call with adapters: whole tiles, not split along K.
@@ -1687,16 +1687,15 @@ hipError_t shrink_routed(const w4a16::AdapterParams& q, const uint16_t* a, int32
 }
 
 struct AdapterWorkspace {
-  size_t h = 0, packed = 0, combine = 0;
+  size_t h = 0, combine = 0;
   int32_t cols = 0;
-  size_t total() const { return h + packed + combine; }
+  size_t total() const { return h + combine; }
 };
 
 AdapterWorkspace adapter_workspace(const w4a16_config& c, const w4a16_weight_desc* d, const w4a16_indexed_routing& r,
                                    const w4a16::AdapterParams& q, bool combine) {
   AdapterWorkspace w;
   w.h = h_bytes(q);
-  w.packed = packed_bytes(q, routed_packs(r));
   w.cols = combine ? combine_cols_of(c, d->N, r.T, r.topk, r.E_glob, r.E_loc) : d->N;
   if (combine) w.combine = al256((size_t)r.T * r.topk * w.cols * sizeof(float));
   return w;
@@ -1709,9 +1708,9 @@ extern "C" {
 size_t w4a16_linear_workspace_bytes(const w4a16_weight_desc* desc, int32_t T, const w4a16_adapters* adapters) {
   if (check_int4_desc(desc) != W4A16_OK || T <= 0) return 0;
   if (adapters && check_adapters(adapters, desc, T) != W4A16_OK) return 0;
-  w4a16::AdapterParams q;
-  if (adapters) q = linear_adapters(*adapters, desc, T);
-  return linear_workspace(desc, T, adapters ? &q : nullptr).total();
+  LinearAdapters ad{};
+  if (adapters) ad = linear_adapters(*adapters, desc, T);
+  return linear_workspace(desc, T, adapters ? &ad : nullptr).total();
 }
 
 w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, const void* packed_s, const uint16_t* x,
@@ -1735,9 +1734,11 @@ w4a16_status w4a16_linear(const w4a16_weight_desc* desc, const void* packed_w, c
     if (st != W4A16_OK) return st;
   }
   if (T == 0) return W4A16_OK;
-  if (adapters) sp.ad = linear_adapters(*adapters, desc, T);
+  LinearAdapters ad{};
+  if (adapters) ad = linear_adapters(*adapters, desc, T);
+  const LinearWorkspace wl = linear_workspace(desc, T, adapters ? &ad : nullptr);
+  sp.ad = ad.q;
   sp.ad.rows = T;
-  const LinearWorkspace wl = linear_workspace(desc, T, adapters ? &sp.ad : nullptr);
   st = check_workspace(wl.total(), workspace, workspace_bytes);
   if (st != W4A16_OK) return st;
   char* ws = static_cast<char*>(workspace);
@@ -1807,8 +1808,7 @@ w4a16_status w4a16_moe_adapter_gemm(const w4a16_weight_desc* desc, const void* p
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   q.h = reinterpret_cast<float*>(ws);
-  if (wl.packed) q.packed = reinterpret_cast<uint16_t*>(ws + wl.h);
-  float* comb = reinterpret_cast<float*>(ws + wl.h + wl.packed);
+  float* comb = reinterpret_cast<float*>(ws + wl.h);
   hipError_t e = shrink_routed(q, a, a_layout, desc, r, s);
   if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, a, combine ? (void*)comb : (void*)out, c.nr, c.waves);
@@ -1865,7 +1865,6 @@ w4a16_status w4a16_moe_adapter_gate_up_silu(const w4a16_weight_desc* desc, const
   if (st != W4A16_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   q.h = static_cast<float*>(workspace);
-  if (wl.packed) q.packed = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + wl.h);
   hipError_t e = shrink_routed(q, x, W4A16_A_TOKEN, desc, r, s);
   if (e != hipSuccess) return hip_fail(e, "adapter shrink launch");
   w4a16::GemmParams p = base_params(desc, packed_w, packed_s, x, out, c.nr, c.waves);
