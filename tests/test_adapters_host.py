@@ -155,6 +155,20 @@ def test_linear_refuses(L):
     assert L.w4a16_linear_workspace_bytes(ctypes.byref(d), 3, None) >= 3 * 64 * 4         # slices of K
 
 
+@pytest.mark.parametrize("T,K,N,rank,planes,packed", [
+    (520, 1120, 2560, 128, 4, True), (511, 1120, 2560, 128, 4, False), (520, 992, 2560, 128, 4, True),
+    (520, 896, 2560, 128, 3, False),                                      # 7 chunks of 128, two a plane at least
+    (64, 3232, 96, 64, 8, None), (65, 3232, 96, 64, 4, None), (64, 3200 // 4, 96, 64, 3, None)])
+def test_linear_workspace_holds_the_planes_and_a_packed_copy(L, T, K, N, rank, planes, packed):
+    d = W.weight_desc(1, N, K)
+    al = lambda n: (n + 255) // 256 * 256
+    need = L.w4a16_linear_workspace_bytes(ctypes.byref(d), T, ctypes.byref(_adapters(N=N, K=K, rank=rank, slices=2)))
+    bare = L.w4a16_linear_workspace_bytes(ctypes.byref(d), T, None)       # slices of K
+    want = al(planes * T * 2 * rank * 4) + al(4 * T) + (al(T * 2 * -(-rank // 16) * 64) if packed else 0)
+    assert need - bare == want
+    assert (bare == 0) == (packed is not None)
+
+
 def _routing(T=3, topk=2, E=4, block_m=16, **kw):
     f = dict(sorted_ids=P, expert_ids=P, num_tokens_padded=P, capacity=W.align_capacity(T, topk, E, block_m),
              block_m=block_m, T=T, topk=topk, topk_ids=P, first_expert=0, E_loc=E, E_glob=E)

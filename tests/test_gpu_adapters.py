@@ -252,6 +252,41 @@ def test_linear_many_rows(T, K, N, rank, slices, runs):
     assert torch.equal(bits_t(P.run()), bits_t(P.run()))
 
 
+# whole tiles over a packed h: at least 512 rows and four planes (K of 1024 with A's rows in four waves, 4096 in one)
+PACKED = [(520, 1120, 2560, 128, 2), (700, 1024, 2080, 72, 2), (1100, 1056, 4096, 256, 1), (2100, 1024, 1024, 72, 2),
+          (600, 4096, 2560, 8, 2), (17000, 1024, 64, 40, 2)]
+
+
+@pytest.mark.parametrize("T,K,N,rank,slices", PACKED)
+@pytest.mark.parametrize("runs", [7, 0])
+def test_linear_packed_inner_values(T, K, N, rank, slices, runs):
+    ids = None
+    if runs:
+        ids = torch.arange(T, device=dev()).mul(runs).div(T, rounding_mode="floor").to(torch.int32) - 1
+    P = Shared(T, K, N, 6, rank, slices, gate_up=slices == 2, ids=ids)
+    P.check()
+    if slices == 2:
+        P.check(silu=True, what="silu")
+
+
+def test_linear_packed_rows_do_not_see_other_requests():
+    P = Shared(700, 1024, 2080, 6, 72, 2)
+    y = P.run()
+    P.a[2].fill_(float("nan"))
+    P.b[4].fill_(float("inf"))
+    z = P.run()
+    rest = (P.ids != 2) & (P.ids != 4)
+    assert torch.equal(bits_t(y)[rest], bits_t(z)[rest])
+    assert z[P.ids == 2].isnan().all()
+
+
+@pytest.mark.parametrize("T", [1, 17, 64, 65])
+@pytest.mark.parametrize("K,rank,slices", [(3232, 64, 2), (6400, 32, 2), (3328, 256, 1)])
+def test_linear_long_rows_of_a(T, K, rank, slices):
+    """Few rows and wide adapters: eight planes of inner values."""
+    Shared(T, K, 96, 5, rank, slices).check()
+
+
 @pytest.mark.parametrize("T", [5, 40, 400])
 def test_linear_one_slice_for_gate_and_up(T):
     P = Shared(T, 384, 160, 4, 16, 1, gate_up=True)
